@@ -22,13 +22,15 @@ ERRORS = {
     -1: "ATTN_ERR_NULL", -2: "ATTN_ERR_SHAPE", -3: "ATTN_ERR_HEAD_DIM", -4: "ATTN_ERR_SCALE",
     -5: "ATTN_ERR_ALIGN", -6: "ATTN_ERR_ARCH", -7: "ATTN_ERR_LAUNCH", -8: "ATTN_ERR_TIMEOUT",
     -9: "ATTN_ERR_OPTION", -10: "ATTN_ERR_WORKSPACE", -11: "ATTN_ERR_STATIC_LIMIT", -12: "ATTN_ERR_LAYOUT",
+    -13: "ATTN_ERR_CACHE",
 }
 
 # Every symbol the header declares (checked by the CPU test-suite).
 EXPORTS = ["attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_host_workspace_size", "attn_get_status",
            "attn_strerror", "attn_last_cuda_error", "attn_version", "attn_fwd_host_static", "attn_fwd_layout",
            "attn_fwd_varlen", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_layout", "attn_bwd_ex",
-           "attn_fwd_fp8", "attn_fwd_fp8_ex"]
+           "attn_fwd_fp8", "attn_fwd_fp8_ex", "attn_fwd_cache", "attn_fwd_cache_workspace_size", "attn_cache_append",
+           "attn_cache_weights", "attn_cache_select", "attn_cache_compact"]
 
 CAUSAL_ALIGN = {"top-left": 0, "bottom-right": 1}
 
@@ -107,6 +109,18 @@ def lib():
     L.attn_fwd_fp8.restype = i
     L.attn_fwd_fp8_ex.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, f, f, f, i, ctypes.POINTER(Options), vp]
     L.attn_fwd_fp8_ex.restype = i
+    L.attn_fwd_cache.argtypes = [vp, vp, vp, f, vp, vp, vp, sz, ctypes.POINTER(Options), vp]
+    L.attn_fwd_cache.restype = i
+    L.attn_fwd_cache_workspace_size.argtypes = [i, i, i, i]
+    L.attn_fwd_cache_workspace_size.restype = sz
+    L.attn_cache_append.argtypes = [vp, vp, vp, i, vp, vp]
+    L.attn_cache_append.restype = i
+    L.attn_cache_weights.argtypes = [vp, vp, vp, f, vp, vp]
+    L.attn_cache_weights.restype = i
+    L.attn_cache_select.argtypes = [vp, vp, i, i, vp, vp]
+    L.attn_cache_select.restype = i
+    L.attn_cache_compact.argtypes = [vp, vp, i, vp]
+    L.attn_cache_compact.restype = i
     L.attn_get_status.argtypes = [vp]
     L.attn_get_status.restype = i
     L.attn_strerror.argtypes = [i]

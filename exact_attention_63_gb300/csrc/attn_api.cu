@@ -248,6 +248,40 @@ namespace attn {
 
 int record_cuda_error(cudaError_t e, const char* what) { return fail_cuda(e, what); }
 
+int usable_device(int* dev, unsigned int** status, int* sms) {
+  const int rc = current_device(dev);
+  if (rc != ATTN_OK) return rc;
+  *status = g_dev[*dev].status;
+  *sms = g_dev[*dev].sms;
+  return ATTN_OK;
+}
+
+int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
+                   const int box[4]) {
+  auto enc = get_encode_fn();
+  if (enc == nullptr) {
+    std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled unavailable");
+    return ATTN_ERR_LAUNCH;
+  }
+  cuuint64_t gd[4], gs[3];
+  cuuint32_t bx[4];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    gd[i] = static_cast<cuuint64_t>(dims[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    if (i < 3) gs[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+  }
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gd, gs, bx, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (CUresult %d)",
+                  static_cast<int>(r));
+    return ATTN_ERR_LAUNCH;
+  }
+  return ATTN_OK;
+}
+
 namespace {
 
 // attn_fwd_host's pipeline: up to kHostChunks slices of the problem, each
@@ -444,6 +478,8 @@ const char* attn_strerror(int status) {
     case ATTN_ERR_LAYOUT:
       return "invalid attn_layout (H not a multiple of num_kv_heads, a stride not a positive multiple of 8, "
              "or an unknown causal_align)";
+    case ATTN_ERR_CACHE:
+      return "invalid attn_cache or attn_new_tokens (struct_size, page_size, strides, head grouping or a size limit)";
     default: return "unknown status";
   }
 }

@@ -43,6 +43,15 @@ int fwd_host(const void* q_h, const void* k_h, const void* v_h, void* o_h, float
 // Record a failed CUDA call for attn_last_cuda_error(); returns ATTN_ERR_LAUNCH.
 int record_cuda_error(cudaError_t e, const char* what);
 
+// The current device's index, status word and multiprocessor count, or the
+// error of a device that is missing or not compute capability 10.3.
+int usable_device(int* dev, unsigned int** status, int* sms);
+
+// Tiled 4-D map over bf16 with element strides of dimensions 1..3 (dimension 0
+// contiguous), 128-byte swizzle.
+int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
+                   const int box[4]);
+
 // FP8 (E4M3) inputs, d = 128 (attn_fwd_fp8.cu).
 cudaError_t launch_fwd_fp8(const LaunchArgs& a, bool causal);
 

@@ -1,0 +1,634 @@
+// Attention of new tokens over a paged cache and over each other.
+//
+//   s_tj = scale·q_t·k_j over the cached keys j and the new tokens j that are t
+//   or an ancestor of t;  O_t = Σ_j exp(s_tj − LSE_t)·v_j,  LSE_t = ln Σ_j exp(s_tj).
+//
+// The group's query heads share one key head, so the rows of one (sequence, key
+// head) are its (token, head of the group) pairs: up to 128 of them make the M
+// dimension of both products, and every key and value row is read once for all.
+// With few rows the operator is bound by reading k and v from device memory
+// (4d bytes a key for 4d·rows flops), with ≥ ~128 rows by the tensor core.
+//
+// Work units are blocks of 128 keys of one (sequence, key head, row tile), in
+// that order.  CTA c of G takes the c-th G-th of all units, whatever sequences
+// they belong to, so one long sequence and a ragged batch both fill the SMs
+// evenly.  A CTA's range covers whole tiles except at its two ends; there it
+// leaves an unnormalised part (O, running maximum, sum) in the workspace, and a
+// second kernel joins the parts of a tile in order.  The ranges follow from the
+// lengths on the device: the host reads nothing back.
+//
+// Two CTAs share an SM (256 TMEM columns and under half of its shared memory
+// each).  Warps: 0 loads (TMA boxes of a page's rows, one lane a box), 1 issues
+// the MMAs, 2-5 compute the softmax, one thread a row (TMEM lane).  Two CTAs
+// rather than one deep pipeline: one CTA's copies and MMAs run under the
+// other's exponentials, with K and V of one block each in flight.
+//
+// d = 128: TMEM S [0,128), with P (bf16) over its first half; O [128,256).
+//          S(g+1) is issued once P(g)·V has completed.
+// d = 64:  S [0,128), P [128,192), O [192,256): S(g+1) is issued once the softmax
+//          has read S(g).
+//
+// The last cached block and the new tokens' keys share one block where both fit.
+// Rows of V that hold no key of the sequence (behind its end, between the two)
+// are zeroed in shared memory: their P is 0, but a stale NaN would spread.
+#include "attn_fwd_kernel.cuh"
+#include "cache_device.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreadsCA = 192;
+constexpr float kTau = 8.0f;  // log2: a row's reference maximum moves when exceeded by more (p ≤ 2^8)
+
+// The key blocks of one sequence: `nfull` full ones, then the cached tail and the
+// new tokens (at row `off` of block `db`).
+struct KeyPlan {
+  int q0, n, len;
+  int nfull, tail, off, db;
+};
+__device__ __forceinline__ KeyPlan key_plan(const CacheAttnParams& p, int s) {
+  KeyPlan k;
+  const SeqRows r = seq_rows(p.c, s);
+  k.q0 = r.q0;
+  k.n = min(r.n, p.c.max_new);
+  k.len = seq_len(p.c, s);
+  k.nfull = k.len >> 7;
+  k.tail = k.len & 127;
+  const int off = (k.tail + p.piece - 1) & ~(p.piece - 1);
+  const bool joined = off + ((k.n + 15) & ~15) <= 128;
+  k.off = joined ? off : 0;
+  k.db = k.nfull + (joined ? 0 : 1);
+  return k;
+}
+__device__ __forceinline__ int row_tiles(const CacheAttnParams& p, int n) { return (n + p.nt - 1) / p.nt; }
+
+__device__ __forceinline__ int units_of(const CacheAttnParams& p, int s) {
+  const KeyPlan k = key_plan(p, s);
+  return k.n == 0 ? 0 : p.c.hkv * row_tiles(p, k.n) * (k.db + 1);
+}
+
+__device__ __forceinline__ int range_start(int units, int cta, int grid) {
+  return static_cast<int>(static_cast<long long>(units) * cta / grid);
+}
+
+// A CTA's share of one (sequence, key head, row tile): blocks [b0, b1).
+struct Segment {
+  int s, h, m, b0, b1;
+  KeyPlan k;
+};
+__device__ __forceinline__ Segment segment_at(const CacheAttnParams& p, const int* tab, int u, int u_end) {
+  Segment g;
+  g.s = find_seq(tab, p.c.n_seq, u);
+  g.k = key_plan(p, g.s);
+  const int nb = g.k.db + 1, mt = row_tiles(p, g.k.n);
+  const int rem = u - tab[g.s], hm = rem / nb;
+  g.b0 = rem - hm * nb;
+  g.h = hm / mt;
+  g.m = hm - g.h * mt;
+  g.b1 = min(nb, g.b0 + (u_end - u));
+  return g;
+}
+__device__ __forceinline__ int cached_in(const KeyPlan& k, int b) {
+  return b < k.nfull ? 128 : (b == k.nfull ? k.tail : 0);
+}
+
+template <int D>
+struct CL {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTile = 128u * D * 2;  // 128 rows of Q, K or V: [half][128 rows][128 B]
+  static constexpr int kStages = D == 128 ? 1 : 2;
+  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
+  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full, s_free, p_full, pv_done, done
+  static constexpr int kNumBars = 2 + 4 * kStages + 5;
+  static constexpr uint32_t kMisc = kBar + 8 * kNumBars;       // TMEM base, abort flag
+  static constexpr uint32_t kSums = kMisc + 8;                 // one int per warp
+  static constexpr uint32_t kTable = (kSums + 32 + 15) & ~15u;
+  static constexpr uint32_t kBytes = kTable + 1024;            // + alignment; the table comes on top
+  static constexpr uint32_t kColS = 0, kColP = D == 128 ? 0 : 128, kColO = D == 128 ? 128 : 192;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsCA, 2)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
+                      const __grid_constant__ CUtensorMap tm_vn, const CacheAttnParams p) {
+  using L = CL<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  const uint32_t bars = base + L::kBar;
+  const uint32_t q_full = bars, q_empty = bars + 8;
+  auto k_full = [&](int s) { return bars + 8u * (2 + s); };
+  auto k_empty = [&](int s) { return bars + 8u * (2 + L::kStages + s); };
+  auto v_full = [&](int s) { return bars + 8u * (2 + 2 * L::kStages + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (2 + 3 * L::kStages + s); };
+  constexpr uint32_t kB = 2 + 4 * L::kStages;
+  const uint32_t s_full = bars + 8u * kB, s_free = bars + 8u * (kB + 1), p_full = bars + 8u * (kB + 2);
+  const uint32_t pv_done = bars + 8u * (kB + 3), done = bars + 8u * (kB + 4);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
+  int* const tab = reinterpret_cast<int*>(smem + L::kTable);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) { return units_of(p, s); });
+  const int units = tab[p.c.n_seq];
+  if (cta == 0)
+    for (int i = threadIdx.x; i <= p.c.n_seq; i += kThreadsCA) p.ws_table[i] = tab[i];
+  const int grid = min(static_cast<int>(gridDim.x), units);  // CTAs with work: each of them at least one unit
+  if (cta >= grid) return;
+  const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
+
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  if (threadIdx.x == 32) {
+    *abort_flag = 0u;
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+
+  if (warp == 0) {
+    // ============================================================= loader
+    // All lanes follow; lane 0 waits and announces the bytes, then lane i < 8
+    // copies the i-th piece of cached rows and lane 8 + i the i-th 16 new rows.
+    auto waited = [&](uint32_t bar, uint32_t parity) -> bool {
+      int ok = 1;
+      if (lane == 0) ok = wait_bar(bar, parity, wc);
+      return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
+    int g = 0, ns = 0, nq = 0, nk = 0, nv = 0;  // blocks, segments; copies issued of each kind
+    bool ok = true;
+    const int ps = p.piece;
+    for (int u = u0; u < u1 && ok; ++ns) {
+      const Segment sg = segment_at(p, tab, u, u1);
+      u += sg.b1 - sg.b0;
+      ok = waited(q_empty, (ns & 1) ^ 1u);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.nt * p.c.group) * 128u * L::kHalves);
+        for (int hf = 0; hf < L::kHalves; ++hf)
+          tma_load_4d(base + L::kQ + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + sg.m * p.nt, q_full);
+      }
+      ++nq;
+      const int nd = (sg.k.n + 15) >> 4;  // 16-row pieces of new keys
+      // Page and slot of this lane's piece; the next block's are fetched early.
+      int page = 0, slot = 0;
+      auto locate = [&](int b) {
+        const int j = (b << 7) + lane * ps;
+        const int blk = j / p.c.page_size;
+        slot = j - blk * p.c.page_size;
+        if (lane * ps < cached_in(sg.k, b)) page = page_for_read(p.c, sg.s, blk);
+      };
+      locate(sg.b0);
+      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
+        const int st = g % L::kStages, ph = (g / L::kStages) & 1;
+        const int cv = cached_in(sg.k, b), npc = (cv + ps - 1) / ps, ndb = b == sg.k.db ? nd : 0;
+        const uint32_t bytes = static_cast<uint32_t>(npc * ps + ndb * 16) * 128u * L::kHalves;
+        const int cur_page = page, cur_slot = slot;
+        auto copy = [&](const CUtensorMap* mc, const CUtensorMap* mn, uint32_t dst, uint32_t full) {
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+          __syncwarp();
+          if (lane < npc) {
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(dst + hf * 16384 + lane * ps * 128, mc, 64 * hf, sg.h, cur_slot, cur_page, full);
+          } else if (lane >= 8 && lane - 8 < ndb) {
+            const int i = lane - 8;
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(dst + hf * 16384 + (sg.k.off + 16 * i) * 128, mn, 64 * hf, sg.h, sg.k.q0 + 16 * i, 0, full);
+          }
+          __syncwarp();
+        };
+        ok = waited(k_empty(st), ph ^ 1u) && !(p.test_flags & 1u);
+        if (!ok) break;
+        copy(&tm_k, &tm_kn, base + L::kK + st * L::kTile, k_full(st));
+        ++nk;
+        if (b + 1 < sg.b1) locate(b + 1);
+        ok = waited(v_empty(st), ph ^ 1u);
+        if (!ok) break;
+        copy(&tm_v, &tm_vn, base + L::kV + st * L::kTile, v_full(st));
+        ++nv;
+      }
+    }
+    // No copy may be in flight when the CTA ends (only possible after an abort).
+    if (lane == 0 && !ok) {
+      const uint64_t t0 = globaltimer_ns();
+      auto drain = [&](uint32_t bar, uint32_t parity) {
+        while (!mbar_try_wait(bar, parity))
+          if (globaltimer_ns() - t0 > p.timeout_ns) break;
+      };
+      if (nq > 0) drain(q_full, (nq - 1) & 1);
+      for (int n = max(0, nk - L::kStages); n < nk; ++n) drain(k_full(n % L::kStages), (n / L::kStages) & 1u);
+      for (int n = max(0, nv - L::kStages); n < nv; ++n) drain(v_full(n % L::kStages), (n / L::kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ========================================================= MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, 128, false);
+      constexpr uint32_t idPV = idesc_bf16(128, D, true);
+      const uint64_t dQ = sdesc_kmajor_sw128(base + L::kQ);
+      const uint32_t tS = tmem + L::kColS, tP = tmem + L::kColP, tO = tmem + L::kColO;
+      int g = 0, ns = 0;
+      bool ok = true;
+      // O (+)= P(n)·V; `first`: the block opens its segment.
+      auto issue_pv = [&](int n, bool first) -> bool {
+        const int st = n % L::kStages;
+        if (!wait_bar(v_full(st), (n / L::kStages) & 1, wc) || !wait_bar(p_full, n & 1, wc)) return false;
+        tc_fence_after();
+        const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tO, tP + kk * 8, dv + ((kk * 2048) >> 4), idPV, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(pv_done);
+        mma_commit(v_empty(st));
+        return true;
+      };
+      bool prev_first = false;
+      for (int u = u0; u < u1 && ok; ++ns) {
+        const Segment sg = segment_at(p, tab, u, u1);
+        u += sg.b1 - sg.b0;
+        for (int b = sg.b0; b < sg.b1; ++b, ++g) {
+          const int st = g % L::kStages;
+          if constexpr (D == 128) {
+            // P(g−1) lies over S: its product has to be done first.
+            if (g > 0) ok = issue_pv(g - 1, prev_first) && wait_bar(pv_done, (g - 1) & 1, wc);
+          } else {
+            if (g > 0) ok = wait_bar(s_free, (g - 1) & 1, wc);
+          }
+          if (ok && b == sg.b0) ok = wait_bar(q_full, ns & 1, wc);
+          ok = ok && wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            mma_ss(tS, dQ + o, dk + o, idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full);
+          mma_commit(k_empty(st));
+          if (b == sg.b1 - 1) mma_commit(q_empty);
+          if constexpr (D == 64) {
+            if (g > 0) ok = issue_pv(g - 1, prev_first);
+            if (!ok) break;
+          }
+          prev_first = b == sg.b0;
+        }
+      }
+      if (ok) issue_pv(g - 1, prev_first);
+      mma_commit(done);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(done, 0))
+        if (globaltimer_ns() - t0 > p.timeout_ns) break;
+    }
+  } else {
+    // ============================================================ softmax
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + L::kColS + lane_off, tP = tmem + L::kColP + lane_off, tO = tmem + L::kColO + lane_off;
+    const float sc = p.scale_log2;
+    const uint64_t sc2 = pack2(sc, sc);
+    int g = 0;
+    bool ok = true;
+    for (int u = u0; u < u1 && ok;) {
+      const Segment sg = segment_at(p, tab, u, u1);
+      const bool first_of_cta = u == u0;
+      u += sg.b1 - sg.b0;
+      const int t0 = sg.m * p.nt, n_rows = min(sg.k.n - t0, p.nt) * p.c.group;
+      const bool active = (warp & 3) * 32 < n_rows;
+      float m_run = -INFINITY, l_run = 0.f;
+      uint32_t anc[4] = {0u, 0u, 0u, 0u};  // the new tokens this row sees
+      if (sg.b1 > sg.k.db && active) {
+        const int t = min(t0 + r / p.c.group, sg.k.n - 1);
+        if (p.parents == nullptr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int bits = min(max(t + 1 - 32 * i, 0), 32);
+            anc[i] = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
+          }
+        } else {
+          int par[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) par[i] = 32 * i + lane < sg.k.n ? p.parents[sg.k.q0 + 32 * i + lane] : -1;
+          int at = t;
+          while (__any_sync(0xffffffffu, at >= 0)) {  // parents come before their children: at most 127 steps
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (at >= 0 && (at >> 5) == i) anc[i] |= 1u << (at & 31);
+            const int a = max(at, 0);
+            int up = -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int x = __shfl_sync(0xffffffffu, par[i], a & 31);
+              if ((a >> 5) == i) up = x;
+            }
+            at = (at >= 0 && up >= 0 && up < at) ? up : -1;
+          }
+        }
+      }
+      auto block = [&](int b, auto mask_tag) -> bool {
+        constexpr bool MASK = decltype(mask_tag)::value;
+        const bool got = wait_bar_cold(s_full, g & 1, wc);
+        if (__any_sync(0xffffffffu, !got)) return false;
+        tc_fence_after();
+        uint32_t vis[4];
+        if constexpr (MASK) {
+          const int cv = cached_in(sg.k, b), dn = b == sg.k.db ? sg.k.n : 0;
+          const int sh = sg.k.off >> 5, bit = sg.k.off & 31;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int n = min(max(cv - 32 * c, 0), 32);
+            vis[c] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            if (dn > 0) {
+              uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (i == c - sh) hi = anc[i];
+                if (i == c - sh - 1) lo = anc[i];
+              }
+              vis[c] |= __funnelshift_l(lo, hi, bit);
+            }
+          }
+          // Zero the rows of V that hold no key (every warp its 32 rows).
+          const int st = g % L::kStages;
+          const bool in = wait_bar_cold(v_full(st), (g / L::kStages) & 1, wc);
+          if (__any_sync(0xffffffffu, !in)) return false;
+          if (!(r < cv || (r >= sg.k.off && r < sg.k.off + dn))) {
+            uint8_t* const row = smem + L::kV + st * L::kTile + r * 128;
+#pragma unroll
+            for (int i = 0; i < 8 * L::kHalves; ++i)
+              *reinterpret_cast<uint4*>(row + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (active) {
+          uint32_t a[32], c2[32];
+          float mx = -INFINITY;
+          // ---- block maximum
+          if constexpr (MASK) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(tS + 32 * c, a);
+              tmem_wait_ld();
+              reg_fence32(a);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((vis[c] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(a[i]));
+            }
+          } else {
+            float m0, m1;
+            tmem_ld32_max(tS, a, m0);
+            tmem_ld32_max(tS + 32, c2, m1);
+            tmem_wait_ld();
+            asm volatile("" : "+f"(m0), "+f"(m1));
+            reg_fence32(a);
+            reg_fence32(c2);
+            mx = fmaxf(m0, m1);
+            tmem_ld32_max(tS + 64, a, m0);
+            tmem_ld32_max(tS + 96, c2, m1);
+            tmem_wait_ld();
+            asm volatile("" : "+f"(m0), "+f"(m1));
+            reg_fence32(a);
+            reg_fence32(c2);
+            mx = fmax3(mx, m0, m1);
+          }
+          mx *= sc;
+          const bool need = r < n_rows && (mx > m_run + kTau || (m_run == -INFINITY && mx > -INFINITY));
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_new = need ? mx : m_run;
+            if (b > sg.b0) {
+              const float alpha = need ? ex2_mufu(m_run - m_new) : 1.f;
+              if (!rescale_o<D>(pv_done, (g - 1) & 1, wc, tO, alpha)) return false;
+              l_run *= alpha;
+            }
+            m_run = m_new;
+          }
+          // ---- exponentials, P in bf16
+          if constexpr (D == 64) {
+            if (g > 0) {  // P·V(g−1) has read P
+              const bool landed = wait_bar_cold(pv_done, (g - 1) & 1, wc);
+              if (__any_sync(0xffffffffu, !landed)) return false;
+              tc_fence_after();
+            }
+          }
+          const float negm = m_run == -INFINITY ? 0.f : -m_run;
+          const uint64_t nm2 = pack2(negm, negm);
+          uint64_t acc[2] = {0, 0};
+          auto chunk = [&](int c, uint32_t(&x)[32]) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2), x0, x1);
+              x0 = ex2_mufu(x0);
+              x1 = ex2_mufu(x1);
+              if constexpr (MASK) {
+                x0 = (vis[c] >> (2 * i)) & 1u ? x0 : 0.f;
+                x1 = (vis[c] >> (2 * i + 1)) & 1u ? x1 : 0.f;
+              }
+              acc[i & 1] = fadd2(acc[i & 1], pack2(x0, x1));
+              pk[i] = pack_bf16x2(x0, x1);
+            }
+            tmem_st16(tP + 16 * c, pk);
+          };
+          tmem_ld32(tS, a);
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            tmem_wait_ld();
+            reg_fence32(a);
+            tmem_ld32(tS + 32 * (c + 1), c2);
+            chunk(c, a);
+            tmem_wait_ld();
+            reg_fence32(c2);
+            if (c == 0) tmem_ld32(tS + 64, a);
+            chunk(c + 1, c2);
+          }
+          float a0, a1;
+          unpack2(fadd2(acc[0], acc[1]), a0, a1);
+          l_run += a0 + a1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        if constexpr (D == 64) warp_arrive(s_free, lane);
+        warp_arrive(p_full, lane);
+        return true;
+      };
+      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g)
+        ok = b < sg.k.nfull ? block(b, std::false_type{}) : block(b, std::true_type{});
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      const bool landed = wait_bar_cold(pv_done, (g - 1) & 1, wc);
+      if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
+      tc_fence_after();
+      if (active) {
+        const bool whole = sg.b0 == 0 && sg.b1 == sg.k.db + 1;
+        const int grp = p.c.group, t = t0 + r / grp, hq = sg.h * grp + r % grp, H = p.c.hkv * grp;
+        const long long token = sg.k.q0 + t;
+        const int slot = 2 * cta + (first_of_cta ? 0 : 1);
+        const long long part = static_cast<long long>(slot) * p.rows + r;
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(tO + 32 * c, x);
+          tmem_wait_ld();
+          reg_fence32(x);
+          if (r < n_rows) {
+            if (whole) {
+              uint4* const dst = reinterpret_cast<uint4*>(p.o + (token * H + hq) * D + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t* o8 = &x[8 * i];
+                uint4 w;
+                w.x = pack_bf16x2(__uint_as_float(o8[0]) * inv, __uint_as_float(o8[1]) * inv);
+                w.y = pack_bf16x2(__uint_as_float(o8[2]) * inv, __uint_as_float(o8[3]) * inv);
+                w.z = pack_bf16x2(__uint_as_float(o8[4]) * inv, __uint_as_float(o8[5]) * inv);
+                w.w = pack_bf16x2(__uint_as_float(o8[6]) * inv, __uint_as_float(o8[7]) * inv);
+                dst[i] = w;
+              }
+            } else {
+              uint4* const dst = reinterpret_cast<uint4*>(p.ws_o + part * D + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+        }
+        if (r < n_rows) {
+          if (whole)
+            p.lse[static_cast<long long>(hq) * p.c.total + token] =
+                l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+          else
+            p.ws_ml[part] = make_float2(m_run, l_run);
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// Joins the parts of the tiles that were split: one warp a row.  With the parts'
+// maxima m_i and sums l_i:  m = max m_i,  O = Σ 2^(m_i − m) O_i / Σ 2^(m_i − m) l_i.
+template <int D>
+__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long item = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int r = static_cast<int>(item % p.rows);
+  const long long tile = item / p.rows;
+  const int m = static_cast<int>(tile % mt_max);
+  const int sh = static_cast<int>(tile / mt_max), h = sh % p.c.hkv, s = sh / p.c.hkv;
+  if (s >= p.c.n_seq) return;
+  const KeyPlan k = key_plan(p, s);
+  const int t0 = m * p.nt, n_rows = min(k.n - t0, p.nt) * p.c.group;
+  if (r >= n_rows) return;
+  const int units = p.ws_table[p.c.n_seq], nb = k.db + 1;
+  grid = min(grid, units);
+  const int ua = p.ws_table[s] + (h * row_tiles(p, k.n) + m) * nb;
+  auto cta_of = [&](int u) { return static_cast<int>(((u + 1ll) * grid - 1) / units); };
+  const int c0 = cta_of(ua), c1 = cta_of(ua + nb - 1);
+  if (c0 == c1) return;  // one CTA did it all and has written the row
+  auto part_of = [&](int c) {
+    const int slot = 2 * c + (range_start(units, c, grid) >= ua ? 0 : 1);
+    return static_cast<long long>(slot) * p.rows + r;
+  };
+  float mx = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.ws_ml[part_of(c)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.f, acc[kPer] = {};
+  for (int cb = c0; cb <= c1; cb += 32) {
+    const int c = cb + lane;
+    float w = 0.f;
+    if (c <= c1) {
+      const float2 ml = p.ws_ml[part_of(c)];
+      w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+      sum += w * ml.y;
+    }
+    const int n = min(32, c1 - cb + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.ws_o + part_of(cb + i) * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] += wi * x.x;
+        acc[1] += wi * x.y;
+        acc[2] += wi * x.z;
+        acc[3] += wi * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] += wi * x.x;
+        acc[1] += wi * x.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int grp = p.c.group, hq = h * grp + r % grp;
+  const long long token = k.q0 + t0 + r / grp;
+  uint16_t* const dst = p.o + (token * p.c.hkv * grp + hq) * D + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0)
+    p.lse[static_cast<long long>(hq) * p.c.total + token] =
+        sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int D>
+cudaError_t launch(const CacheAttnLaunch& a) {
+  const CacheAttnParams& p = a.p;
+  const unsigned int smem = CL<D>::kBytes + 4u * (p.c.n_seq + 1);
+  static volatile bool configured[64] = {};
+  if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
+  if (!configured[a.device]) {
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               CL<D>::kBytes + 4 * (kCacheMaxSeq + 1));
+    if (e != cudaSuccess) return e;
+    configured[a.device] = true;
+  }
+  cache_attn_kernel<D><<<a.grid, kThreadsCA, smem, a.stream>>>(a.q, a.k, a.v, a.kn, a.vn, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int mt_max = (p.c.max_new + p.nt - 1) / p.nt;
+  const long long rows = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max * p.rows;
+  cache_join_kernel<D><<<static_cast<unsigned int>((rows + 7) / 8), 256, 0, a.stream>>>(p, a.grid, mt_max);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn(const CacheAttnLaunch& a) { return a.p.c.d == 64 ? launch<64>(a) : launch<128>(a); }
+
+}  // namespace attn

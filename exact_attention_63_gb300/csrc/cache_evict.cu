@@ -1,0 +1,385 @@
+// The cache's bookkeeping operators: appending rows, choosing the tokens that
+// stay, moving them together.  All three are bound by memory (append, compact)
+// or by the passes over a head's weights in shared memory (select).
+#include "attn_gb300.h"
+#include "cache_device.cuh"
+
+namespace attn {
+namespace {
+
+// ------------------------------------------------------------------- append
+// One warp copies one token's k or v: H_kv·d·2 bytes, 16 a lane, four loads in
+// flight.  The k warps also set the weights and positions.
+__global__ void __launch_bounds__(256) cache_append_kernel(const CacheAppendParams p) {
+  const CacheParams& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const long long wi = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int i = static_cast<int>(wi >> 1), which = static_cast<int>(wi & 1);
+  if (i >= p.n_rows) return;
+  // The last sequence s with cu[s] <= i, 32 candidates a step.
+  int lo = 0, n = c.n_seq;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool le = lane * step < n && c.cu[at] <= i;
+    const unsigned int votes = __ballot_sync(0xffffffffu, le);
+    const int k = votes == 0u ? 0 : 31 - __clz(votes);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  const int a = min(max(c.cu[lo], 0), p.n_rows), z = min(max(c.cu[lo + 1], a), p.n_rows);
+  if (i < a || i >= z) return;
+  const int len = seq_len(c, lo), slot = len - z + i;
+  if (slot < 0) return;
+  const int src = p.rows != nullptr ? p.rows[i] : i;
+  if (src < 0 || src >= c.total) return;
+  const int blk = slot / c.page_size, js = slot - blk * c.page_size;
+  const int page = c.table[static_cast<long long>(lo) * c.max_blocks + blk];
+  if (page < 0 || page >= c.n_pages) return;
+
+  const long long* const st = which ? c.v_st : c.k_st;
+  const long long* const ns = which ? p.vn_st : p.kn_st;
+  uint16_t* const dst = (which ? c.v : c.k) + page * st[0] + js * st[1];
+  const uint16_t* const from = (which ? p.vn : p.kn) + src * ns[0];
+  const int sh = c.d == 128 ? 4 : 3, chunks = c.hkv << sh, mask = (1 << sh) - 1;
+  for (int q = lane; q < chunks; q += 128) {
+    uint4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int qq = q + 32 * e;
+      if (qq < chunks) x[e] = *reinterpret_cast<const uint4*>(from + (qq >> sh) * ns[1] + (qq & mask) * 8);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int qq = q + 32 * e;
+      if (qq < chunks) *reinterpret_cast<uint4*>(dst + (qq >> sh) * st[2] + (qq & mask) * 8) = x[e];
+    }
+  }
+  if (which == 0) {
+    const int pos = (p.seq_pos != nullptr ? p.seq_pos[lo] : len) - z + i;
+    for (int h = lane; h < c.hkv; h += 32) {
+      const long long at = (static_cast<long long>(page) * c.hkv + h) * c.page_size + js;
+      if (c.weights != nullptr) c.weights[at] = 0.f;
+      if (c.positions != nullptr) c.positions[at] = pos;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ compact
+// One warp looks at 32 entries of kept and moves the rows of those beyond the
+// budget: d/8 lanes of 16 bytes a row, k and v side by side, four rows in flight.
+__global__ void __launch_bounds__(256) cache_compact_kernel(const CacheParams c, const int* kept, int budget) {
+  const int lane = threadIdx.x & 31;
+  const long long wi = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int tiles = (budget + 31) / 32;
+  const long long sh = wi / tiles;
+  const int s = static_cast<int>(sh / c.hkv), h = static_cast<int>(sh % c.hkv);
+  if (s >= c.n_seq) return;
+  const int i = static_cast<int>(wi % tiles) * 32 + lane;
+  int from = -1;
+  if (i < budget) from = kept[sh * budget + i];
+  bool move = from >= budget && from < c.cap && i < c.cap;
+  long long k0 = 0, k1 = 0, v0 = 0, v1 = 0;
+  if (move) {
+    const int* const tab = c.table + static_cast<long long>(s) * c.max_blocks;
+    const int b0 = from / c.page_size, j0 = from - b0 * c.page_size, b1 = i / c.page_size, j1 = i - b1 * c.page_size;
+    const int p0 = tab[b0], p1 = tab[b1];
+    move = p0 >= 0 && p0 < c.n_pages && p1 >= 0 && p1 < c.n_pages;
+    if (move) {
+      k0 = p0 * c.k_st[0] + j0 * c.k_st[1];
+      k1 = p1 * c.k_st[0] + j1 * c.k_st[1];
+      v0 = p0 * c.v_st[0] + j0 * c.v_st[1];
+      v1 = p1 * c.v_st[0] + j1 * c.v_st[1];
+      const long long a0 = (static_cast<long long>(p0) * c.hkv + h) * c.page_size + j0;
+      const long long a1 = (static_cast<long long>(p1) * c.hkv + h) * c.page_size + j1;
+      if (c.weights != nullptr) c.weights[a1] = c.weights[a0];
+      if (c.positions != nullptr) c.positions[a1] = c.positions[a0];
+    }
+  }
+  unsigned int todo = __ballot_sync(0xffffffffu, move);
+  const int per = c.d / 8, grp = lane / per, at = (lane % per) * 8, both = 32 / per / 2;  // rows a step: 1 or 2
+  const bool is_v = grp & 1;
+  const uint16_t* const src = (is_v ? c.v + h * c.v_st[2] : c.k + h * c.k_st[2]) + at;
+  uint16_t* const dst = (is_v ? c.v + h * c.v_st[2] : c.k + h * c.k_st[2]) + at;
+  while (todo) {
+    uint4 x[4];
+    long long to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // This lane's row: the (grp/2)-th of the next `both` entries.
+      int mine = -1;
+      for (int b = 0; b < both; ++b) {
+        const int j = todo ? __ffs(todo) - 1 : -1;
+        todo &= todo - 1;  // 0 stays 0
+        if (b == (grp >> 1)) mine = j;
+      }
+      const int l = max(mine, 0);
+      const long long fk = __shfl_sync(0xffffffffu, k0, l), fv = __shfl_sync(0xffffffffu, v0, l);
+      const long long tk = __shfl_sync(0xffffffffu, k1, l), tv = __shfl_sync(0xffffffffu, v1, l);
+      to[e] = mine < 0 ? -1 : (is_v ? tv : tk);
+      if (mine >= 0) x[e] = *reinterpret_cast<const uint4*>(src + (is_v ? fv : fk));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (to[e] >= 0) *reinterpret_cast<uint4*>(dst + to[e]) = x[e];
+  }
+}
+
+// ------------------------------------------------------------------- select
+// One CTA ranks one (sequence, head).  The budget-th largest key is found digit
+// by digit (11, 11 and 10 bits) from histograms in shared memory; one pass then
+// marks the slots that stay in a bit map (of those equal to the threshold, the
+// first ones), and the k-th freed slot below n finds the k-th kept slot behind
+// it by a binary search over the map's counts.  Keys stay in shared memory where
+// a sequence fits, else each pass reads the weights again.
+constexpr int kThreadsSel = 1024;
+constexpr int kBins = 2048;
+constexpr uint32_t kSmemMax = 232448;
+
+// Larger key = stays earlier: 0xffffffff for the newest, then the weight in the
+// order of its bits, 0 for NaN.
+__device__ __forceinline__ uint32_t rank_key(float w, bool newest) {
+  if (newest) return 0xffffffffu;
+  if (w != w) return 0u;
+  const uint32_t b = __float_as_uint(w + 0.f);  // −0 as +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+struct SelectSmem {
+  uint32_t words, groups, keys;  // bit-map words, groups of four words, cached keys
+};
+__host__ __device__ inline SelectSmem select_smem(int cap) {
+  SelectSmem m;
+  m.groups = static_cast<uint32_t>((cap + 127) / 128);
+  m.words = 4 * m.groups;
+  const uint32_t fixed = kBins * 4 + 64 * 4 + m.words * 4 + (m.groups + 1) * 4;
+  const uint32_t room = (kSmemMax - fixed) / 4;
+  m.keys = room < static_cast<uint32_t>(cap) ? room : static_cast<uint32_t>(cap);
+  return m;
+}
+inline uint32_t select_bytes(int cap) {
+  const SelectSmem m = select_smem(cap);
+  return kBins * 4 + 64 * 4 + m.words * 4 + (m.groups + 1) * 4 + m.keys * 4;
+}
+
+// Exclusive sum over the CTA's threads, and the total; `w`: 33 ints.
+__device__ __forceinline__ int block_exclusive(int v, int* w, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) w[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int x = w[lane];
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    w[lane] = s - x;
+    if (lane == 31) w[32] = s;
+  }
+  __syncthreads();
+  const int r = w[warp] + incl - v;
+  *total = w[32];
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreadsSel)
+    cache_select_kernel(const CacheParams c, const int* seq_pos, int budget, int recent, int* kept) {
+  extern __shared__ uint32_t sel_smem[];
+  const SelectSmem lay = select_smem(c.cap);
+  int* const hist = reinterpret_cast<int*>(sel_smem);
+  int* const scratch = hist + kBins;  // 33 for scans, then [40] digit, [41] count above
+  uint32_t* const bits = reinterpret_cast<uint32_t*>(scratch + 64);
+  int* const before = reinterpret_cast<int*>(bits + lay.words);
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(before + lay.groups + 1);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int s = blockIdx.x / c.hkv, h = blockIdx.x - s * c.hkv;
+  const int len = seq_len(c, s), n = min(len, budget);
+  int* const out = kept + static_cast<long long>(blockIdx.x) * budget;
+  for (int i = n + tid; i < budget; i += kThreadsSel) out[i] = -1;
+  if (len <= budget) {
+    for (int i = tid; i < n; i += kThreadsSel) out[i] = i;
+    return;
+  }
+  const int* const tab = c.table + static_cast<long long>(s) * c.max_blocks;
+  const long long newest = (c.positions != nullptr ? static_cast<long long>(seq_pos[s]) : len) - recent;
+  auto load_key = [&](int j) -> uint32_t {
+    const int b = j / c.page_size;
+    const int page = min(max(tab[b], 0), c.n_pages - 1);
+    const long long at = (static_cast<long long>(page) * c.hkv + h) * c.page_size + (j - b * c.page_size);
+    const int pos = c.positions != nullptr ? c.positions[at] : j;
+    return rank_key(c.weights[at], pos >= newest);
+  };
+  const bool cached = len <= static_cast<int>(lay.keys);
+  auto key_of = [&](int j) { return cached ? keys[j] : load_key(j); };
+
+  // ---- threshold: the budget-th largest key, and how many equal to it stay
+  uint32_t prefix = 0, fixed_bits = 0;
+  int want = budget;  // rank of the threshold among the keys that match the prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
+    for (int i = tid; i < kBins; i += kThreadsSel) hist[i] = 0;
+    __syncthreads();
+    if (pass == 0 && cached) {
+#pragma unroll 4
+      for (int j = tid; j < len; j += kThreadsSel) {
+        const uint32_t k = load_key(j);
+        keys[j] = k;
+        atomicAdd(&hist[k >> 21], 1);
+      }
+    } else {
+#pragma unroll 4
+      for (int j = tid; j < len; j += kThreadsSel) {
+        const uint32_t k = key_of(j);
+        if ((k & fixed_bits) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
+      }
+    }
+    __syncthreads();
+    // Bins from the top: thread t has bins kBins − 1 − 2t and the next lower one.
+    const int hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
+    int total;
+    const int above = block_exclusive(hi + lo, scratch, &total);
+    if (above < want && want <= above + hi + lo) {
+      const bool in_hi = want <= above + hi;
+      scratch[40] = kBins - 1 - 2 * tid - (in_hi ? 0 : 1);
+      scratch[41] = above + (in_hi ? 0 : hi);
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(scratch[40]) << shift;
+    fixed_bits |= ((1u << width) - 1u) << shift;
+    want -= scratch[41];
+    __syncthreads();
+  }
+  const uint32_t thr = prefix;
+
+  // ---- the map of the slots that stay; each warp has a run of groups of 128 slots
+  const int groups = (len + 127) / 128, per = (groups + 31) / 32;
+  const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
+  int eq = 0;
+  for (int g = g0; g < g1; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = g * 128 + 32 * e + lane;
+      const uint32_t k = j < len ? key_of(j) : 0u;
+      const uint32_t be = __ballot_sync(0xffffffffu, j < len && k == thr), bg = __ballot_sync(0xffffffffu, j < len && k > thr);
+      if (lane == 0) bits[4 * g + e] = bg;
+      eq += __popc(be);
+    }
+  int total;
+  int eq_before = block_exclusive(lane == 0 ? eq : 0, scratch, &total);
+  eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
+  int src = 0;  // kept slots at or beyond n in this warp's run
+  for (int g = g0; g < g1; ++g) {
+    if (eq > 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = g * 128 + 32 * e + lane;
+        const uint32_t be = __ballot_sync(0xffffffffu, j < len && key_of(j) == thr);
+        const int rank = eq_before + __popc(be & ((1u << lane) - 1u));
+        const uint32_t stay = __ballot_sync(0xffffffffu, ((be >> lane) & 1u) && rank < want);
+        if (lane == 0) bits[4 * g + e] |= stay;
+        eq_before += __popc(be);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      before[g] = src;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int lowest = g * 128 + 32 * e;
+        uint32_t m = bits[4 * g + e];
+        if (lowest + 32 <= n) m = 0u;
+        else if (lowest < n) m &= ~0u << (n - lowest);
+        src += __popc(m);
+      }
+    }
+  }
+  int src_before = block_exclusive(lane == 0 ? src : 0, scratch, &total);
+  src_before = __shfl_sync(0xffffffffu, src_before, 0);
+  for (int g = g0 + lane; g < g1; g += 32) before[g] += src_before;
+
+  // ---- slots below n: kept where they are, or filled by the k-th kept slot behind
+  const int wn = (n + 31) / 32, wper = (wn + 31) / 32;
+  const int w0 = min(wn, warp * wper), w1 = min(wn, w0 + wper);
+  __syncthreads();
+  int holes = 0;
+  for (int w = w0 + lane; w < w1; w += 32) {
+    const uint32_t live = w * 32 + 32 <= n ? 0xffffffffu : (1u << (n - w * 32)) - 1u;
+    holes += __popc(~bits[w] & live);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) holes += __shfl_xor_sync(0xffffffffu, holes, o);
+  int hole_before = block_exclusive(lane == 0 ? holes : 0, scratch, &total);
+  hole_before = __shfl_sync(0xffffffffu, hole_before, 0);
+  const int g_first = n / 128;
+  for (int w = w0; w < w1; ++w) {
+    const int j = w * 32 + lane;
+    const uint32_t live = w * 32 + 32 <= n ? 0xffffffffu : (1u << (n - w * 32)) - 1u;
+    const uint32_t free_ = ~bits[w] & live;
+    if (j < n) {
+      int from = j;
+      if ((free_ >> lane) & 1u) {
+        int k = hole_before + __popc(free_ & ((1u << lane) - 1u));
+        int lo = g_first, hi = groups - 1;  // the last group with before[g] <= k
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (before[mid] <= k) lo = mid;
+          else hi = mid - 1;
+        }
+        k -= before[lo];
+        from = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int lowest = lo * 128 + 32 * e;
+          uint32_t m = bits[4 * lo + e];
+          if (lowest + 32 <= n) m = 0u;
+          else if (lowest < n) m &= ~0u << (n - lowest);
+          const int cnt = __popc(m);
+          if (k >= 0 && k < cnt) from = lowest + static_cast<int>(__fns(m, 0, k + 1));
+          k -= cnt;
+        }
+      }
+      out[j] = from;
+    }
+    hole_before += __popc(free_);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheAppendParams& p, int, cudaStream_t stream) {
+  const long long warps = 2ll * p.n_rows;
+  cache_append_kernel<<<static_cast<unsigned int>((warps + 7) / 8), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const CacheParams& c, const int* kept, int budget, int, cudaStream_t stream) {
+  const long long warps = static_cast<long long>(c.n_seq) * c.hkv * ((budget + 31) / 32);
+  cache_compact_kernel<<<static_cast<unsigned int>((warps + 7) / 8), 256, 0, stream>>>(c, kept, budget);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_select(const CacheParams& c, const int* seq_pos, int budget, int recent, int* kept, int device,
+                                int, cudaStream_t stream) {
+  static volatile bool configured[64] = {};
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!configured[device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    configured[device] = true;
+  }
+  cache_select_kernel<<<c.n_seq * c.hkv, kThreadsSel, select_bytes(c.cap), stream>>>(c, seq_pos, budget, recent, kept);
+  return cudaGetLastError();
+}
+
+}  // namespace attn

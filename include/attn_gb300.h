@@ -66,7 +66,8 @@ enum {
   ATTN_ERR_OPTION = -9,    /* an attn_options field is out of range */
   ATTN_ERR_WORKSPACE = -10, /* workspace missing, misaligned or smaller than required */
   ATTN_ERR_STATIC_LIMIT = -11, /* problem needs more than ATTN_STATIC_WORKSPACE_BYTES (attn_fwd_host_static) */
-  ATTN_ERR_LAYOUT = -12       /* an attn_layout field is invalid (head grouping, strides, causal alignment) */
+  ATTN_ERR_LAYOUT = -12,      /* an attn_layout field is invalid (head grouping, strides, causal alignment) */
+  ATTN_ERR_CACHE = -13        /* an attn_cache or attn_new_tokens field is invalid */
 };
 
 /*
@@ -393,6 +394,173 @@ int attn_fwd_fp8_ex(const void* q8, const void* k8, const void* v8, void* o, flo
                     int B, int H, int Sq, int Sk, int d, float scale,
                     float descale_q, float descale_k, float descale_v, int causal,
                     const attn_options* opts, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A key/value cache in pages, and the operators on it.
+ *
+ * attn_cache describes a cache that the caller owns.  Zero-initialise and set
+ * struct_size = sizeof(attn_cache).
+ *   k, v        : device, bf16 pages [n_pages, page_size, num_kv_heads, d].
+ *   k_strides, v_strides : element strides of page, slot and head (the d
+ *                 elements stay contiguous); all zero selects the dense layout,
+ *                 otherwise each a positive multiple of 8 below 2^38.  Pages
+ *                 stored [n_pages, num_kv_heads, page_size, d] are such a view.
+ *   weights     : device, fp32 [n_pages, num_kv_heads, page_size], the attention
+ *                 weight that each cached key has gathered; or NULL.
+ *   positions   : device, int32 [n_pages, num_kv_heads, page_size], the position
+ *                 in its sequence of the token in each slot (heads may hold
+ *                 different tokens after an eviction); or NULL.
+ *   block_table : device, int32 [n_seq, max_blocks]: slot j of sequence s is
+ *                 slot j % page_size of page block_table[s, j / page_size].
+ *   seq_lens    : device, int32 [n_seq]: sequence s holds slots [0, seq_lens[s]).
+ *   page_size   : a multiple of 16, at most 65536.
+ *   d           : 64 or 128.
+ *   n_seq       : 1 to 2048.  max_blocks * page_size is at most 2^30.
+ * Lengths and tables are read on the device: a length outside
+ * [0, max_blocks*page_size] is clamped, a key on a page outside [0, n_pages)
+ * is read from a page inside and not written.  A malformed table gives wrong
+ * results but no access outside the tensors.  Slots at or beyond seq_lens may
+ * hold anything, NaN included.
+ * Sequences may share pages as long as nothing writes to them: the pages that
+ * attn_cache_append, attn_cache_weights and attn_cache_compact write to must
+ * belong to one sequence each.
+ *
+ * attn_new_tokens describes packed rows of new tokens: sequence s owns rows
+ * [cu_seqlens[s], cu_seqlens[s+1]).  Zero-initialise and set struct_size.
+ *   q           : device, bf16 [total, H, d].
+ *   k, v        : device, bf16 [total, num_kv_heads, d].
+ *   q_strides, k_strides, v_strides : element strides of token and head; both
+ *                 zero = dense, otherwise positive multiples of 8 below 2^38
+ *                 (slices of a packed [total, H + 2 H_kv, d] projection).
+ *   cu_seqlens  : device, int32 [n_seq + 1], ascending from 0; clamped to
+ *                 [0, total].  A sequence may have no new token.
+ *   max_seqlen  : host, at least the most new tokens of a sequence; rows beyond
+ *                 it are neither read nor written.
+ *   H           : query heads, a multiple of num_kv_heads, at most 128 times it.
+ * Every call is asynchronous on `stream`, allocates nothing and can be captured
+ * into a graph; lengths, tables and offsets may change between replays.
+ * Errors are as for attn_fwd, with ATTN_ERR_CACHE for an invalid field of the
+ * two structs and ATTN_ERR_ALIGN for a tensor that is not 16-byte (k, v, q, o),
+ * 4-byte (all others) or, for attn_cache_weights' lse, 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef struct attn_cache {
+  size_t struct_size;
+  void* k;
+  void* v;
+  long long k_strides[3];
+  long long v_strides[3];
+  float* weights;
+  int* positions;
+  const int* block_table;
+  const int* seq_lens;
+  int n_pages, page_size, max_blocks, n_seq, num_kv_heads, d;
+} attn_cache;
+
+typedef struct attn_new_tokens {
+  size_t struct_size;
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_strides[2];
+  long long k_strides[2];
+  long long v_strides[2];
+  const int* cu_seqlens;
+  int total, max_seqlen, H;
+} attn_new_tokens;
+
+/*
+ * attn_fwd_cache — attention of new tokens over a cache and over each other:
+ * one token a sequence, a chain of them, or a tree of drafted ones.
+ *   Token t of a sequence (counted within the sequence) sees every cached slot
+ *   [0, seq_lens[s]), itself, and its ancestors among the new tokens; x->k and
+ *   x->v are the new tokens' own keys and values, not yet in the cache.
+ *   parents : device, int32 [total]: the parent of a token, counted within its
+ *             sequence; -1 where the parent is the last cached token.  A value
+ *             outside [0, t) counts as -1.  NULL: a chain, token t's parent is
+ *             t - 1.
+ *   o       : device, bf16 [total, H, d] (dense); lse: fp32 [H, total], natural
+ *             log.  Rows before cu_seqlens[0] or behind cu_seqlens[n_seq] stay
+ *             as they were.
+ *   workspace : device, 256-byte aligned, at least
+ *             attn_fwd_cache_workspace_size(H, num_kv_heads, max_seqlen, d)
+ *             bytes; its contents on entry do not matter.  Calls that overlap
+ *             on the GPU need workspaces of their own.
+ *   opts    : timeout_ms and ATTN_TEST_WITHHOLD_KV apply; the rest must be zero.
+ * max_seqlen is at most ATTN_CACHE_MAX_NEW.  The keys of a sequence are split
+ * over the GPU's SMs and joined by a second kernel; the split depends on the
+ * lengths alone, so results are reproducible bit for bit.  Arithmetic as
+ * attn_fwd: P in bf16, statistics and sums in fp32.
+ */
+#define ATTN_CACHE_MAX_NEW 128
+size_t attn_fwd_cache_workspace_size(int H, int num_kv_heads, int max_seqlen, int d);
+int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int* parents, float scale, void* o,
+                   float* lse, void* workspace, size_t workspace_bytes, const attn_options* opts,
+                   cudaStream_t stream);
+
+/*
+ * attn_cache_append — put new tokens' keys and values into the cache.
+ *   cache->seq_lens are the lengths AFTER the append: token i of the n new ones
+ *   of sequence s goes into slot seq_lens[s] - n + i (a negative slot is
+ *   skipped).  cache->weights (where given) becomes 0 there, and
+ *   cache->positions (where given) seq_pos[s] - n + i.
+ *   x       : k, v, cu_seqlens, total (q, H, max_seqlen are not used).
+ *   rows    : device, int32 [n_rows] or NULL.  With rows, cu_seqlens counts
+ *             entries of rows, and token i of sequence s is row
+ *             rows[cu_seqlens[s] + i] of x->k and x->v (the accepted path of a
+ *             drafted tree); an entry outside [0, total) is skipped.
+ *   seq_pos : device, int32 [n_seq], tokens of the sequence that have ever been
+ *             appended, the new ones included; NULL: seq_lens.
+ */
+int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const int* rows, int n_rows,
+                      const int* seq_pos, cudaStream_t stream);
+
+/*
+ * attn_cache_weights — add the attention weight that each cached key received.
+ *   weights_out[key] = cache->weights[key] + sum over the sequence's query rows
+ *   i and the query heads of the key's head of exp(scale*q_i.k - lse_i), over
+ *   the rows that see the key: row i of n sees slots j <= seq_lens[s] - n + i
+ *   (the n tokens are the newest in the cache).
+ *   x           : q, cu_seqlens, total, max_seqlen, H.  lse: device, fp32
+ *                 [H, total], natural log, as attn_fwd_varlen and attn_fwd_cache
+ *                 return it.  A row with lse = -inf or +inf adds nothing.
+ *   cache->weights : may be NULL (counts as zeros).  cache->v is not used.
+ *   weights_out : device, fp32 [n_pages, num_kv_heads, page_size]; may be
+ *                 cache->weights.  Every slot in use is written, no other.
+ * max_seqlen is not limited (whole prompts).  Sums are fp32, in a fixed order.
+ */
+int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,
+                       float* weights_out, cudaStream_t stream);
+
+/*
+ * attn_cache_select — which tokens stay when each sequence and head may keep
+ * `budget` of them.
+ *   The newest slots (position >= seq_pos[s] - recent) rank first, all alike;
+ *   the others by gathered weight, heavier first, a NaN below every number.  Of
+ *   slots that rank alike the lower goes first.  The first
+ *   n = min(seq_lens[s], budget) stay.
+ *   kept    : device, int32 [n_seq, num_kv_heads, budget] (written): the slot
+ *             that the token at slot i afterwards has now; -1 for i >= n.  A
+ *             token below slot n that stays keeps its slot; the slots below n
+ *             that become free, ascending, take the others, ascending.
+ *   cache   : weights; positions where recent counts by position (NULL: by slot,
+ *             as if positions were slots and seq_pos were seq_lens); k, v are not
+ *             used.
+ *   seq_pos : device, int32 [n_seq]; needed with positions.
+ * budget >= 1, 0 <= recent <= budget, and max_blocks*page_size at most
+ * ATTN_CACHE_MAX_SELECT.
+ */
+#define ATTN_CACHE_MAX_SELECT (1 << 20)
+int attn_cache_select(const attn_cache* cache, const int* seq_pos, int budget, int recent, int* kept,
+                      cudaStream_t stream);
+
+/*
+ * attn_cache_compact — move the kept tokens: for every kept[s, h, i] >= budget
+ * the rows of k and v, and the entries of weights and positions where given, of
+ * slot kept[s, h, i] go to slot i of the same head.  Entries below budget move
+ * nothing, so sources and destinations never meet.  Afterwards the caller sets
+ * seq_lens to min(seq_lens, budget).  An entry beyond the table is skipped.
+ */
+int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cudaStream_t stream);
 
 /*
  * attn_get_status — synchronises `stream`, then returns and clears the current
