@@ -35,8 +35,11 @@ the call runs on, and the one its outputs and workspace are allocated on.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
+import struct
 
 import torch
 
@@ -66,130 +69,147 @@ class NewTokens(ctypes.Structure):
                 ("max_seqlen", ctypes.c_int), ("H", ctypes.c_int)]
 
 
-def _need(name, t, dtype, dims, device, contiguous=True):
+# The structs as bytes in native layout: filled in one call, where a ctypes
+# structure takes one per field (a decoding step is short enough to notice).
+_CACHE = struct.Struct("@N2P6q4P6i")
+_TOKENS = struct.Struct("@N3P6qP3i")
+assert _CACHE.size == ctypes.sizeof(Cache) and _TOKENS.size <= ctypes.sizeof(NewTokens)
+_TOKENS_PAD = b"\0" * (ctypes.sizeof(NewTokens) - _TOKENS.size)
+
+
+def _refuse(name, t, dtype, dims, dev, contiguous):
+    """The reason why _need refused t."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dims or not t.is_cuda:
         raise ValueError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.stride(-1) != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous" if contiguous else f"{name} must have a contiguous last dimension")
 
 
-def _pages(name, t, device):
-    _need(name, t, _BF16, 4, device, contiguous=False)
+def _need(name, t, dtype, dims, dev):
+    """t is a contiguous tensor of the type on CUDA device dev; its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.get_device() != dev or \
+            not t.is_contiguous():
+        _refuse(name, t, dtype, dims, dev, True)
+    return t.data_ptr()
+
+
+def _rows(name, t, dims, dev):
+    """t is a bf16 tensor on CUDA device dev whose last dimension is contiguous:
+    its address, and the element strides of the others for the library (0: dense).
+    The stride of a dimension of one entry means nothing; the dense one stands for it."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != dims or t.get_device() != dev:
+        _refuse(name, t, _BF16, dims, dev, False)
+    if t.is_contiguous():
+        return t.data_ptr(), (0, 0, 0) if dims == 4 else (0, 0)
+    if t.stride(-1) != 1:
+        _refuse(name, t, _BF16, dims, dev, False)
+    return t.data_ptr(), _strides(t)
 
 
 def _strides(t):
-    """Element strides of all but the last dimension, for the library.  A stride
-    of a dimension of one entry means nothing: the dense one stands for it."""
     if t.is_contiguous():
         return (0,) * (t.dim() - 1)
-    out, dense = [], t.shape[-1]
+    shape, stride, out, dense = t.shape, t.stride(), [], t.shape[-1]
     for i in range(t.dim() - 2, -1, -1):
-        if t.shape[i] > 1 and t.stride(i) < t.shape[-1]:
-            raise ValueError(f"overlapping rows: strides {tuple(t.stride())} of shape {tuple(t.shape)}")
-        out.append(t.stride(i) if t.shape[i] > 1 else max(dense, 8))
-        dense = max(dense, out[-1] * t.shape[i])
+        if shape[i] > 1 and stride[i] < shape[-1]:
+            raise ValueError(f"overlapping rows: strides {tuple(stride)} of shape {tuple(shape)}")
+        out.append(stride[i] if shape[i] > 1 else max(dense, 8))
+        dense = max(dense, out[-1] * shape[i])
     return tuple(reversed(out))
 
 
-def _cache_struct(k, v, block_table, seq_lens, weights, positions, hkv, d, n_pages, page_size):
-    c = Cache()
-    c.struct_size = ctypes.sizeof(Cache)
-    if k is not None:
-        c.k = k.data_ptr()
-        c.k_strides[:] = _strides(k)
-    if v is not None:
-        c.v = v.data_ptr()
-        c.v_strides[:] = _strides(v)
-    if weights is not None:
-        c.weights = weights.data_ptr()
-    if positions is not None:
-        c.positions = positions.data_ptr()
-    c.block_table = block_table.data_ptr()
-    if seq_lens is not None:
-        c.seq_lens = seq_lens.data_ptr()
-    c.n_pages, c.page_size, c.num_kv_heads, c.d = n_pages, page_size, hkv, d
-    c.n_seq, c.max_blocks = block_table.shape
-    return c
-
-
-def _check_cache(k, v, block_table, seq_lens, weights=None, positions=None):
-    """Types, shapes and devices of a cache's tensors; (device, H_kv, d, n_pages, page_size)."""
-    lead = k if k is not None else weights
-    if not isinstance(lead, torch.Tensor) or not lead.is_cuda:
+def _device(t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("the cache must be CUDA tensors")
-    dev = lead.device
+    return t.get_device()
+
+
+def _seq(name, t, n, dev):
+    ptr = _need(name, t, _I32, 1, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return ptr
+
+
+def _per_slot(name, t, dtype, shape, dev):
+    ptr = _need(name, t, dtype, 3, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [n_pages, H_kv, page_size] = {tuple(shape)}")
+    return ptr
+
+
+def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
+    """attn_cache of checked tensors; (bytes, H_kv, d, n_seq).  What an operator does
+    not use is None."""
+    table = _need("block_table", block_table, _I32, 2, dev)
+    n_seq, max_blocks = block_table.shape
+    kp = vp = wp = pp = lp = 0
+    ks = vs = (0, 0, 0)
     if k is not None:
-        _pages("k_cache", k, dev)
+        kp, ks = _rows("k_cache", k, 4, dev)
         n_pages, page_size, hkv, d = k.shape
         if v is not None:
-            _pages("v_cache", v, dev)
+            vp, vs = _rows("v_cache", v, 4, dev)
             if v.shape != k.shape:
                 raise ValueError(f"v_cache {tuple(v.shape)} must be shaped like k_cache {tuple(k.shape)}")
     else:
-        _need("weights", weights, _F32, 3, dev)
+        if weights.dim() != 3:
+            _refuse("weights", weights, _F32, 3, dev, True)
         n_pages, hkv, page_size = weights.shape
         d = 0
-    _need("block_table", block_table, _I32, 2, dev)
+    if weights is not None:
+        wp = _per_slot("weights", weights, _F32, (n_pages, hkv, page_size), dev)
+    if positions is not None:
+        pp = _per_slot("positions", positions, _I32, (n_pages, hkv, page_size), dev)
     if seq_lens is not None:
-        _need("seq_lens", seq_lens, _I32, 1, dev)
-        if seq_lens.shape[0] != block_table.shape[0]:
-            raise ValueError("seq_lens and block_table must have as many sequences")
-    for name, t, dt in (("weights", weights, _F32), ("positions", positions, _I32)):
-        if t is not None:
-            _need(name, t, dt, 3, dev)
-            if tuple(t.shape) != (n_pages, hkv, page_size):
-                raise ValueError(f"{name} must be [n_pages, H_kv, page_size] = {(n_pages, hkv, page_size)}")
-    return dev, hkv, d, n_pages, page_size
+        lp = _seq("seq_lens", seq_lens, n_seq, dev)
+    return (_CACHE.pack(_CACHE.size, kp, vp, *ks, *vs, wp, pp, table, lp, n_pages, page_size, max_blocks, n_seq, hkv,
+                        d), hkv, d, n_seq)
 
 
-def _check_seq(name, t, n, dev):
-    _need(name, t, _I32, 1, dev)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries")
+def _pack_tokens(q, k, v, cu, total, max_seqlen, H):
+    """attn_new_tokens from (address, strides) pairs."""
+    return _TOKENS.pack(ctypes.sizeof(NewTokens), q[0], k[0], v[0], *q[1], *k[1], *v[1], cu, total, max_seqlen,
+                        H) + _TOKENS_PAD
+
+
+_NONE = (0, (0, 0))
 
 
 def _new_kv(k_new, v_new, hkv, d, dev):
-    _need("k_new", k_new, _BF16, 3, dev, contiguous=False)
-    _need("v_new", v_new, _BF16, 3, dev, contiguous=False)
-    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (hkv, d):
+    kn, vn = _rows("k_new", k_new, 3, dev), _rows("v_new", v_new, 3, dev)
+    if k_new.shape != v_new.shape or k_new.shape[1] != hkv or k_new.shape[2] != d:
         raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be [total, {hkv}, {d}]")
+    return kn, vn
 
 
-class _on:
-    """The tensors' device as the current one and `stream` as its current stream."""
-
-    def __init__(self, dev, stream):
-        self.cm = torch.cuda.stream(stream) if stream is not None else None
-        self.dev = dev if dev.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.dev is not None:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        if self.cm is not None:
-            self.cm.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *a):
-        if self.cm is not None:
-            self.cm.__exit__(*a)
-        if self.dev is not None:
-            self.guard.__exit__(*a)
+@contextlib.contextmanager
+def _switched(dev, stream):
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
 
 
-def _stream_fits(stream, dev):
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+def _on(dev, stream):
+    """Context in which the tensors' device is current and so is the stream (what is
+    allocated inside belongs to it); gives the stream's handle."""
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return _switched(dev, stream)
 
 
 def workspace_size(H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
     """Bytes of attn_fwd_cache's workspace (0: the sizes are not supported)."""
     return int(attn.lib().attn_fwd_cache_workspace_size(H, H_kv, max_seqlen_q, d))
+
+
+_workspace_bytes = functools.lru_cache(maxsize=None)(workspace_size)
 
 
 def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q: int,
@@ -205,52 +225,48 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     lse [H, total] fp32); rows that belong to no sequence are not written.
     ``workspace``: a uint8 tensor of workspace_size(...) bytes, else allocated.
     """
-    dev, hkv, d, n_pages, page_size = _check_cache(k_cache, v_cache, block_table, seq_lens)
+    dev = _device(k_cache)
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
-    _need("q", q, _BF16, 3, dev, contiguous=False)
-    _new_kv(k_new, v_new, hkv, d, dev)
-    total, H = q.shape[0], q.shape[1]
-    if k_new.shape[0] != total or q.shape[2] != d or H % hkv != 0:
+    c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, None, None)
+    qr = _rows("q", q, 3, dev)
+    kn, vn = _new_kv(k_new, v_new, hkv, d, dev)
+    total, H, dq = q.shape
+    if k_new.shape[0] != total or dq != d or H % hkv != 0:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k_new {tuple(k_new.shape)}, cache heads {hkv}, d {d}")
-    _check_seq("cu_seqlens_q", cu_seqlens_q, block_table.shape[0] + 1, dev)
-    if parents is not None:
-        _check_seq("parents", parents, total, dev)
+    cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
+    par = None if parents is None else _seq("parents", parents, total, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    _stream_fits(stream, dev)
+    if out is not None:
+        _need("out", out, _BF16, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+    if lse is not None:
+        _need("lse", lse, _F32, 2, dev)
+        if tuple(lse.shape) != (H, total):
+            raise ValueError("lse must be [H, total]")
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
     max_seqlen_q = int(max_seqlen_q)
-    L = attn.lib()
     with _on(dev, stream) as s:
+        device = k_cache.device
         if out is None:
-            out = torch.empty((total, H, d), dtype=_BF16, device=dev)
-        else:
-            _need("out", out, _BF16, 3, dev)
-            if tuple(out.shape) != (total, H, d):
-                raise ValueError("out must be shaped like q")
+            out = torch.empty((total, H, d), dtype=_BF16, device=device)
         if lse is None:
-            lse = torch.empty((H, total), dtype=_F32, device=dev)
-        else:
-            _need("lse", lse, _F32, 2, dev)
-            if tuple(lse.shape) != (H, total):
-                raise ValueError("lse must be [H, total]")
+            lse = torch.empty((H, total), dtype=_F32, device=device)
         if total == 0:
             return out, lse
         if workspace is None:
-            workspace = torch.empty(L.attn_fwd_cache_workspace_size(H, hkv, max_seqlen_q, d), dtype=torch.uint8,
-                                    device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+            workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
         if options is not None:
             options.struct_size = ctypes.sizeof(attn.Options)
-        c = _cache_struct(k_cache, v_cache, block_table, seq_lens, None, None, hkv, d, n_pages, page_size)
-        x = NewTokens(ctypes.sizeof(NewTokens), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _strides(q),
-                      _strides(k_new), _strides(v_new), cu_seqlens_q.data_ptr(), total, max_seqlen_q, H)
-        rc = L.attn_fwd_cache(ctypes.byref(c), ctypes.byref(x), None if parents is None else parents.data_ptr(),
-                              float(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(),
-                              ctypes.byref(options) if options is not None else None, s)
-    attn._check(rc)
+        rc = attn.lib().attn_fwd_cache(c, _pack_tokens(qr, kn, vn, cu, total, max_seqlen_q, H), par, scale,
+                                       out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(),
+                                       ctypes.byref(options) if options is not None else None, s)
+    if rc:
+        attn._check(rc)
     return out, lse
 
 
@@ -264,27 +280,22 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     of k_new and v_new, cu_new then counts entries of it: the accepted path of a
     drafted tree.
     """
-    dev, hkv, d, n_pages, page_size = _check_cache(k_cache, v_cache, block_table, seq_lens, weights, positions)
+    dev = _device(k_cache)
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
-    _new_kv(k_new, v_new, hkv, d, dev)
-    n_seq = block_table.shape[0]
-    _check_seq("cu_new", cu_new, n_seq + 1, dev)
+    c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, weights, positions)
+    kn, vn = _new_kv(k_new, v_new, hkv, d, dev)
+    cu = _seq("cu_new", cu_new, n_seq + 1, dev)
+    total, n_rows, rp = k_new.shape[0], 0, None
     if rows is not None:
-        _need("rows", rows, _I32, 1, dev)
-    if seq_pos is not None:
-        _check_seq("seq_pos", seq_pos, n_seq, dev)
-    _stream_fits(stream, dev)
-    if k_new.shape[0] == 0 or (rows is not None and rows.shape[0] == 0):
+        rp, n_rows = _need("rows", rows, _I32, 1, dev), rows.shape[0]
+    sp = None if seq_pos is None else _seq("seq_pos", seq_pos, n_seq, dev)
+    if total == 0 or (rows is not None and n_rows == 0):
         return
     with _on(dev, stream) as s:
-        c = _cache_struct(k_cache, v_cache, block_table, seq_lens, weights, positions, hkv, d, n_pages, page_size)
-        x = NewTokens(ctypes.sizeof(NewTokens), None, k_new.data_ptr(), v_new.data_ptr(), (0, 0), _strides(k_new),
-                      _strides(v_new), cu_new.data_ptr(), k_new.shape[0], 0, 0)
-        rc = attn.lib().attn_cache_append(ctypes.byref(c), ctypes.byref(x), None if rows is None else rows.data_ptr(),
-                                          0 if rows is None else rows.shape[0],
-                                          None if seq_pos is None else seq_pos.data_ptr(), s)
-    attn._check(rc)
+        rc = attn.lib().attn_cache_append(c, _pack_tokens(_NONE, kn, vn, cu, total, 0, 0), rp, n_rows, sp, s)
+    if rc:
+        attn._check(rc)
 
 
 def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q: int, weights=None,
@@ -298,36 +309,33 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     (out is then needed).  Any number of queries: a decoded token, the last window
     of a prompt or the whole of it.
     """
-    dev, hkv, d, n_pages, page_size = _check_cache(k_cache, None, block_table, seq_lens, weights)
+    dev = _device(k_cache)
     if seq_lens is None:
         raise ValueError("seq_lens is needed")
+    c, hkv, d, n_seq = _pack_cache(dev, k_cache, None, block_table, seq_lens, weights, None)
     if out is None:
         out = weights
     if out is None:
         raise ValueError("one of weights and out is needed")
-    _need("out", out, _F32, 3, dev)
-    if tuple(out.shape) != (n_pages, hkv, page_size):
-        raise ValueError(f"out must be [n_pages, H_kv, page_size] = {(n_pages, hkv, page_size)}")
-    _need("q", q, _BF16, 3, dev, contiguous=False)
-    total, H = q.shape[0], q.shape[1]
-    if q.shape[2] != d or H % hkv != 0:
+    n_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    op = _per_slot("out", out, _F32, (n_pages, hkv, page_size), dev)
+    qr = _rows("q", q, 3, dev)
+    total, H, dq = q.shape
+    if dq != d or H % hkv != 0:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, cache heads {hkv}, d {d}")
-    _need("lse", lse, _F32, 2, dev)
+    if total == 0:
+        raise ValueError("q has no rows")
+    lp = _need("lse", lse, _F32, 2, dev)
     if tuple(lse.shape) != (H, total):
         raise ValueError(f"lse must be [H, total] = {(H, total)}")
-    _check_seq("cu_seqlens_q", cu_seqlens_q, block_table.shape[0] + 1, dev)
+    cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    _stream_fits(stream, dev)
     with _on(dev, stream) as s:
-        if total == 0:
-            raise ValueError("q has no rows")
-        c = _cache_struct(k_cache, None, block_table, seq_lens, weights, None, hkv, d, n_pages, page_size)
-        x = NewTokens(ctypes.sizeof(NewTokens), q.data_ptr(), None, None, _strides(q), (0, 0), (0, 0),
-                      cu_seqlens_q.data_ptr(), total, int(max_seqlen_q), H)
-        rc = attn.lib().attn_cache_weights(ctypes.byref(c), ctypes.byref(x), lse.data_ptr(), float(scale),
-                                           out.data_ptr(), s)
-    attn._check(rc)
+        rc = attn.lib().attn_cache_weights(c, _pack_tokens(qr, _NONE, _NONE, cu, total, int(max_seqlen_q), H), lp,
+                                           scale, op, s)
+    if rc:
+        attn._check(rc)
     return out
 
 
@@ -341,28 +349,25 @@ def cache_select(weights, block_table, seq_lens, budget: int, recent: int = 0, p
     behind the last.  Tokens that stay below slot ``budget`` keep their slot; the
     others fill the slots that become free, both ascending.
     """
-    dev, hkv, _, n_pages, page_size = _check_cache(None, None, block_table, seq_lens, weights, positions)
+    dev = _device(weights)
     if seq_lens is None:
         raise ValueError("seq_lens is needed")
-    n_seq = block_table.shape[0]
-    if seq_pos is not None:
-        _check_seq("seq_pos", seq_pos, n_seq, dev)
-    elif positions is not None:
+    c, hkv, _, n_seq = _pack_cache(dev, None, None, block_table, seq_lens, weights, positions)
+    if positions is not None and seq_pos is None:
         raise ValueError("positions need seq_pos")
+    sp = None if seq_pos is None else _seq("seq_pos", seq_pos, n_seq, dev)
     budget, recent = int(budget), int(recent)
-    _stream_fits(stream, dev)
+    if kept is not None:
+        _need("kept", kept, _I32, 3, dev)
+        if tuple(kept.shape) != (n_seq, hkv, budget):
+            raise ValueError(f"kept must be [n_seq, H_kv, budget] = {(n_seq, hkv, budget)}")
     with _on(dev, stream) as s:
         if kept is None:
-            kept = torch.empty((n_seq, hkv, max(budget, 0)), dtype=_I32, device=dev)
-        else:
-            _need("kept", kept, _I32, 3, dev)
-            if tuple(kept.shape) != (n_seq, hkv, budget):
-                raise ValueError(f"kept must be [n_seq, H_kv, budget] = {(n_seq, hkv, budget)}")
-        c = _cache_struct(None, None, block_table, seq_lens, weights, positions, hkv, 0, n_pages, page_size)
-        # (an empty tensor has no address: let the library answer for the budget)
-        rc = attn.lib().attn_cache_select(ctypes.byref(c), None if seq_pos is None else seq_pos.data_ptr(), budget,
-                                          recent, kept.data_ptr() or 16, s)
-    attn._check(rc)
+            kept = torch.empty((n_seq, hkv, max(budget, 0)), dtype=_I32, device=weights.device)
+        # (an empty tensor has no address: the library answers for the budget)
+        rc = attn.lib().attn_cache_select(c, sp, budget, recent, kept.data_ptr() or 16, s)
+    if rc:
+        attn._check(rc)
     return kept
 
 
@@ -370,17 +375,17 @@ def cache_compact(kept, k_cache, v_cache, block_table, weights=None, positions=N
     """Move the tokens that cache_select kept, in place: for every kept[s, h, i] >=
     budget (= kept.shape[2]) the key, value, weight and position of that slot go to
     slot i.  Set seq_lens to min(seq_lens, budget) afterwards."""
-    dev, hkv, d, n_pages, page_size = _check_cache(k_cache, v_cache, block_table, None, weights, positions)
+    dev = _device(k_cache)
     if v_cache is None:
         raise ValueError("v_cache is needed")
-    _need("kept", kept, _I32, 3, dev)
-    if kept.shape[0] != block_table.shape[0] or kept.shape[1] != hkv or kept.shape[2] < 1:
+    c, hkv, _, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, None, weights, positions)
+    kp = _need("kept", kept, _I32, 3, dev)
+    if kept.shape[0] != n_seq or kept.shape[1] != hkv or kept.shape[2] < 1:
         raise ValueError(f"kept must be [n_seq, H_kv, budget], not {tuple(kept.shape)}")
-    _stream_fits(stream, dev)
     with _on(dev, stream) as s:
-        c = _cache_struct(k_cache, v_cache, block_table, None, weights, positions, hkv, d, n_pages, page_size)
-        rc = attn.lib().attn_cache_compact(ctypes.byref(c), kept.data_ptr(), kept.shape[2], s)
-    attn._check(rc)
+        rc = attn.lib().attn_cache_compact(c, kp, kept.shape[2], s)
+    if rc:
+        attn._check(rc)
 
 
 def cache_evict(k_cache, v_cache, weights, block_table, seq_lens, budget: int, recent: int = 0, positions=None,

@@ -133,14 +133,7 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
-  prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) { return units_of(p, s); });
-  const int units = tab[p.c.n_seq];
-  if (cta == 0)
-    for (int i = threadIdx.x; i <= p.c.n_seq; i += kThreadsCA) p.ws_table[i] = tab[i];
-  const int grid = min(static_cast<int>(gridDim.x), units);  // CTAs with work: each of them at least one unit
-  if (cta >= grid) return;
-  const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
-
+  // TMEM and barriers are set up while the lengths are on their way.
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 256);
     tmem_relinquish();
@@ -164,8 +157,25 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  __syncthreads();
+  if (threadIdx.x == 64) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_kn);
+    tma_prefetch_desc(&tm_vn);
+  }
+  prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) { return units_of(p, s); });
   tc_fence_after();
+  const int units = tab[p.c.n_seq];
+  if (cta == 0)
+    for (int i = threadIdx.x; i <= p.c.n_seq; i += kThreadsCA) p.ws_table[i] = tab[i];
+  const int grid = min(static_cast<int>(gridDim.x), units);  // CTAs with work: each of them at least one unit
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (cta >= grid) {
+    if (warp == 0) tmem_dealloc(*tmem_slot, 256);
+    return;
+  }
+  const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
 
@@ -534,76 +544,123 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
   }
 }
 
-// Joins the parts of the tiles that were split: one warp a row.  With the parts'
-// maxima m_i and sums l_i:  m = max m_i,  O = Σ 2^(m_i − m) O_i / Σ 2^(m_i − m) l_i.
-template <int D>
+// Joins the parts of the tiles that were split.  With the parts' maxima m_i and
+// sums l_i:  m = max m_i,  O = Σ 2^(m_i − m) O_i / Σ 2^(m_i − m) l_i.
+// A block of eight warps takes kJoinRows rows of a tile, a warp a row (SPLIT = 1:
+// many rows, few parts each), or one row with the parts dealt out to the warps
+// (SPLIT = 8: few rows; one long sequence leaves a part on every CTA).
+constexpr int kJoinRows = 32;
+
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max) {
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int r = static_cast<int>(item % p.rows);
-  const long long tile = item / p.rows;
-  const int m = static_cast<int>(tile % mt_max);
-  const int sh = static_cast<int>(tile / mt_max), h = sh % p.c.hkv, s = sh / p.c.hkv;
-  if (s >= p.c.n_seq) return;
+  __shared__ float s_acc[SPLIT][D];
+  __shared__ float2 s_ml[SPLIT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned int chunks = SPLIT == 1 ? (p.rows + kJoinRows - 1) / kJoinRows : p.rows;
+  unsigned int x = blockIdx.x;
+  const int row0 = static_cast<int>(x % chunks) * (SPLIT == 1 ? kJoinRows : 1);
+  x /= chunks;
+  const int m = static_cast<int>(x % mt_max);
+  x /= mt_max;
+  const int h = static_cast<int>(x % p.c.hkv), s = static_cast<int>(x / p.c.hkv);
   const KeyPlan k = key_plan(p, s);
-  const int t0 = m * p.nt, n_rows = min(k.n - t0, p.nt) * p.c.group;
-  if (r >= n_rows) return;
+  const int grp = p.c.group, t0 = m * p.nt, n_rows = min(k.n - t0, p.nt) * grp;
+  // The attention kernel's results, complete and visible.  Every block waits, so
+  // that this kernel never ends before that one.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row0 >= n_rows) return;
   const int units = p.ws_table[p.c.n_seq], nb = k.db + 1;
   grid = min(grid, units);
   const int ua = p.ws_table[s] + (h * row_tiles(p, k.n) + m) * nb;
   auto cta_of = [&](int u) { return static_cast<int>(((u + 1ll) * grid - 1) / units); };
   const int c0 = cta_of(ua), c1 = cta_of(ua + nb - 1);
-  if (c0 == c1) return;  // one CTA did it all and has written the row
-  auto part_of = [&](int c) {
-    const int slot = 2 * c + (range_start(units, c, grid) >= ua ? 0 : 1);
-    return static_cast<long long>(slot) * p.rows + r;
-  };
-  float mx = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.ws_ml[part_of(c)].x);
+  if (c0 == c1) return;  // one CTA did it all and has written the rows
+  // Every CTA's part but the first's is the first of its range.
+  const int slot0 = 2 * c0 + (range_start(units, c0, grid) >= ua ? 0 : 1);
+  auto part_of = [&](int c, int r) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * p.rows + r; };
+
+  auto gather = [&](int r, int first, int step, float& mx, float& sum, float(&acc)[kPer]) {
+    mx = -INFINITY;
+    for (int c = first + lane * step; c <= c1; c += 32 * step) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float sum = 0.f, acc[kPer] = {};
-  for (int cb = c0; cb <= c1; cb += 32) {
-    const int c = cb + lane;
-    float w = 0.f;
-    if (c <= c1) {
-      const float2 ml = p.ws_ml[part_of(c)];
-      w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
-      sum += w * ml.y;
-    }
-    const int n = min(32, c1 - cb + 1);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.ws_o + part_of(cb + i) * D + lane * kPer;
-      if constexpr (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
-        acc[2] += wi * x.z;
-        acc[3] += wi * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    for (int cb = first; cb <= c1; cb += 32 * step) {
+      const int c = cb + lane * step;
+      float w = 0.f;
+      if (c <= c1) {
+        const float2 ml = p.ws_ml[part_of(c, r)];
+        w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+        sum += w * ml.y;
+      }
+      const int n = min(32, (c1 - cb) / step + 1);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* src = p.ws_o + part_of(cb + i * step, r) * D + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          acc[0] += wi * y.x;
+          acc[1] += wi * y.y;
+          acc[2] += wi * y.z;
+          acc[3] += wi * y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          acc[0] += wi * y.x;
+          acc[1] += wi * y.y;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int grp = p.c.group, hq = h * grp + r % grp;
-  const long long token = k.q0 + t0 + r / grp;
-  uint16_t* const dst = p.o + (token * p.c.hkv * grp + hq) * D + lane * kPer;
-  if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0)
-    p.lse[static_cast<long long>(hq) * p.c.total + token] =
-        sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  };
+  auto finish = [&](int r, float mx, float sum, const float(&acc)[kPer]) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int hq = h * grp + r % grp;
+    const long long token = k.q0 + t0 + r / grp;
+    uint16_t* const dst = p.o + (token * p.c.hkv * grp + hq) * D + lane * kPer;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0)
+      p.lse[static_cast<long long>(hq) * p.c.total + token] =
+          sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
+  };
+
+  float mx, sum, acc[kPer];
+  if constexpr (SPLIT == 1) {
+    for (int r = row0 + warp; r < min(row0 + kJoinRows, n_rows); r += 8) {
+      gather(r, c0, 1, mx, sum, acc);
+      finish(r, mx, sum, acc);
+    }
+  } else {
+    gather(row0, c0 + warp, SPLIT, mx, sum, acc);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
+    if (lane == 0) s_ml[warp] = make_float2(mx, sum);
+    __syncthreads();
+    if (warp != 0) return;
+    mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) mx = fmaxf(mx, s_ml[w].x);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) {
+      const float2 ml = s_ml[w];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+      sum += f * ml.y;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += f * s_acc[w][lane * kPer + i];
+    }
+    finish(row0, mx, sum, acc);
+  }
 }
 
 template <int D>
@@ -622,9 +679,22 @@ cudaError_t launch(const CacheAttnLaunch& a) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int mt_max = (p.c.max_new + p.nt - 1) / p.nt;
-  const long long rows = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max * p.rows;
-  cache_join_kernel<D><<<static_cast<unsigned int>((rows + 7) / 8), 256, 0, a.stream>>>(p, a.grid, mt_max);
-  return cudaGetLastError();
+  const long long tiles = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max;
+  const bool few = tiles * p.rows <= 16 * a.grid / 2;  // at most 16 blocks an SM, a row each
+  const long long blocks = tiles * (few ? p.rows : (p.rows + kJoinRows - 1) / kJoinRows);
+  // The join starts while the attention kernel runs and waits for its end on the
+  // device, which hides its launch.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned int>(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = a.stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 8>, p, a.grid, mt_max)
+             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 1>, p, a.grid, mt_max);
 }
 
 }  // namespace
