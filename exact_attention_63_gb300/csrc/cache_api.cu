@@ -50,8 +50,8 @@ int check_cache(const attn_cache* a, int kv, CacheParams* c) {
   const long long dense[3] = {hd * a->page_size, hd, a->d};
   if ((kv & 1) && !resolve<3>(a->k_strides, dense, c->k_st)) return ATTN_ERR_CACHE;
   if ((kv & 2) && !resolve<3>(a->v_strides, dense, c->v_st)) return ATTN_ERR_CACHE;
-  if (((kv & 1) && !aligned(a->k, 16)) || ((kv & 2) && !aligned(a->v, 16)) || !aligned(a->weights, 4) ||
-      !aligned(a->positions, 4) || !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4))
+  if (((kv & 1) && !aligned(a->k, 16)) || ((kv & 2) && !aligned(a->v, 16)) || !aligned(a->weights, 16) ||
+      !aligned(a->positions, 16) || !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4))
     return ATTN_ERR_ALIGN;
   c->k = static_cast<uint16_t*>(a->k);
   c->v = static_cast<uint16_t*>(a->v);
@@ -249,15 +249,19 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   const long long dense[2] = {static_cast<long long>(x->H) * c.d, c.d};
   long long qs[2];
   if (!resolve<2>(x->q_strides, dense, qs)) return ATTN_ERR_CACHE;
-  if (!aligned(lse, 4) || !aligned(weights_out, 4)) return ATTN_ERR_ALIGN;
+  if (!aligned(lse, 4) || !aligned(weights_out, 16)) return ATTN_ERR_ALIGN;
   int sms = 0;
   if ((rc = attn::usable_device(&a.device, &a.p.status, &sms)) != ATTN_OK) return rc;
   a.p.lse = lse;
   a.p.out = weights_out;
   a.p.nt = tile_tokens(c.group, c.max_new);
   a.p.n_cols = (a.p.nt * c.group + 15) & ~15;
+  a.p.by_hkv = attn::fast_div(c.hkv);
+  a.p.by_page = attn::fast_div(c.page_size);
+  a.p.by_nt = attn::fast_div(a.p.nt);
   a.p.piece = piece_of(c.page_size);
   a.p.scale_log2 = scale * 1.4426950408889634f;
+  a.p.inv_scale = 1.f / scale;
   a.p.timeout_ns = kDefaultTimeoutMs * 1000000ull;
   a.grid = tiles < sms ? static_cast<int>(tiles) : sms;
   a.stream = stream;

@@ -54,9 +54,9 @@ __device__ __forceinline__ void prefix_table(int n, int* tab, int* sums, F units
   __syncthreads();
 }
 
-// The sequence s with tab[s] <= u < tab[s + 1].
-__device__ __forceinline__ int find_seq(const int* tab, int n, int u) {
-  int lo = 0, hi = n - 1;
+// The sequence s with tab[s] <= u < tab[s + 1]; `lo`: one known not to be behind it.
+__device__ __forceinline__ int find_seq(const int* tab, int n, int u, int lo = 0) {
+  int hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (tab[mid] <= u) lo = mid;

@@ -144,21 +144,36 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool newest) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Position of the k-th (from 0) set bit of m.
+__device__ __forceinline__ int nth_bit(uint32_t m, int k) {
+  int at = 0;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const int below = __popc((m >> at) & ((1u << w) - 1u));
+    if (k >= below) {
+      k -= below;
+      at += w;
+    }
+  }
+  return at;
+}
+
 struct SelectSmem {
   uint32_t words, groups, keys;  // bit-map words, groups of four words, cached keys
+  uint32_t offset;               // of the keys, bytes
 };
 __host__ __device__ inline SelectSmem select_smem(int cap) {
   SelectSmem m;
   m.groups = static_cast<uint32_t>((cap + 127) / 128);
   m.words = 4 * m.groups;
-  const uint32_t fixed = kBins * 4 + 64 * 4 + m.words * 4 + (m.groups + 1) * 4;
-  const uint32_t room = (kSmemMax - fixed) / 4;
-  m.keys = room < static_cast<uint32_t>(cap) ? room : static_cast<uint32_t>(cap);
+  m.offset = (kBins * 4 + 64 * 4 + m.words * 4 + m.groups * 4 + 15) & ~15u;
+  const uint32_t room = (kSmemMax - m.offset) / 16 * 4;
+  m.keys = room < static_cast<uint32_t>(cap) ? room : static_cast<uint32_t>(cap);  // cap: a multiple of 16
   return m;
 }
 inline uint32_t select_bytes(int cap) {
   const SelectSmem m = select_smem(cap);
-  return kBins * 4 + 64 * 4 + m.words * 4 + (m.groups + 1) * 4 + m.keys * 4;
+  return m.offset + m.keys * 4;
 }
 
 // Exclusive sum over the CTA's threads, and the total; `w`: 33 ints.
@@ -192,13 +207,13 @@ __device__ __forceinline__ int block_exclusive(int v, int* w, int* total) {
 
 __global__ void __launch_bounds__(kThreadsSel)
     cache_select_kernel(const CacheParams c, const int* seq_pos, int budget, int recent, int* kept) {
-  extern __shared__ uint32_t sel_smem[];
+  extern __shared__ __align__(16) uint32_t sel_smem[];
   const SelectSmem lay = select_smem(c.cap);
   int* const hist = reinterpret_cast<int*>(sel_smem);
   int* const scratch = hist + kBins;  // 33 for scans, then [40] digit, [41] count above
   uint32_t* const bits = reinterpret_cast<uint32_t*>(scratch + 64);
   int* const before = reinterpret_cast<int*>(bits + lay.words);
-  uint32_t* const keys = reinterpret_cast<uint32_t*>(before + lay.groups + 1);
+  uint4* const kq = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(sel_smem) + lay.offset);  // four keys each
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / c.hkv, h = blockIdx.x - s * c.hkv;
@@ -211,15 +226,23 @@ __global__ void __launch_bounds__(kThreadsSel)
   }
   const int* const tab = c.table + static_cast<long long>(s) * c.max_blocks;
   const long long newest = (c.positions != nullptr ? static_cast<long long>(seq_pos[s]) : len) - recent;
-  auto load_key = [&](int j) -> uint32_t {
-    const int b = j / c.page_size;
+  // Four slots at a time: page_size is a multiple of four, so they share a page.
+  const int quads = (len + 3) / 4;
+  auto load_quad = [&](int b, int off, int j) -> uint4 {
     const int page = min(max(tab[b], 0), c.n_pages - 1);
-    const long long at = (static_cast<long long>(page) * c.hkv + h) * c.page_size + (j - b * c.page_size);
-    const int pos = c.positions != nullptr ? c.positions[at] : j;
-    return rank_key(c.weights[at], pos >= newest);
+    const long long at = (static_cast<long long>(page) * c.hkv + h) * c.page_size + off;
+    const float4 w = *reinterpret_cast<const float4*>(c.weights + at);
+    int4 pos = make_int4(j, j + 1, j + 2, j + 3);
+    if (c.positions != nullptr) pos = *reinterpret_cast<const int4*>(c.positions + at);
+    return make_uint4(rank_key(w.x, pos.x >= newest), rank_key(w.y, pos.y >= newest), rank_key(w.z, pos.z >= newest),
+                      rank_key(w.w, pos.w >= newest));
   };
   const bool cached = len <= static_cast<int>(lay.keys);
-  auto key_of = [&](int j) { return cached ? keys[j] : load_key(j); };
+  auto quad_of = [&](int q) -> uint4 {
+    if (cached) return kq[q];
+    const int b = 4 * q / c.page_size;
+    return load_quad(b, 4 * q - b * c.page_size, 4 * q);
+  };
 
   // ---- threshold: the budget-th largest key, and how many equal to it stay
   uint32_t prefix = 0, fixed_bits = 0;
@@ -229,19 +252,41 @@ __global__ void __launch_bounds__(kThreadsSel)
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
     for (int i = tid; i < kBins; i += kThreadsSel) hist[i] = 0;
     __syncthreads();
-    if (pass == 0 && cached) {
-#pragma unroll 4
-      for (int j = tid; j < len; j += kThreadsSel) {
-        const uint32_t k = load_key(j);
-        keys[j] = k;
-        atomicAdd(&hist[k >> 21], 1);
+    auto count = [&](uint4 k, int q) {
+      const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * q + e < len && (x[e] & fixed_bits) == prefix)
+          atomicAdd(&hist[(x[e] >> shift) & ((1u << width) - 1u)], 1);
+    };
+    if (pass == 0) {
+      const int db = 4 * kThreadsSel / c.page_size, doff = 4 * kThreadsSel - db * c.page_size;
+      int b = 4 * tid / c.page_size, off = 4 * tid - b * c.page_size;
+      for (int q0 = tid; q0 < quads; q0 += 4 * kThreadsSel) {
+        uint4 k[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int q = q0 + e * kThreadsSel;
+          if (q < quads) k[e] = load_quad(b, off, 4 * q);
+          b += db;
+          off += doff;
+          if (off >= c.page_size) {
+            off -= c.page_size;
+            ++b;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int q = q0 + e * kThreadsSel;
+          if (q < quads) {
+            if (cached) kq[q] = k[e];
+            count(k[e], q);
+          }
+        }
       }
     } else {
-#pragma unroll 4
-      for (int j = tid; j < len; j += kThreadsSel) {
-        const uint32_t k = key_of(j);
-        if ((k & fixed_bits) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
-      }
+#pragma unroll 2
+      for (int q = tid; q < quads; q += kThreadsSel) count(quad_of(q), q);
     }
     __syncthreads();
     // Bins from the top: thread t has bins kBins − 1 − 2t and the next lower one.
@@ -261,47 +306,72 @@ __global__ void __launch_bounds__(kThreadsSel)
   }
   const uint32_t thr = prefix;
 
-  // ---- the map of the slots that stay; each warp has a run of groups of 128 slots
+  // ---- the map of the slots that stay; each warp has a run of groups of 128
+  // slots, a lane four of them
   const int groups = (len + 127) / 128, per = (groups + 31) / 32;
   const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
-  int eq = 0;
-  for (int g = g0; g < g1; ++g)
+  const unsigned int octet = 0xffu << (lane & 24);
+  auto nibble = [&](int g, uint32_t& gt, uint32_t& eq) {
+    const int q = g * 32 + lane;
+    gt = eq = 0u;
+    if (q < quads) {
+      const uint4 k = quad_of(q);
+      const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = g * 128 + 32 * e + lane;
-      const uint32_t k = j < len ? key_of(j) : 0u;
-      const uint32_t be = __ballot_sync(0xffffffffu, j < len && k == thr), bg = __ballot_sync(0xffffffffu, j < len && k > thr);
-      if (lane == 0) bits[4 * g + e] = bg;
-      eq += __popc(be);
+      for (int e = 0; e < 4; ++e)
+        if (4 * q + e < len) {
+          gt |= (x[e] > thr ? 1u : 0u) << e;
+          eq |= (x[e] == thr ? 1u : 0u) << e;
+        }
     }
+  };
+  int eq = 0;
+  for (int g = g0; g < g1; ++g) {
+    uint32_t ng, ne;
+    nibble(g, ng, ne);
+    const uint32_t word = __reduce_or_sync(octet, ng << (4 * (lane & 7)));
+    if ((lane & 7) == 0) bits[4 * g + (lane >> 3)] = word;
+    eq += __popc(ne);
+  }
+  eq = __reduce_add_sync(0xffffffffu, eq);
   int total;
   int eq_before = block_exclusive(lane == 0 ? eq : 0, scratch, &total);
   eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
   int src = 0;  // kept slots at or beyond n in this warp's run
   for (int g = g0; g < g1; ++g) {
-    if (eq > 0) {
+    if (eq > 0 && eq_before < want) {  // of the equal ones the first stay
+      uint32_t ng, ne;
+      nibble(g, ng, ne);
+      const int mine = __popc(ne);
+      int incl = mine;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = g * 128 + 32 * e + lane;
-        const uint32_t be = __ballot_sync(0xffffffffu, j < len && key_of(j) == thr);
-        const int rank = eq_before + __popc(be & ((1u << lane) - 1u));
-        const uint32_t stay = __ballot_sync(0xffffffffu, ((be >> lane) & 1u) && rank < want);
-        if (lane == 0) bits[4 * g + e] |= stay;
-        eq_before += __popc(be);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
       }
-      __syncwarp();
-    }
-    if (lane == 0) {
-      before[g] = src;
+      int room = want - eq_before - (incl - mine);
+      uint32_t stay = 0u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int lowest = g * 128 + 32 * e;
-        uint32_t m = bits[4 * g + e];
-        if (lowest + 32 <= n) m = 0u;
-        else if (lowest < n) m &= ~0u << (n - lowest);
-        src += __popc(m);
-      }
+      for (int e = 0; e < 4; ++e)
+        if ((ne >> e) & 1u) {
+          if (room > 0) stay |= 1u << e;
+          --room;
+        }
+      const uint32_t word = __reduce_or_sync(octet, stay << (4 * (lane & 7)));
+      if ((lane & 7) == 0) bits[4 * g + (lane >> 3)] |= word;
+      eq_before += __shfl_sync(0xffffffffu, incl, 31);
     }
+    __syncwarp();
+    int cnt = 0;
+    if (lane < 4) {
+      const int lowest = g * 128 + 32 * lane;
+      uint32_t m = bits[4 * g + lane];
+      if (lowest + 32 <= n) m = 0u;
+      else if (lowest < n) m &= ~0u << (n - lowest);
+      cnt = __popc(m);
+    }
+    if (lane == 0) before[g] = src;
+    src += __reduce_add_sync(0xffffffffu, cnt);
   }
   int src_before = block_exclusive(lane == 0 ? src : 0, scratch, &total);
   src_before = __shfl_sync(0xffffffffu, src_before, 0);
@@ -344,7 +414,7 @@ __global__ void __launch_bounds__(kThreadsSel)
           if (lowest + 32 <= n) m = 0u;
           else if (lowest < n) m &= ~0u << (n - lowest);
           const int cnt = __popc(m);
-          if (k >= 0 && k < cnt) from = lowest + static_cast<int>(__fns(m, 0, k + 1));
+          if (k >= 0 && k < cnt) from = lowest + nth_bit(m, k);
           k -= cnt;
         }
       }

@@ -12,6 +12,24 @@ namespace attn {
 constexpr int kCacheMaxSeq = 2048;   // sequences of one call: their offsets are kept in shared memory
 constexpr int kCacheMaxCtas = 320;   // CTAs of the attention kernel (two per SM); sizes its workspace
 
+// Division by a number fixed for the launch: x / d = x·mul >> (31 + log), exact
+// for 0 ≤ x < 2^31 (mul = ⌈2^(31 + log) / d⌉, log = ⌈log2 d⌉).  The loaders of short
+// tiles do several divisions a tile, one warp alone: the compiler's division, some
+// 30 dependent instructions, showed.
+struct FastDiv {
+  unsigned int mul;
+  int shift, d;
+  __host__ __device__ int operator()(int x) const {
+    return d == 1 ? x : static_cast<int>((static_cast<unsigned long long>(x) * mul) >> shift);
+  }
+};
+inline FastDiv fast_div(int d) {
+  int log = 0;
+  while ((1ll << log) < d) ++log;
+  const unsigned long long num = 1ull << (31 + log);
+  return {d == 1 ? 0u : static_cast<unsigned int>((num + d - 1) / d), 31 + log, d};
+}
+
 // What every cache kernel knows of the cache and the new tokens.
 struct CacheParams {
   uint16_t* k;
@@ -56,10 +74,12 @@ struct CacheWeightParams {
   CacheParams c;
   const float* lse;      // [H, total]
   float* out;
+  FastDiv by_hkv, by_page, by_nt;
   int nt;                // tokens of a chunk
   int n_cols;            // its rows rounded up to the MMA's multiple of 16
+  int k_stages, q_stages;  // slots of the two rings (set by the launch)
   int piece;
-  float scale_log2;
+  float scale_log2, inv_scale;
   unsigned int* status;
   uint64_t timeout_ns;
 };

@@ -15,30 +15,58 @@
 // tiles, which most rows see, first, and every second round of CTAs in reverse,
 // so that the heaviest tiles and the lightest go to the same CTA.
 //
-// Warps: 0 loads, 1 issues the MMAs, 4-7 and 8-11 sum the two halves of the tile.
-// TMEM: S of half w, buffer i at columns 256·i + 128·w.
+// The −LSE of a column comes out of the tensor core with the score: one more step
+// of 16 along the product's inner dimension multiplies a constant (1, 1, 1, 0, …) on
+// the keys' side with (hi, mid, lo, 0, …) on the rows', three bf16 numbers that add
+// up to −LSE/scale to 24 bits.  The sums then read no shared memory, whose bandwidth
+// the MMAs' operands fill: with the LSE loaded from there, one value for every four
+// bytes of operands, the sums of a chunk took 2.3 times as long as the exponentials.
+//
+// Warps: 0 loads keys; 1 and 2 issue the MMAs of a half each (one thread issues an
+// MMA every ~80 cycles beside the sums, and a commit costs it more than that); 3 and
+// 20 in turn load a chunk of rows and prepare its columns; 4-7 and 8-11 sum the two
+// halves of the tile over the even chunks, 12-15 and 16-19 over the odd ones, so that
+// one chunk's waits and latencies hide behind the other's exponentials.
+// TMEM: S of half w, buffer i at columns 256·i + 128·w.  Shared memory holds a ring
+// of 128-key slots and one of chunks; a chunk of few rows takes little room, which
+// the key ring gets (more bytes in flight where memory is the bound).
 #include "attn_fwd_kernel.cuh"
 #include "cache_device.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kThreadsCW = 384;
+constexpr int kThreadsCW = 672;
 constexpr int kTileKeys = 256;
+
+constexpr int kMaxStages = 8;
+constexpr int kColSlots = 4;
 
 template <int D>
 struct WL {
   static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kK1 = 128u * D * 2;               // 128 keys: [half][128 rows][128 B]
-  static constexpr int kKStages = 2, kQStages = D == 128 ? 2 : 4;
-  static constexpr uint32_t kK = 0, kQ = kKStages * 2 * kK1, kCol = kQ + kQStages * kK1;
-  static constexpr uint32_t kBar = kCol + 8 * 128 * 8;        // 8 warps' own copies of (−LSE·log2 e, limit) per column
-  static constexpr int kNumBars = 2 * kKStages + 2 * kQStages + 4 + 1;
+  static constexpr uint32_t kSlot = 128u * D * 2;   // 128 keys: [half][128 rows][128 B]
+  static constexpr uint32_t kOnes = 0;              // the keys' side of the added step, 4 KB
+  static constexpr uint32_t kCol = 4096;            // kColSlots × (the rows' side, 4 KB; 128 ints)
+  static constexpr uint32_t kColBytes = 4096 + 512;
+  static constexpr int kNumBars = 4 * kMaxStages + 2 * kColSlots + 12;
+  static constexpr uint32_t kSet = kCol + kColSlots * kColBytes;  // 256 sums of the odd chunks
+  static constexpr uint32_t kBar = kSet + 1024;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
   static constexpr uint32_t kSums = kMisc + 8;
-  static constexpr uint32_t kTable = (kSums + 48 + 15) & ~15u;
-  static constexpr uint32_t kBytes = kTable + 1024;
+  static constexpr uint32_t kTable = (kSums + 80 + 15) & ~15u;
+  // then the table of n_seq + 1 ints, three ints a sequence, and from a 1024-byte
+  // boundary the two rings
+  __host__ __device__ static uint32_t rings(int n_seq) { return (kTable + 4u * (4 * n_seq + 1) + 1023u) & ~1023u; }
 };
+
+// Shared-memory matrix descriptor of the added step's operands, without swizzle:
+// [two halves of 8 along K][groups of 8 rows][8 rows][16 bytes], halves 2 KB and
+// groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_added(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(2048 >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
 
 struct WTile {
   int s, h, j0;       // keys [j0, j0 + 256) of sequence s, head h
@@ -46,25 +74,22 @@ struct WTile {
   int c0, c1;         // chunks that see a key of the tile
 };
 
-__device__ __forceinline__ int tiles_of(const CacheParams& c, int s) {
-  return c.hkv * ((seq_len(c, s) + kTileKeys - 1) / kTileKeys);
-}
-__device__ __forceinline__ WTile tile_at(const CacheWeightParams& p, const int* tab, int u) {
+// `from`: a sequence known to begin at or before tile u (the last one asked for).
+__device__ __forceinline__ WTile tile_at(const CacheWeightParams& p, const int* tab, int u, int from = 0) {
   WTile t;
-  t.s = find_seq(tab, p.c.n_seq, u);
-  const SeqRows r = seq_rows(p.c, t.s);
-  t.q0 = r.q0;
-  t.n = r.n;
-  t.rows = min(r.n, p.c.max_new);
-  t.len = seq_len(p.c, t.s);
-  const int rem = u - tab[t.s];
-  t.h = rem % p.c.hkv;
-  t.j0 = rem / p.c.hkv * kTileKeys;
+  t.s = u < tab[from + 1] ? from : find_seq(tab, p.c.n_seq, u, from);
+  const int* const seq = tab + p.c.n_seq + 1 + 3 * t.s;  // its first row, rows and length
+  t.q0 = seq[0];
+  t.n = seq[1];
+  t.rows = min(t.n, p.c.max_new);
+  t.len = seq[2];
+  const int rem = u - tab[t.s], kt = p.by_hkv(rem);
+  t.h = rem - kt * p.c.hkv;
+  t.j0 = kt * kTileKeys;
   // Row i sees slots up to len − n + i: the first that sees slot j0.
   const int first = max(0, t.j0 - t.len + t.n);
-  t.c0 = first / p.nt;
-  t.c1 = (t.rows + p.nt - 1) / p.nt;
-  t.c1 = max(t.c0, t.c1);
+  t.c0 = p.by_nt(first);
+  t.c1 = max(t.c0, p.by_nt(t.rows + p.nt - 1));
   return t;
 }
 
@@ -85,23 +110,25 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   uint8_t* const smem = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBar;
   auto k_full = [&](int s) { return bars + 8u * s; };
-  auto k_empty = [&](int s) { return bars + 8u * (L::kKStages + s); };
-  auto q_full = [&](int s) { return bars + 8u * (2 * L::kKStages + s); };
-  auto q_empty = [&](int s) { return bars + 8u * (2 * L::kKStages + L::kQStages + s); };
-  constexpr uint32_t kB = 2 * L::kKStages + 2 * L::kQStages;
-  auto s_full = [&](int i) { return bars + 8u * (kB + i); };
-  auto s_free = [&](int i) { return bars + 8u * (kB + 2 + i); };
-  const uint32_t done = bars + 8u * (kB + 4);
+  auto k_empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  auto q_full = [&](int s) { return bars + 8u * (2 * kMaxStages + s); };
+  auto q_empty = [&](int s) { return bars + 8u * (3 * kMaxStages + s); };
+  auto c_full = [&](int s) { return bars + 8u * (4 * kMaxStages + s); };
+  auto c_empty = [&](int s) { return bars + 8u * (4 * kMaxStages + kColSlots + s); };
+  constexpr uint32_t kB = 4 * kMaxStages + 2 * kColSlots;
+  auto s_full = [&](int w, int i) { return bars + 8u * (kB + 2 * w + i); };
+  auto s_free = [&](int w, int i) { return bars + 8u * (kB + 4 + 2 * w + i); };
+  auto done = [&](int w) { return bars + 8u * (kB + 8 + w); };
+  const uint32_t x_full = bars + 8u * (kB + 10), x_empty = bars + 8u * (kB + 11);
+  const uint32_t ring_k = base + L::rings(p.c.n_seq), ring_q = ring_k + p.k_stages * L::kSlot;
+  const uint32_t q_half = static_cast<uint32_t>(p.n_cols) * 128u, q_bytes = q_half * L::kHalves;
+  const int kst = p.k_stages, qst = p.q_stages;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
-
-  prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) { return tiles_of(p.c, s); });
-  const int units = tab[p.c.n_seq];
-  if (tile_of(0, cta, grid, units) < 0) return;
 
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -110,24 +137,52 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   }
   if (threadIdx.x == 32) {
     *abort_flag = 0u;
-    for (int i = 0; i < L::kKStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(k_full(i), 1);
       mbar_init(k_empty(i), 1);
-    }
-    for (int i = 0; i < L::kQStages; ++i) {
       mbar_init(q_full(i), 1);
-      mbar_init(q_empty(i), 1);
+      mbar_init(q_empty(i), 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full(i), 1);
-      mbar_init(s_free(i), 8);
+    for (int i = 0; i < kColSlots; ++i) {
+      mbar_init(c_full(i), 1);
+      mbar_init(c_empty(i), 10);  // two issuers, the set's eight warps
     }
-    mbar_init(done, 1);
+    for (int w = 0; w < 2; ++w) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(s_full(w, i), 1);
+        mbar_init(s_free(w, i), 4);
+      }
+      mbar_init(done(w), 1);
+    }
+    mbar_init(x_full, 8);
+    mbar_init(x_empty, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  __syncthreads();
+  // The added step's constant side, and zeros where the other side stays zero.
+  for (int i = threadIdx.x; i < 256; i += kThreadsCW) {
+    *reinterpret_cast<uint4*>(smem + L::kOnes + 16 * i) =
+        i < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    if (i >= 128)
+      for (int j = 0; j < kColSlots; ++j)
+        *reinterpret_cast<uint4*>(smem + L::kCol + j * L::kColBytes + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) {
+    const SeqRows r = seq_rows(p.c, s);
+    const int len = seq_len(p.c, s);
+    int* const seq = tab + p.c.n_seq + 1 + 3 * s;
+    seq[0] = r.q0;
+    seq[1] = r.n;
+    seq[2] = len;
+    return p.c.hkv * ((len + kTileKeys - 1) / kTileKeys);
+  });
   tc_fence_after();
+  const int units = tab[p.c.n_seq];
+  if (tile_of(0, cta, grid, units) < 0) {
+    if (warp == 0) tmem_dealloc(*tmem_slot, 512);
+    return;
+  }
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
   const int nt = p.nt, grp = p.c.group;
@@ -140,41 +195,41 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
     const int ps = p.piece;
-    int nk = 0, nq = 0;
+    int nk = 0;
     bool ok = true;
-    for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
-      const WTile t = tile_at(p, tab, u);
-      if (t.c0 == t.c1) continue;  // no row sees it: nothing to multiply
-      // The tile's keys in pieces of ps rows: lane i has the i-th.
-      const int keys = min(kTileKeys, t.len - t.j0), npc = (keys + ps - 1) / ps;
-      int page = 0, slot = 0;
-      if (lane < npc) {
-        const int j = t.j0 + lane * ps, blk = j / p.c.page_size;
+    // Lane 8w + i copies the i-th piece of half w; its page, a tile ahead.
+    const int my_row = 128 * (lane >> 3) + (lane & 7) * ps;
+    auto locate = [&](const WTile& t, int& page, int& slot) {
+      const int j = t.j0 + my_row;
+      if (lane < 16 && (lane & 7) * ps < 128 && j < t.len) {
+        const int blk = p.by_page(j);
         slot = j - blk * p.c.page_size;
         page = page_for_read(p.c, t.s, blk);
       }
-      const int ks = nk % L::kKStages;
-      ok = waited(k_empty(ks), ((nk / L::kKStages) & 1) ^ 1u);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
-      __syncwarp();
-      if (lane < npc) {
-        const int row = lane * ps;
-        const uint32_t dst = base + L::kK + (2 * ks + (row >> 7)) * L::kK1 + (row & 127) * 128;
-        for (int hf = 0; hf < L::kHalves; ++hf) tma_load_4d(dst + hf * 16384, &tm_k, 64 * hf, t.h, slot, page, k_full(ks));
+    };
+    int u = tile_of(0, cta, grid, units);
+    WTile t = tile_at(p, tab, u), t_next = t;
+    int page = 0, slot = 0, page_next = 0, slot_next = 0;
+    locate(t, page, slot);
+    for (int n = 0; ok && u >= 0; ++n, t = t_next, page = page_next, slot = slot_next) {
+      u = tile_of(n + 1, cta, grid, units);
+      if (u >= 0) {
+        t_next = tile_at(p, tab, u, t.s);
+        locate(t_next, page_next, slot_next);
       }
-      __syncwarp();
-      ++nk;
-      for (int c = t.c0; c < t.c1 && ok; ++c) {
-        const int qs = nq % L::kQStages;
-        ok = waited(q_empty(qs), ((nq / L::kQStages) & 1) ^ 1u);
+      if (t.c0 == t.c1) continue;  // no row sees it: nothing to multiply
+      const int keys = min(kTileKeys, t.len - t.j0);
+      for (int w = 0; w < 2 && 128 * w < keys; ++w, ++nk) {
+        const int npc = (min(128, keys - 128 * w) + ps - 1) / ps, ks = nk % kst;
+        ok = waited(k_empty(ks), ((nk / kst) & 1) ^ 1u);
         if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(nt * grp) * 128u * L::kHalves);
+        if (lane == 0) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
+        __syncwarp();
+        if ((lane >> 3) == w && (lane & 7) < npc)
           for (int hf = 0; hf < L::kHalves; ++hf)
-            tma_load_4d(base + L::kQ + qs * L::kK1 + hf * 16384, &tm_q, 64 * hf, 0, t.h, t.q0 + c * nt, q_full(qs));
-        }
-        ++nq;
+            tma_load_4d(ring_k + ks * L::kSlot + (lane & 7) * ps * 128 + hf * 16384, &tm_k, 64 * hf, t.h, slot, page,
+                        k_full(ks));
+        __syncwarp();
       }
     }
     if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
@@ -183,122 +238,230 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         while (!mbar_try_wait(bar, parity))
           if (globaltimer_ns() - t0 > p.timeout_ns) break;
       };
-      for (int n = max(0, nk - L::kKStages); n < nk; ++n) drain(k_full(n % L::kKStages), (n / L::kKStages) & 1u);
-      for (int n = max(0, nq - L::kQStages); n < nq; ++n) drain(q_full(n % L::kQStages), (n / L::kQStages) & 1u);
+      for (int n = max(0, nk - kst); n < nk; ++n) drain(k_full(n % kst), (n / kst) & 1u);
     }
-  } else if (warp == 1) {
-    // ========================================================= MMA issuer
+  } else if (warp == 1 || warp == 2) {
+    // ======================================================== MMA issuers
     if (lane == 0) {
       const uint32_t id = idesc_bf16(128, p.n_cols, false);
-      int nk = 0, nq = 0;
+      const int w = warp - 1;
+      int nk = 0, nq = 0, from = 0;
       bool ok = true;
       for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
-        const WTile t = tile_at(p, tab, u);
+        const WTile t = tile_at(p, tab, u, from);
+        from = t.s;
         if (t.c0 == t.c1) continue;
-        const int ks = nk % L::kKStages;
-        ok = wait_bar(k_full(ks), (nk / L::kKStages) & 1, wc);
+        // A tile's second half may have no keys: its issuer only keeps count.
+        const int halves = t.len - t.j0 > 128 ? 2 : 1, ks = (nk + w) % kst;
+        if (w < halves) ok = wait_bar(k_full(ks), ((nk + w) / kst) & 1, wc);
+        const uint64_t dk = sdesc_kmajor_sw128(ring_k + ks * L::kSlot);
         for (int c = t.c0; c < t.c1 && ok; ++c, ++nq) {
-          const int qs = nq % L::kQStages, buf = nq & 1;
-          ok = wait_bar(q_full(qs), (nq / L::kQStages) & 1, wc) && wait_bar(s_free(buf), ((nq >> 1) & 1) ^ 1u, wc);
+          const int qs = nq % qst, buf = nq & 1;
+          const int cs = nq % kColSlots;
+          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc) && wait_bar(c_full(cs), (nq / kColSlots) & 1, wc) &&
+               wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ + qs * L::kK1);
+          if (w < halves) {
+            tc_fence_after();
+            mma_ss(tmem + 256 * buf + 128 * w, sdesc_added(base + L::kOnes),
+                   sdesc_added(base + L::kCol + cs * L::kColBytes), id, 0u);
+            const uint64_t dq = sdesc_kmajor_sw128(ring_q + qs * q_bytes);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + (2 * ks + w) * L::kK1);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              mma_ss(tmem + 256 * buf + 128 * w, dk + o, dq + o, id, kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + 256 * buf + 128 * w, dk + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                     dq + (((kk >> 2) * q_half + (kk & 3) * 32) >> 4), id, 1u);
           }
-          mma_commit(s_full(buf));
+          mma_commit(s_full(w, buf));
           mma_commit(q_empty(qs));
-          if (c == t.c1 - 1) mma_commit(k_empty(ks));
+          mma_commit(c_empty(cs));
         }
-        ++nk;
+        if (ok && w < halves) mma_commit(k_empty(ks));
+        nk += halves;
       }
-      mma_commit(done);
+      mma_commit(done(w));
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(done, 0))
+      while (!mbar_try_wait(done(w), 0))
         if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
-  } else if (warp >= 4) {
-    // =============================================================== sums
-    const int w = (warp - 4) >> 2;                       // half of the tile
-    const int row = 128 * w + (warp & 3) * 32 + lane;    // key of the tile
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float* const col_lse = reinterpret_cast<float*>(smem + L::kCol) + (warp - 4) * 256;
-    int* const col_lim = reinterpret_cast<int*>(col_lse + 128);
-    const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2);
-    int nq = 0;
+  } else if (warp == 3 || warp == 20) {
+    // ============================================================ columns
+    // The chunks with this warp's parity: their rows, and for each column
+    // −LSE/scale (−inf: it adds nothing) and the last slot seen; lane l has
+    // columns l, l + 32, …
+    int tk[4];
+    const float* src[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = lane + 32 * i;
+      tk[i] = col < nt * grp ? col / grp : 1 << 30;
+      src[i] = p.lse + static_cast<long long>(col % grp) * p.c.total;
+    }
+    int nq = 0, from = 0, mine = 0;
     bool ok = true;
     for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
-      const WTile t = tile_at(p, tab, u);
-      const int key = t.j0 + row;
-      float total = 0.f;
+      const WTile t = tile_at(p, tab, u, from);
+      from = t.s;
+      const long long row0 = static_cast<long long>(t.h) * grp * p.c.total + t.q0;
       for (int c = t.c0; c < t.c1; ++c, ++nq) {
-        const int buf = nq & 1;
-        const int tok0 = c * nt;
-        // This warp's copy of the columns' −LSE·log2 e (−inf: adds nothing) and
-        // of the last slot each one sees.
-        __syncwarp();
-        for (int col = lane; col < 128; col += 32) {
-          const int tk = tok0 + col / grp, g = col - (col / grp) * grp;
-          float v = -INFINITY;
-          if (col < nt * grp && tk < t.rows) {
-            v = -p.lse[static_cast<long long>(t.h * grp + g) * p.c.total + t.q0 + tk] * 1.4426950408889634f;
-            if (v == INFINITY) v = -INFINITY;
+        if ((nq & 1) != (warp & 1)) continue;  // 3: the odd ones
+        int go = 1;
+        if (lane == 0) {
+          const int qs = nq % qst;
+          go = wait_bar(q_empty(qs), ((nq / qst) & 1) ^ 1u, wc);
+          if (go) {
+            mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(nt * grp) * 128u * L::kHalves);
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(ring_q + qs * q_bytes + hf * q_half, &tm_q, 64 * hf, 0, t.h, t.q0 + c * nt, q_full(qs));
+            mine = nq + 1;
           }
-          col_lse[col] = v;
-          col_lim[col] = t.len - t.n + tk;
         }
-        __syncwarp();
-        const bool got = wait_bar_cold(s_full(buf), (nq >> 1) & 1, wc);
-        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
-        tc_fence_after();
-        // No mask where the chunk's first row sees the last key of this half.
-        const bool masked = min(t.j0 + 128 * w + 127, t.len - 1) > t.len - t.n + tok0;
-        float sum = 0.f;
-        for (int cc = 0; cc < p.n_cols; cc += 32) {
-          uint32_t x[32];
-          tmem_ld32(tmem + 256 * buf + 128 * w + cc + lane_off, x);
-          tmem_wait_ld();
-          reg_fence32(x);
-          uint64_t acc[2] = {0, 0};
+        if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
+        float v[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 nl = *reinterpret_cast<const float2*>(&col_lse[cc + 2 * i]);
-            float a, b;
-            unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, pack2(nl.x, nl.y)), a, b);
-            a = ex2_mufu(a);
-            b = ex2_mufu(b);
-            // A column without a row may hold anything.
-            if (nl.x == -INFINITY) a = 0.f;
-            if (nl.y == -INFINITY) b = 0.f;
-            if (masked) {
-              if (key > col_lim[cc + 2 * i]) a = 0.f;
-              if (key > col_lim[cc + 2 * i + 1]) b = 0.f;
-            }
-            acc[i & 1] = fadd2(acc[i & 1], pack2(a, b));
+        for (int i = 0; i < 4; ++i) {
+          v[i] = -INFINITY;
+          if (tk[i] < t.rows - c * nt) {
+            v[i] = -src[i][row0 + c * nt + tk[i]] * p.inv_scale;
+            if (v[i] == INFINITY) v[i] = -INFINITY;
           }
-          float a0, a1;
-          unpack2(fadd2(acc[0], acc[1]), a0, a1);
-          sum += a0 + a1;
         }
-        total += sum;
-        tc_fence_before();
-        warp_arrive(s_free(buf), lane);
+        const int cs = nq % kColSlots;
+        const bool got = wait_bar_cold(c_empty(cs), ((nq / kColSlots) & 1) ^ 1u, wc);
+        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
+        uint8_t* const col = smem + L::kCol + cs * L::kColBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // v = hi + mid + lo, each a rounding to bf16 of what the ones before leave.
+          const uint32_t hi = pack_bf16x2(v[i], 0.f) & 0xffffu;
+          float rest = v[i] - __uint_as_float(hi << 16);
+          if (v[i] == -INFINITY) rest = 0.f;
+          const uint32_t mid = pack_bf16x2(rest, 0.f) & 0xffffu;
+          const uint32_t lo = pack_bf16x2(rest - __uint_as_float(mid << 16), 0.f) & 0xffffu;
+          *reinterpret_cast<uint4*>(col + 16 * (lane + 32 * i)) = make_uint4(hi | (mid << 16), lo, 0u, 0u);
+          reinterpret_cast<int*>(col + 4096)[lane + 32 * i] = t.len - t.n + c * nt + (tk[i] & 0xffff);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(c_full(cs), lane);
       }
-      if (!ok) break;
+    }
+    if (lane == 0 && !ok) {  // this warp's copies (chunks mine − 1, mine − 3, …) have to land
+      const uint64_t t0 = globaltimer_ns();
+      for (int c = mine - 1; c >= 0 && c > mine - 1 - qst; c -= 2)
+        while (!mbar_try_wait(q_full(c % qst), (c / qst) & 1u))
+          if (globaltimer_ns() - t0 > p.timeout_ns) break;
+    }
+  } else {
+    // =============================================================== sums
+    const int w = ((warp - 4) >> 2) & 1, set = (warp - 4) >> 3;  // half of the tile; parity of the chunks
+    const int row = 128 * w + (warp & 3) * 32 + lane;            // key of the tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2);
+    float* const other = reinterpret_cast<float*>(smem + L::kSet);
+    // The weight gathered so far by this thread's key of tile t: where it is, and
+    // the load, issued a tile ahead (under a full memory pipe it takes as long as a
+    // tile of few rows).
+    auto fetch = [&](const WTile& t, long long& at, float& start) {
+      const int key = t.j0 + row;
+      at = -1;
+      start = 0.f;
       if (key < t.len) {
-        const int blk = key / p.c.page_size;
+        const int blk = p.by_page(key);
         const int page = p.c.table[static_cast<long long>(t.s) * p.c.max_blocks + blk];
         if (page >= 0 && page < p.c.n_pages) {
-          const long long at = (static_cast<long long>(page) * p.c.hkv + t.h) * p.c.page_size + (key - blk * p.c.page_size);
-          p.out[at] = (p.c.weights != nullptr ? p.c.weights[at] : 0.f) + total;
+          at = (static_cast<long long>(page) * p.c.hkv + t.h) * p.c.page_size + (key - blk * p.c.page_size);
+          if (p.c.weights != nullptr) start = p.c.weights[at];
         }
       }
+    };
+    int nq = 0, joins = 0;
+    bool ok = true;
+    int u = tile_of(0, cta, grid, units);
+    WTile t = tile_at(p, tab, u), t_next = t;
+    long long at, at_next = -1;
+    float start, start_next = 0.f;
+    fetch(t, at, start);
+    for (int n = 0; u >= 0; ++n, t = t_next, at = at_next, start = start_next) {
+      u = tile_of(n + 1, cta, grid, units);
+      if (u >= 0) {
+        t_next = tile_at(p, tab, u, t.s);
+        fetch(t_next, at_next, start_next);
+      }
+      const int key = t.j0 + row;
+      const bool live = t.j0 + 128 * w + (warp & 3) * 32 < t.len;  // this warp has a key
+      const int chunks = t.c1 - t.c0;
+      // The one set that has a part of it writes the tile: with several chunks the
+      // even one, after the odd one's sums.
+      const bool writes = chunks == 1 ? (nq & 1) == set : set == 0;
+      float total = 0.f;
+      for (int c = t.c0; c < t.c1; ++c, ++nq) {
+        if ((nq & 1) != set) continue;
+        const int cs = nq % kColSlots;
+        const int tok0 = c * nt, valid = min(nt, t.rows - tok0) * grp;
+        // No mask where the chunk's first row sees the last key of this half.
+        const bool masked = min(t.j0 + 128 * w + 127, t.len - 1) > t.len - t.n + tok0;
+        bool got = wait_bar_cold(s_full(w, set), (nq >> 1) & 1, wc);
+        if (masked) got = got && wait_bar_cold(c_full(cs), (nq / kColSlots) & 1, wc);
+        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
+        tc_fence_after();
+        const int* const lim = reinterpret_cast<const int*>(smem + L::kCol + cs * L::kColBytes + 4096);
+        const uint32_t tS = tmem + 256 * set + 128 * w + lane_off;
+        uint64_t acc[2] = {0, 0};
+        // 2^(scale·log2 e·(s − LSE/scale)) over 32 columns.
+        auto group = [&](int cc, uint32_t(&x)[32]) {
+          if (cc + 32 <= valid && !masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a, b;
+              unpack2(fmul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2), a, b);
+              acc[i & 1] = fadd2(acc[i & 1], pack2(ex2_mufu(a), ex2_mufu(b)));
+            }
+          } else {
+            // Columns without a row may hold anything: nothing of them is added.
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float a = ex2_mufu(__uint_as_float(x[i]) * p.scale_log2);
+              sum += (cc + i >= valid || (masked && key > lim[cc + i])) ? 0.f : a;
+            }
+            acc[0] = fadd2(acc[0], pack2(sum, 0.f));
+          }
+        };
+        if (live) {
+#pragma unroll 1
+          for (int cc = 0; cc < valid; cc += 32) {
+            uint32_t x[32];
+            tmem_ld32(tS + cc, x);
+            tmem_wait_ld();
+            reg_fence32(x);
+            group(cc, x);
+          }
+        }
+        float a0, a1;
+        unpack2(fadd2(acc[0], acc[1]), a0, a1);
+        total += a0 + a1;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(s_free(w, set));
+          mbar_arrive(c_empty(cs));
+        }
+      }
+      if (!ok) break;
+      if (chunks > 1) {
+        if (set == 1) {
+          const bool got = wait_bar_cold(x_empty, (joins & 1) ^ 1u, wc);
+          if (__any_sync(0xffffffffu, !got)) break;
+          other[row] = total;
+          warp_arrive(x_full, lane);
+        } else {
+          const bool got = wait_bar_cold(x_full, joins & 1, wc);
+          if (__any_sync(0xffffffffu, !got)) break;
+          total += other[row];
+          warp_arrive(x_empty, lane);
+        }
+        ++joins;
+      }
+      if (writes && at >= 0) p.out[at] = start + total;
     }
   }
 
@@ -312,16 +475,23 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
 
 template <int D>
 cudaError_t launch(const CacheWeightLaunch& a) {
-  const unsigned int smem = WL<D>::kBytes + 4u * (a.p.c.n_seq + 1);
+  CacheWeightParams p = a.p;
+  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq), q_bytes = static_cast<uint32_t>(p.n_cols) * D * 2;
+  // Four chunks in flight, and the keys get the rest: two slots (one tile) at least.
+  p.q_stages = 4;
+  while (room - p.q_stages * q_bytes < 2 * WL<D>::kSlot) --p.q_stages;  // many sequences: their table takes room
+  const uint32_t k_stages = (room - p.q_stages * q_bytes) / WL<D>::kSlot;
+  p.k_stages = static_cast<int>(k_stages < kMaxStages ? k_stages : kMaxStages);
+  const uint32_t smem = WL<D>::rings(p.c.n_seq) + p.k_stages * WL<D>::kSlot + p.q_stages * q_bytes + 1024u;
   static volatile bool configured[64] = {};
   if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
   if (!configured[a.device]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               WL<D>::kBytes + 4 * (kCacheMaxSeq + 1));
+    const cudaError_t e =
+        cudaFuncSetAttribute(cache_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
     configured[a.device] = true;
   }
-  cache_weights_kernel<D><<<a.grid, kThreadsCW, smem, a.stream>>>(a.q, a.k, a.p);
+  cache_weights_kernel<D><<<a.grid, kThreadsCW, smem, a.stream>>>(a.q, a.k, p);
   return cudaGetLastError();
 }
 

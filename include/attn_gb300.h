@@ -440,8 +440,8 @@ int attn_fwd_fp8_ex(const void* q8, const void* k8, const void* v8, void* o, flo
  * Every call is asynchronous on `stream`, allocates nothing and can be captured
  * into a graph; lengths, tables and offsets may change between replays.
  * Errors are as for attn_fwd, with ATTN_ERR_CACHE for an invalid field of the
- * two structs and ATTN_ERR_ALIGN for a tensor that is not 16-byte (k, v, q, o),
- * 4-byte (all others) or, for attn_cache_weights' lse, 4-byte aligned.
+ * two structs and ATTN_ERR_ALIGN for a tensor that is not aligned to 16 bytes
+ * (k, v, q, o, weights, positions) or 4 bytes (all others).
  * ------------------------------------------------------------------------ */
 typedef struct attn_cache {
   size_t struct_size;

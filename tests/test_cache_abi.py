@@ -80,8 +80,8 @@ PAGED = ("attend", "append", "weigh", "compact")   # those that read k
     ("n_pages", 0, SHAPE, ALL), ("max_blocks", 0, SHAPE, ALL), ("max_blocks", 1 << 27, CACHE, ALL),
     ("num_kv_heads", 0, SHAPE, ALL), ("num_kv_heads", 3, CACHE, ("attend", "weigh")),
     ("d", 96, DIM, PAGED), ("k", A + 8, ALIGN, PAGED), ("v", A + 8, ALIGN, ("attend", "append", "compact")),
-    ("block_table", A + 2, ALIGN, ALL), ("seq_lens", A + 1, ALIGN, ALL), ("weights", A + 2, ALIGN, ALL),
-    ("positions", A + 2, ALIGN, ALL),
+    ("block_table", A + 2, ALIGN, ALL), ("seq_lens", A + 1, ALIGN, ALL), ("weights", A + 4, ALIGN, ALL),
+    ("positions", A + 8, ALIGN, ALL),
     ("k_strides", (2048, 128, 60), CACHE, PAGED), ("k_strides", (2048, 0, 64), CACHE, PAGED),
     ("v_strides", (-2048, 128, 64), CACHE, ("attend", "append", "compact")),
     ("k_strides", (1 << 38, 128, 64), CACHE, PAGED),
@@ -116,7 +116,7 @@ def test_token_fields(L, field, value, expect, ops):
     (dict(kept=None), NULL, ("select", "compact")), (dict(seq_pos=None), NULL, ("select",)),
     (dict(scale=0.0), SCALE, ("attend", "weigh")), (dict(scale=float("nan")), SCALE, ("attend", "weigh")),
     (dict(o=A + 8), ALIGN, ("attend",)), (dict(lse=A + 2), ALIGN, ("attend", "weigh")),
-    (dict(parents=A + 1), ALIGN, ("attend",)), (dict(out=A + 2), ALIGN, ("weigh",)),
+    (dict(parents=A + 1), ALIGN, ("attend",)), (dict(out=A + 8), ALIGN, ("weigh",)),
     (dict(kept=A + 2), ALIGN, ("select", "compact")), (dict(seq_pos=A + 2), ALIGN, ("append", "select")),
     (dict(rows=A + 2, n_rows=3), ALIGN, ("append",)), (dict(rows=A, n_rows=0), SHAPE, ("append",)),
     (dict(budget=0), SHAPE, ("select", "compact")), (dict(recent=-1), SHAPE, ("select",)),
