@@ -22,11 +22,12 @@
 // the MMAs' operands fill: with the LSE loaded from there, one value for every four
 // bytes of operands, the sums of a chunk took 2.3 times as long as the exponentials.
 //
-// Warps: 0 loads keys; 1 and 2 issue the MMAs of a half each (one thread issues an
-// MMA every ~80 cycles beside the sums, and a commit costs it more than that); 3 and
-// 20 in turn load a chunk of rows and prepare its columns; 4-7 and 8-11 sum the two
-// halves of the tile over the even chunks, 12-15 and 16-19 over the odd ones, so that
-// one chunk's waits and latencies hide behind the other's exponentials.
+// Warps: 0 loads keys; 1 and 2 issue the MMAs of a half each; 3 loads the chunks of
+// rows and prepares their columns, a chunk's LSE fetched under the one before; 4-7
+// and 8-11 sum a half each, a thread a key: it takes all of a chunk's scores into
+// registers at once and gives the S buffer back, so that the tensor core works on the
+// next two chunks while the exponentials of one run (twice as many sum warps that
+// kept S in TMEM meanwhile were slower: 257 against 214 us on a prompt of 8000 tokens, 32 heads over 8 at d = 128).
 // TMEM: S of half w, buffer i at columns 256·i + 128·w.  Shared memory holds a ring
 // of 128-key slots and one of chunks; a chunk of few rows takes little room, which
 // the key ring gets (more bytes in flight where memory is the bound).
@@ -36,22 +37,20 @@
 namespace attn {
 namespace {
 
-constexpr int kThreadsCW = 672;
+constexpr int kThreadsCW = 384;
 constexpr int kTileKeys = 256;
 
 constexpr int kMaxStages = 8;
-constexpr int kColSlots = 4;
+constexpr int kMaxChunks = 4;  // slots of the chunk ring
 
 template <int D>
 struct WL {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kSlot = 128u * D * 2;   // 128 keys: [half][128 rows][128 B]
   static constexpr uint32_t kOnes = 0;              // the keys' side of the added step, 4 KB
-  static constexpr uint32_t kCol = 4096;            // kColSlots × (the rows' side, 4 KB; 128 ints)
-  static constexpr uint32_t kColBytes = 4096 + 512;
-  static constexpr int kNumBars = 4 * kMaxStages + 2 * kColSlots + 12;
-  static constexpr uint32_t kSet = kCol + kColSlots * kColBytes;  // 256 sums of the odd chunks
-  static constexpr uint32_t kBar = kSet + 1024;
+  static constexpr uint32_t kCol = 4096;            // the rows' side, 4 KB for each chunk slot
+  static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxChunks + 10;
+  static constexpr uint32_t kBar = kCol + kMaxChunks * 4096;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
   static constexpr uint32_t kSums = kMisc + 8;
   static constexpr uint32_t kTable = (kSums + 80 + 15) & ~15u;
@@ -112,14 +111,11 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   auto k_full = [&](int s) { return bars + 8u * s; };
   auto k_empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
   auto q_full = [&](int s) { return bars + 8u * (2 * kMaxStages + s); };
-  auto q_empty = [&](int s) { return bars + 8u * (3 * kMaxStages + s); };
-  auto c_full = [&](int s) { return bars + 8u * (4 * kMaxStages + s); };
-  auto c_empty = [&](int s) { return bars + 8u * (4 * kMaxStages + kColSlots + s); };
-  constexpr uint32_t kB = 4 * kMaxStages + 2 * kColSlots;
+  auto q_empty = [&](int s) { return bars + 8u * (2 * kMaxStages + kMaxChunks + s); };
+  constexpr uint32_t kB = 2 * kMaxStages + 2 * kMaxChunks;
   auto s_full = [&](int w, int i) { return bars + 8u * (kB + 2 * w + i); };
   auto s_free = [&](int w, int i) { return bars + 8u * (kB + 4 + 2 * w + i); };
   auto done = [&](int w) { return bars + 8u * (kB + 8 + w); };
-  const uint32_t x_full = bars + 8u * (kB + 10), x_empty = bars + 8u * (kB + 11);
   const uint32_t ring_k = base + L::rings(p.c.n_seq), ring_q = ring_k + p.k_stages * L::kSlot;
   const uint32_t q_half = static_cast<uint32_t>(p.n_cols) * 128u, q_bytes = q_half * L::kHalves;
   const int kst = p.k_stages, qst = p.q_stages;
@@ -140,12 +136,10 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(k_full(i), 1);
       mbar_init(k_empty(i), 1);
-      mbar_init(q_full(i), 1);
-      mbar_init(q_empty(i), 2);
     }
-    for (int i = 0; i < kColSlots; ++i) {
-      mbar_init(c_full(i), 1);
-      mbar_init(c_empty(i), 10);  // two issuers, the set's eight warps
+    for (int i = 0; i < kMaxChunks; ++i) {
+      mbar_init(q_full(i), 2);   // its rows, its columns
+      mbar_init(q_empty(i), 2);  // both issuers
     }
     for (int w = 0; w < 2; ++w) {
       for (int i = 0; i < 2; ++i) {
@@ -154,8 +148,6 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       }
       mbar_init(done(w), 1);
     }
-    mbar_init(x_full, 8);
-    mbar_init(x_empty, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -164,8 +156,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     *reinterpret_cast<uint4*>(smem + L::kOnes + 16 * i) =
         i < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
     if (i >= 128)
-      for (int j = 0; j < kColSlots; ++j)
-        *reinterpret_cast<uint4*>(smem + L::kCol + j * L::kColBytes + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < kMaxChunks; ++j)
+        *reinterpret_cast<uint4*>(smem + L::kCol + j * 4096 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
   prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) {
@@ -257,23 +249,20 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         const uint64_t dk = sdesc_kmajor_sw128(ring_k + ks * L::kSlot);
         for (int c = t.c0; c < t.c1 && ok; ++c, ++nq) {
           const int qs = nq % qst, buf = nq & 1;
-          const int cs = nq % kColSlots;
-          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc) && wait_bar(c_full(cs), (nq / kColSlots) & 1, wc) &&
-               wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
+          const uint32_t tS = tmem + 256 * buf + 128 * w;
+          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc) && wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
           if (!ok) break;
           if (w < halves) {
             tc_fence_after();
-            mma_ss(tmem + 256 * buf + 128 * w, sdesc_added(base + L::kOnes),
-                   sdesc_added(base + L::kCol + cs * L::kColBytes), id, 0u);
+            mma_ss(tS, sdesc_added(base + L::kOnes), sdesc_added(base + L::kCol + qs * 4096), id, 0u);
             const uint64_t dq = sdesc_kmajor_sw128(ring_q + qs * q_bytes);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + 256 * buf + 128 * w, dk + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+              mma_ss(tS, dk + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                      dq + (((kk >> 2) * q_half + (kk & 3) * 32) >> 4), id, 1u);
           }
           mma_commit(s_full(w, buf));
           mma_commit(q_empty(qs));
-          mma_commit(c_empty(cs));
         }
         if (ok && w < halves) mma_commit(k_empty(ks));
         nk += halves;
@@ -283,11 +272,10 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       while (!mbar_try_wait(done(w), 0))
         if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
-  } else if (warp == 3 || warp == 20) {
-    // ============================================================ columns
-    // The chunks with this warp's parity: their rows, and for each column
-    // −LSE/scale (−inf: it adds nothing) and the last slot seen; lane l has
-    // columns l, l + 32, …
+  } else if (warp == 3) {
+    // ================================================================ rows
+    // Each chunk's rows, and for each column −LSE/scale (−inf: it adds nothing);
+    // lane l has columns l, l + 32, …
     int tk[4];
     const float* src[4];
 #pragma unroll
@@ -296,67 +284,75 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       tk[i] = col < nt * grp ? col / grp : 1 << 30;
       src[i] = p.lse + static_cast<long long>(col % grp) * p.c.total;
     }
-    int nq = 0, from = 0, mine = 0;
-    bool ok = true;
-    for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
-      const WTile t = tile_at(p, tab, u, from);
-      from = t.s;
-      const long long row0 = static_cast<long long>(t.h) * grp * p.c.total + t.q0;
-      for (int c = t.c0; c < t.c1; ++c, ++nq) {
-        if ((nq & 1) != (warp & 1)) continue;  // 3: the odd ones
-        int go = 1;
-        if (lane == 0) {
-          const int qs = nq % qst;
-          go = wait_bar(q_empty(qs), ((nq / qst) & 1) ^ 1u, wc);
-          if (go) {
-            mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(nt * grp) * 128u * L::kHalves);
-            for (int hf = 0; hf < L::kHalves; ++hf)
-              tma_load_4d(ring_q + qs * q_bytes + hf * q_half, &tm_q, 64 * hf, 0, t.h, t.q0 + c * nt, q_full(qs));
-            mine = nq + 1;
-          }
-        }
-        if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = -INFINITY;
-          if (tk[i] < t.rows - c * nt) {
-            v[i] = -src[i][row0 + c * nt + tk[i]] * p.inv_scale;
-            if (v[i] == INFINITY) v[i] = -INFINITY;
-          }
-        }
-        const int cs = nq % kColSlots;
-        const bool got = wait_bar_cold(c_empty(cs), ((nq / kColSlots) & 1) ^ 1u, wc);
-        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
-        uint8_t* const col = smem + L::kCol + cs * L::kColBytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // v = hi + mid + lo, each a rounding to bf16 of what the ones before leave.
-          const uint32_t hi = pack_bf16x2(v[i], 0.f) & 0xffffu;
-          float rest = v[i] - __uint_as_float(hi << 16);
-          if (v[i] == -INFINITY) rest = 0.f;
-          const uint32_t mid = pack_bf16x2(rest, 0.f) & 0xffffu;
-          const uint32_t lo = pack_bf16x2(rest - __uint_as_float(mid << 16), 0.f) & 0xffffu;
-          *reinterpret_cast<uint4*>(col + 16 * (lane + 32 * i)) = make_uint4(hi | (mid << 16), lo, 0u, 0u);
-          reinterpret_cast<int*>(col + 4096)[lane + 32 * i] = t.len - t.n + c * nt + (tk[i] & 0xffff);
-        }
-        fence_proxy_async_smem();
-        warp_arrive(c_full(cs), lane);
+    // The chunk after (n, t, c) of this CTA; false at the end.
+    int n = 0, u = tile_of(0, cta, grid, units);
+    WTile t = tile_at(p, tab, u);
+    int c = t.c0 - 1;
+    auto advance = [&]() -> bool {
+      ++c;
+      while (c >= t.c1) {
+        u = tile_of(++n, cta, grid, units);
+        if (u < 0) return false;
+        t = tile_at(p, tab, u, t.s);
+        c = t.c0;
       }
+      return true;
+    };
+    float v[4];
+    auto fetch = [&]() {
+      const long long row0 = static_cast<long long>(t.h) * grp * p.c.total + t.q0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = tk[i] < t.rows - c * nt ? src[i][row0 + c * nt + tk[i]] : INFINITY;
+    };
+    bool more = advance(), ok = true;
+    if (more) fetch();
+    int nq = 0;
+    for (; more; ++nq) {
+      const int qs = nq % qst;
+      int go = 1;
+      if (lane == 0) {
+        go = wait_bar(q_empty(qs), ((nq / qst) & 1) ^ 1u, wc);
+        if (go) {
+          mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(nt * grp) * 128u * L::kHalves);
+          for (int hf = 0; hf < L::kHalves; ++hf)
+            tma_load_4d(ring_q + qs * q_bytes + hf * q_half, &tm_q, 64 * hf, 0, t.h, t.q0 + c * nt, q_full(qs));
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = -v[i] * p.inv_scale;
+        if (x[i] == INFINITY) x[i] = -INFINITY;
+      }
+      more = advance();
+      if (more) fetch();
+      uint8_t* const col = smem + L::kCol + qs * 4096;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // x = hi + mid + lo, each a rounding to bf16 of what the ones before leave.
+        const uint32_t hi = pack_bf16x2(x[i], 0.f) & 0xffffu;
+        float rest = x[i] - __uint_as_float(hi << 16);
+        if (x[i] == -INFINITY) rest = 0.f;
+        const uint32_t mid = pack_bf16x2(rest, 0.f) & 0xffffu;
+        const uint32_t lo = pack_bf16x2(rest - __uint_as_float(mid << 16), 0.f) & 0xffffu;
+        *reinterpret_cast<uint4*>(col + 16 * (lane + 32 * i)) = make_uint4(hi | (mid << 16), lo, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(q_full(qs), lane);
     }
-    if (lane == 0 && !ok) {  // this warp's copies (chunks mine − 1, mine − 3, …) have to land
+    if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
       const uint64_t t0 = globaltimer_ns();
-      for (int c = mine - 1; c >= 0 && c > mine - 1 - qst; c -= 2)
-        while (!mbar_try_wait(q_full(c % qst), (c / qst) & 1u))
+      for (int i = max(0, nq - qst); i < nq; ++i)
+        while (!mbar_try_wait(q_full(i % qst), (i / qst) & 1u))
           if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
   } else {
     // =============================================================== sums
-    const int w = ((warp - 4) >> 2) & 1, set = (warp - 4) >> 3;  // half of the tile; parity of the chunks
-    const int row = 128 * w + (warp & 3) * 32 + lane;            // key of the tile
+    const int w = (warp - 4) >> 2;                     // half of the tile
+    const int row = 128 * w + (warp & 3) * 32 + lane;  // key of the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2);
-    float* const other = reinterpret_cast<float*>(smem + L::kSet);
     // The weight gathered so far by this thread's key of tile t: where it is, and
     // the load, issued a tile ahead (under a full memory pipe it takes as long as a
     // tile of few rows).
@@ -373,7 +369,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         }
       }
     };
-    int nq = 0, joins = 0;
+    int nq = 0;
     bool ok = true;
     int u = tile_of(0, cta, grid, units);
     WTile t = tile_at(p, tab, u), t_next = t;
@@ -388,80 +384,71 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       }
       const int key = t.j0 + row;
       const bool live = t.j0 + 128 * w + (warp & 3) * 32 < t.len;  // this warp has a key
-      const int chunks = t.c1 - t.c0;
-      // The one set that has a part of it writes the tile: with several chunks the
-      // even one, after the odd one's sums.
-      const bool writes = chunks == 1 ? (nq & 1) == set : set == 0;
       float total = 0.f;
       for (int c = t.c0; c < t.c1; ++c, ++nq) {
-        if ((nq & 1) != set) continue;
-        const int cs = nq % kColSlots;
-        const int tok0 = c * nt, valid = min(nt, t.rows - tok0) * grp;
+        const int buf = nq & 1, tok0 = c * nt, valid = min(nt, t.rows - tok0) * grp;
         // No mask where the chunk's first row sees the last key of this half.
         const bool masked = min(t.j0 + 128 * w + 127, t.len - 1) > t.len - t.n + tok0;
-        bool got = wait_bar_cold(s_full(w, set), (nq >> 1) & 1, wc);
-        if (masked) got = got && wait_bar_cold(c_full(cs), (nq / kColSlots) & 1, wc);
+        const bool got = wait_bar_cold(s_full(w, buf), (nq >> 1) & 1, wc);
         if (__any_sync(0xffffffffu, !got)) { ok = false; break; }
         tc_fence_after();
-        const int* const lim = reinterpret_cast<const int*>(smem + L::kCol + cs * L::kColBytes + 4096);
-        const uint32_t tS = tmem + 256 * set + 128 * w + lane_off;
+        const uint32_t tS = tmem + 256 * buf + 128 * w + lane_off;
+        uint32_t x[128];
+        auto load = [&](int i) { tmem_ld32(tS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i])); };
+        auto loaded = [&](int i) { reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i])); };
         uint64_t acc[2] = {0, 0};
         // 2^(scale·log2 e·(s − LSE/scale)) over 32 columns.
-        auto group = [&](int cc, uint32_t(&x)[32]) {
-          if (cc + 32 <= valid && !masked) {
+        auto sum_all = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a, b;
-              unpack2(fmul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2), a, b);
-              acc[i & 1] = fadd2(acc[i & 1], pack2(ex2_mufu(a), ex2_mufu(b)));
-            }
-          } else {
-            // Columns without a row may hold anything: nothing of them is added.
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float a = ex2_mufu(__uint_as_float(x[i]) * p.scale_log2);
-              sum += (cc + i >= valid || (masked && key > lim[cc + i])) ? 0.f : a;
-            }
-            acc[0] = fadd2(acc[0], pack2(sum, 0.f));
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack2(fmul2(pack2(__uint_as_float(x[i0 + 2 * i]), __uint_as_float(x[i0 + 2 * i + 1])), sc2), a, b);
+            acc[i & 1] = fadd2(acc[i & 1], pack2(ex2_mufu(a), ex2_mufu(b)));
           }
         };
-        if (live) {
+        if (live && valid == 128 && !masked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load(i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) loaded(i);
+          tc_fence_before();
+          warp_arrive(s_free(w, buf), lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum_all(32 * i);
+        } else {
+          if (live) {
+            // Columns without a row may hold anything: nothing of them is added.
+            // Column i belongs to row tok0 + i / group, which sees slots up to
+            // len − n + its number; so the first column that sees this key is
+            const int first = masked ? max(0, min(key - (t.len - t.n) - tok0, 128)) * grp : 0;
 #pragma unroll 1
-          for (int cc = 0; cc < valid; cc += 32) {
-            uint32_t x[32];
-            tmem_ld32(tS + cc, x);
-            tmem_wait_ld();
-            reg_fence32(x);
-            group(cc, x);
+            for (int cc = 0; cc < valid; cc += 32) {
+              tmem_ld32(tS + cc, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+              tmem_wait_ld();
+              loaded(0);
+              if (cc + 32 <= valid && !masked) {
+                sum_all(0);
+              } else {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float a = ex2_mufu(__uint_as_float(x[i]) * p.scale_log2);
+                  sum += cc + i < valid && cc + i >= first ? a : 0.f;
+                }
+                acc[0] = fadd2(acc[0], pack2(sum, 0.f));
+              }
+            }
           }
+          tc_fence_before();
+          warp_arrive(s_free(w, buf), lane);
         }
         float a0, a1;
         unpack2(fadd2(acc[0], acc[1]), a0, a1);
         total += a0 + a1;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(s_free(w, set));
-          mbar_arrive(c_empty(cs));
-        }
       }
       if (!ok) break;
-      if (chunks > 1) {
-        if (set == 1) {
-          const bool got = wait_bar_cold(x_empty, (joins & 1) ^ 1u, wc);
-          if (__any_sync(0xffffffffu, !got)) break;
-          other[row] = total;
-          warp_arrive(x_full, lane);
-        } else {
-          const bool got = wait_bar_cold(x_full, joins & 1, wc);
-          if (__any_sync(0xffffffffu, !got)) break;
-          total += other[row];
-          warp_arrive(x_empty, lane);
-        }
-        ++joins;
-      }
-      if (writes && at >= 0) p.out[at] = start + total;
+      if (at >= 0) p.out[at] = start + total;
     }
   }
 
