@@ -72,44 +72,59 @@ class NewTokens(ctypes.Structure):
 # The structs as bytes in native layout: filled in one call, where a ctypes
 # structure takes one per field (a decoding step is short enough to notice).
 _CACHE = struct.Struct("@N2P6q4P6i")
-_TOKENS = struct.Struct("@N3P6qP3i")
-assert _CACHE.size == ctypes.sizeof(Cache) and _TOKENS.size <= ctypes.sizeof(NewTokens)
-_TOKENS_PAD = b"\0" * (ctypes.sizeof(NewTokens) - _TOKENS.size)
+_TOKENS = struct.Struct("@N3P6qP3i0P")  # (0P: padded to a pointer's alignment, as in C)
+_TOKENS_SIZE = _TOKENS.size
+assert _CACHE.size == ctypes.sizeof(Cache) and _TOKENS_SIZE == ctypes.sizeof(NewTokens)
 
 
-def _refuse(name, t, dtype, dims, dev, contiguous):
-    """The reason why _need refused t."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dims or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
+# Checks are written to cost little when they pass (a decoding step's kernels take
+# ~10 us): one call a tensor, which returns its address; the shape comes with it, so
+# that unpacking it checks the number of dimensions.
+
+
+def _refuse(name, t, dtype, dev, contiguous):
+    """The reason why _need or _rows refused t."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, not {type(t).__name__}")
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     raise ValueError(f"{name} must be contiguous" if contiguous else f"{name} must have a contiguous last dimension")
 
 
-def _need(name, t, dtype, dims, dev):
-    """t is a contiguous tensor of the type on CUDA device dev; its address."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.get_device() != dev or \
-            not t.is_contiguous():
-        _refuse(name, t, dtype, dims, dev, True)
-    return t.data_ptr()
+def _need(name, t, dtype, dev):
+    """Address of t, a contiguous tensor of the type on CUDA device dev."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, dtype, dev, True)
 
 
-def _rows(name, t, dims, dev):
-    """t is a bf16 tensor on CUDA device dev whose last dimension is contiguous:
-    its address, and the element strides of the others for the library (0: dense).
-    The stride of a dimension of one entry means nothing; the dense one stands for it."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != dims or t.get_device() != dev:
-        _refuse(name, t, _BF16, dims, dev, False)
-    if t.is_contiguous():
-        return t.data_ptr(), (0, 0, 0) if dims == 4 else (0, 0)
-    if t.stride(-1) != 1:
-        _refuse(name, t, _BF16, dims, dev, False)
-    return t.data_ptr(), _strides(t)
+def _rows(name, t, dev):
+    """Address of t, a bf16 tensor on CUDA device dev whose last dimension is
+    contiguous, and the element strides of the others for the library: (0, …) for
+    dense ones."""
+    try:
+        if t.dtype is _BF16 and t.get_device() == dev:
+            if t.is_contiguous():
+                return t.data_ptr(), _DENSE[t.dim()]
+            if t.stride(-1) == 1:
+                return t.data_ptr(), _strides(t)
+    except AttributeError:
+        pass
+    _refuse(name, t, _BF16, dev, False)
+
+
+_DENSE = tuple((0,) * max(0, n - 1) for n in range(65))
 
 
 def _strides(t):
+    """The stride of a dimension of one entry means nothing; the dense one stands for it."""
     if t.is_contiguous():
-        return (0,) * (t.dim() - 1)
+        return _DENSE[t.dim()]
     shape, stride, out, dense = t.shape, t.stride(), [], t.shape[-1]
     for i in range(t.dim() - 2, -1, -1):
         if shape[i] > 1 and stride[i] < shape[-1]:
@@ -119,45 +134,51 @@ def _strides(t):
     return tuple(reversed(out))
 
 
-def _device(t):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("the cache must be CUDA tensors")
-    return t.get_device()
+def _shape(name, t, n):
+    """t's n sizes."""
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a {n}-D tensor")
+    return t.shape
 
 
 def _seq(name, t, n, dev):
-    ptr = _need(name, t, _I32, 1, dev)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries")
+    ptr = _need(name, t, _I32, dev)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have {n} entries, not shape {tuple(t.shape)}")
     return ptr
 
 
 def _per_slot(name, t, dtype, shape, dev):
-    ptr = _need(name, t, dtype, 3, dev)
+    ptr = _need(name, t, dtype, dev)
     if t.shape != shape:
-        raise ValueError(f"{name} must be [n_pages, H_kv, page_size] = {tuple(shape)}")
+        raise ValueError(f"{name} must be [n_pages, H_kv, page_size] = {tuple(shape)}, not {tuple(t.shape)}")
     return ptr
+
+
+def _device(name, t):
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
 def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
     """attn_cache of checked tensors; (bytes, H_kv, d, n_seq).  What an operator does
     not use is None."""
-    table = _need("block_table", block_table, _I32, 2, dev)
-    n_seq, max_blocks = block_table.shape
-    kp = vp = wp = pp = lp = 0
-    ks = vs = (0, 0, 0)
+    table = _need("block_table", block_table, _I32, dev)
+    n_seq, max_blocks = _shape("block_table", block_table, 2)
+    vp = wp = pp = lp = 0
+    vs = (0, 0, 0)
     if k is not None:
-        kp, ks = _rows("k_cache", k, 4, dev)
-        n_pages, page_size, hkv, d = k.shape
+        kp, ks = _rows("k_cache", k, dev)
+        n_pages, page_size, hkv, d = _shape("k_cache", k, 4)
         if v is not None:
-            vp, vs = _rows("v_cache", v, 4, dev)
+            vp, vs = _rows("v_cache", v, dev)
             if v.shape != k.shape:
                 raise ValueError(f"v_cache {tuple(v.shape)} must be shaped like k_cache {tuple(k.shape)}")
     else:
-        if weights.dim() != 3:
-            _refuse("weights", weights, _F32, 3, dev, True)
-        n_pages, hkv, page_size = weights.shape
-        d = 0
+        kp, ks, d = 0, vs, 0
+        n_pages, hkv, page_size = _shape("weights", weights, 3)
     if weights is not None:
         wp = _per_slot("weights", weights, _F32, (n_pages, hkv, page_size), dev)
     if positions is not None:
@@ -170,38 +191,42 @@ def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
 
 def _pack_tokens(q, k, v, cu, total, max_seqlen, H):
     """attn_new_tokens from (address, strides) pairs."""
-    return _TOKENS.pack(ctypes.sizeof(NewTokens), q[0], k[0], v[0], *q[1], *k[1], *v[1], cu, total, max_seqlen,
-                        H) + _TOKENS_PAD
+    return _TOKENS.pack(_TOKENS_SIZE, q[0], k[0], v[0], *q[1], *k[1], *v[1], cu, total, max_seqlen, H)
 
 
 _NONE = (0, (0, 0))
 
 
 def _new_kv(k_new, v_new, hkv, d, dev):
-    kn, vn = _rows("k_new", k_new, 3, dev), _rows("v_new", v_new, 3, dev)
-    if k_new.shape != v_new.shape or k_new.shape[1] != hkv or k_new.shape[2] != d:
+    kn, vn = _rows("k_new", k_new, dev), _rows("v_new", v_new, dev)
+    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.shape[1:] != (hkv, d):
         raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be [total, {hkv}, {d}]")
     return kn, vn
 
 
+def _elsewhere(dev, stream):
+    """Whether a call has to switch device or stream first."""
+    if stream is None:
+        return torch._C._cuda_getDevice() != dev
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return True
+
+
 @contextlib.contextmanager
 def _switched(dev, stream):
+    """The tensors' device is current, and so is the stream: what is allocated inside
+    belongs to it."""
     with torch.cuda.device(dev):
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
+            yield
         else:
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                yield
 
 
-def _on(dev, stream):
-    """Context in which the tensors' device is current and so is the stream (what is
-    allocated inside belongs to it); gives the stream's handle."""
-    if stream is None and torch._C._cuda_getDevice() == dev:
-        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(dev))
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
-    return _switched(dev, stream)
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def workspace_size(H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
@@ -225,13 +250,17 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     lse [H, total] fp32); rows that belong to no sequence are not written.
     ``workspace``: a uint8 tensor of workspace_size(...) bytes, else allocated.
     """
-    dev = _device(k_cache)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
+                                  max_seqlen_q, parents, scale, out, lse, workspace, None, options)
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, None, None)
-    qr = _rows("q", q, 3, dev)
+    qr = _rows("q", q, dev)
     kn, vn = _new_kv(k_new, v_new, hkv, d, dev)
-    total, H, dq = q.shape
+    total, H, dq = _shape("q", q, 3)
     if k_new.shape[0] != total or dq != d or H % hkv != 0:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k_new {tuple(k_new.shape)}, cache heads {hkv}, d {d}")
     cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
@@ -239,32 +268,31 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is not None:
-        _need("out", out, _BF16, 3, dev)
+        _need("out", out, _BF16, dev)
         if out.shape != q.shape:
             raise ValueError("out must be shaped like q")
     if lse is not None:
-        _need("lse", lse, _F32, 2, dev)
-        if tuple(lse.shape) != (H, total):
+        _need("lse", lse, _F32, dev)
+        if lse.shape != (H, total):
             raise ValueError("lse must be [H, total]")
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     max_seqlen_q = int(max_seqlen_q)
-    with _on(dev, stream) as s:
-        device = k_cache.device
-        if out is None:
-            out = torch.empty((total, H, d), dtype=_BF16, device=device)
-        if lse is None:
-            lse = torch.empty((H, total), dtype=_F32, device=device)
-        if total == 0:
-            return out, lse
-        if workspace is None:
-            workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
-        if options is not None:
-            options.struct_size = ctypes.sizeof(attn.Options)
-        rc = attn.lib().attn_fwd_cache(c, _pack_tokens(qr, kn, vn, cu, total, max_seqlen_q, H), par, scale,
-                                       out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(),
-                                       ctypes.byref(options) if options is not None else None, s)
+    device = k_cache.device
+    if out is None:
+        out = torch.empty((total, H, d), dtype=_BF16, device=device)
+    if lse is None:
+        lse = torch.empty((H, total), dtype=_F32, device=device)
+    if total == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
+    if options is not None:
+        options.struct_size = ctypes.sizeof(attn.Options)
+    rc = attn.lib().attn_fwd_cache(c, _pack_tokens(qr, kn, vn, cu, total, max_seqlen_q, H), par, scale,
+                                   out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(),
+                                   ctypes.byref(options) if options is not None else None, _stream(dev))
     if rc:
         attn._check(rc)
     return out, lse
@@ -280,7 +308,11 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     of k_new and v_new, cu_new then counts entries of it: the accepted path of a
     drafted tree.
     """
-    dev = _device(k_cache)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, rows, weights, positions,
+                                seq_pos)
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, weights, positions)
@@ -288,12 +320,12 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     cu = _seq("cu_new", cu_new, n_seq + 1, dev)
     total, n_rows, rp = k_new.shape[0], 0, None
     if rows is not None:
-        rp, n_rows = _need("rows", rows, _I32, 1, dev), rows.shape[0]
+        rp = _need("rows", rows, _I32, dev)
+        (n_rows,) = _shape("rows", rows, 1)
     sp = None if seq_pos is None else _seq("seq_pos", seq_pos, n_seq, dev)
     if total == 0 or (rows is not None and n_rows == 0):
         return
-    with _on(dev, stream) as s:
-        rc = attn.lib().attn_cache_append(c, _pack_tokens(_NONE, kn, vn, cu, total, 0, 0), rp, n_rows, sp, s)
+    rc = attn.lib().attn_cache_append(c, _pack_tokens(_NONE, kn, vn, cu, total, 0, 0), rp, n_rows, sp, _stream(dev))
     if rc:
         attn._check(rc)
 
@@ -309,7 +341,10 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     (out is then needed).  Any number of queries: a decoded token, the last window
     of a prompt or the whole of it.
     """
-    dev = _device(k_cache)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, weights, scale, out)
     if seq_lens is None:
         raise ValueError("seq_lens is needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, None, block_table, seq_lens, weights, None)
@@ -317,23 +352,21 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
         out = weights
     if out is None:
         raise ValueError("one of weights and out is needed")
-    n_pages, page_size = k_cache.shape[0], k_cache.shape[1]
-    op = _per_slot("out", out, _F32, (n_pages, hkv, page_size), dev)
-    qr = _rows("q", q, 3, dev)
-    total, H, dq = q.shape
+    op = _per_slot("out", out, _F32, (k_cache.shape[0], hkv, k_cache.shape[1]), dev)
+    qr = _rows("q", q, dev)
+    total, H, dq = _shape("q", q, 3)
     if dq != d or H % hkv != 0:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, cache heads {hkv}, d {d}")
     if total == 0:
         raise ValueError("q has no rows")
-    lp = _need("lse", lse, _F32, 2, dev)
-    if tuple(lse.shape) != (H, total):
+    lp = _need("lse", lse, _F32, dev)
+    if lse.shape != (H, total):
         raise ValueError(f"lse must be [H, total] = {(H, total)}")
     cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _on(dev, stream) as s:
-        rc = attn.lib().attn_cache_weights(c, _pack_tokens(qr, _NONE, _NONE, cu, total, int(max_seqlen_q), H), lp,
-                                           scale, op, s)
+    rc = attn.lib().attn_cache_weights(c, _pack_tokens(qr, _NONE, _NONE, cu, total, int(max_seqlen_q), H), lp,
+                                       scale, op, _stream(dev))
     if rc:
         attn._check(rc)
     return out
@@ -349,7 +382,10 @@ def cache_select(weights, block_table, seq_lens, budget: int, recent: int = 0, p
     behind the last.  Tokens that stay below slot ``budget`` keep their slot; the
     others fill the slots that become free, both ascending.
     """
-    dev = _device(weights)
+    dev = _device("weights", weights)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_select(weights, block_table, seq_lens, budget, recent, positions, seq_pos, kept)
     if seq_lens is None:
         raise ValueError("seq_lens is needed")
     c, hkv, _, n_seq = _pack_cache(dev, None, None, block_table, seq_lens, weights, positions)
@@ -358,14 +394,13 @@ def cache_select(weights, block_table, seq_lens, budget: int, recent: int = 0, p
     sp = None if seq_pos is None else _seq("seq_pos", seq_pos, n_seq, dev)
     budget, recent = int(budget), int(recent)
     if kept is not None:
-        _need("kept", kept, _I32, 3, dev)
-        if tuple(kept.shape) != (n_seq, hkv, budget):
+        _need("kept", kept, _I32, dev)
+        if kept.shape != (n_seq, hkv, budget):
             raise ValueError(f"kept must be [n_seq, H_kv, budget] = {(n_seq, hkv, budget)}")
-    with _on(dev, stream) as s:
-        if kept is None:
-            kept = torch.empty((n_seq, hkv, max(budget, 0)), dtype=_I32, device=weights.device)
-        # (an empty tensor has no address: the library answers for the budget)
-        rc = attn.lib().attn_cache_select(c, sp, budget, recent, kept.data_ptr() or 16, s)
+    if kept is None:
+        kept = torch.empty((n_seq, hkv, max(budget, 0)), dtype=_I32, device=weights.device)
+    # (an empty tensor has no address: the library answers for the budget)
+    rc = attn.lib().attn_cache_select(c, sp, budget, recent, kept.data_ptr() or 16, _stream(dev))
     if rc:
         attn._check(rc)
     return kept
@@ -375,15 +410,17 @@ def cache_compact(kept, k_cache, v_cache, block_table, weights=None, positions=N
     """Move the tokens that cache_select kept, in place: for every kept[s, h, i] >=
     budget (= kept.shape[2]) the key, value, weight and position of that slot go to
     slot i.  Set seq_lens to min(seq_lens, budget) afterwards."""
-    dev = _device(k_cache)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_compact(kept, k_cache, v_cache, block_table, weights, positions)
     if v_cache is None:
         raise ValueError("v_cache is needed")
     c, hkv, _, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, None, weights, positions)
-    kp = _need("kept", kept, _I32, 3, dev)
-    if kept.shape[0] != n_seq or kept.shape[1] != hkv or kept.shape[2] < 1:
+    kp = _need("kept", kept, _I32, dev)
+    if kept.dim() != 3 or kept.shape[:2] != (n_seq, hkv) or kept.shape[2] < 1:
         raise ValueError(f"kept must be [n_seq, H_kv, budget], not {tuple(kept.shape)}")
-    with _on(dev, stream) as s:
-        rc = attn.lib().attn_cache_compact(c, kp, kept.shape[2], s)
+    rc = attn.lib().attn_cache_compact(c, kp, kept.shape[2], _stream(dev))
     if rc:
         attn._check(rc)
 

@@ -127,21 +127,29 @@ int fail(cudaError_t e, const char* what) { return e == cudaSuccess ? ATTN_OK : 
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Tokens and rows of a row tile: as many whole tokens as 128 rows hold.
+// Tokens of a row tile: as many whole ones as 128 rows hold.
 int tile_tokens(int group, int max_new) {
   const int nt = 128 / group;
   return nt < max_new ? nt : max_new;
 }
 
-struct Workspace {
+// The attention kernel's row tiles, and its workspace: the sequences' table, then a
+// part (maximum and sum, output) for each end of each CTA's range.
+struct Tiles {
+  int nt, per_cta, ntt, rows, max_ctas;
   size_t ml, o, bytes;
 };
-Workspace workspace_of(int rows, int d) {
-  Workspace w;
-  w.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
-  w.o = w.ml + up256(2ull * attn::kCacheMaxCtas * rows * sizeof(float2));
-  w.bytes = w.o + 2ull * attn::kCacheMaxCtas * rows * d * sizeof(float);
-  return w;
+Tiles tiles_of(int group, int max_new, int d) {
+  Tiles t;
+  t.nt = tile_tokens(group, max_new);
+  t.per_cta = t.nt < max_new ? 2 : 1;
+  t.ntt = t.per_cta * t.nt < max_new ? t.per_cta * t.nt : max_new;
+  t.rows = t.ntt * group;
+  t.max_ctas = attn::kCacheMaxCtas / t.per_cta;
+  t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
+  t.o = t.ml + up256(2ull * t.max_ctas * t.rows * sizeof(float2));
+  t.bytes = t.o + 2ull * t.max_ctas * t.rows * d * sizeof(float);
+  return t;
 }
 
 }  // namespace
@@ -152,8 +160,7 @@ size_t attn_fwd_cache_workspace_size(int H, int num_kv_heads, int max_seqlen, in
   if (H < 1 || num_kv_heads < 1 || H % num_kv_heads != 0 || H / num_kv_heads > 128 || max_seqlen < 1 ||
       max_seqlen > ATTN_CACHE_MAX_NEW || (d != 64 && d != 128))
     return 0;
-  const int group = H / num_kv_heads;
-  return workspace_of(tile_tokens(group, max_seqlen) * group, d).bytes;
+  return tiles_of(H / num_kv_heads, max_seqlen, d).bytes;
 }
 
 int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int* parents, float scale, void* o,
@@ -167,10 +174,10 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
   if (rc != ATTN_OK || (rc = check_tokens(x, true, &c)) != ATTN_OK) return rc;
   if (x->k == nullptr || x->v == nullptr || c.lens == nullptr) return ATTN_ERR_NULL;
   if (x->max_seqlen > ATTN_CACHE_MAX_NEW) return ATTN_ERR_SHAPE;
-  const int nt = tile_tokens(c.group, c.max_new), rows = nt * c.group;
-  const long long tiles = (c.max_new + nt - 1) / nt;
+  const Tiles w = tiles_of(c.group, c.max_new, c.d);
+  const long long tiles = (c.max_new + w.ntt - 1) / w.ntt;
   // Units and rows of the two kernels' grids.
-  if (tiles * c.n_seq * c.hkv > kMaxInt / (c.cap / 128 + 3) || tiles * c.n_seq * c.hkv * rows > kMaxInt ||
+  if (tiles * c.n_seq * c.hkv > kMaxInt / (c.cap / 128 + 3) || tiles * c.n_seq * c.hkv * w.rows > kMaxInt ||
       static_cast<long long>(x->H) * c.total > kMaxInt)
     return ATTN_ERR_SHAPE;
   if ((rc = check_scale(scale)) != ATTN_OK) return rc;
@@ -183,7 +190,6 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
   if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(parents, 4))
     return ATTN_ERR_ALIGN;
   if ((rc = check_options(opts, &a.p.timeout_ns, &a.p.test_flags)) != ATTN_OK) return rc;
-  const Workspace w = workspace_of(rows, c.d);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.bytes) return ATTN_ERR_WORKSPACE;
   int sms = 0;
   if ((rc = attn::usable_device(&a.device, &a.p.status, &sms)) != ATTN_OK) return rc;
@@ -195,16 +201,19 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
   a.p.ws_table = reinterpret_cast<int*>(ws);
   a.p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
-  a.p.rows = rows;
-  a.p.nt = nt;
+  a.p.rows = w.rows;
+  a.p.nt = w.nt;
+  a.p.ntt = w.ntt;
+  a.tiles = w.per_cta;
   a.p.piece = piece_of(c.page_size);
   a.p.scale_log2 = scale * 1.4426950408889634f;
-  a.grid = 2 * sms < attn::kCacheMaxCtas ? 2 * sms : attn::kCacheMaxCtas;
+  const int ctas = 2 * sms / w.per_cta;
+  a.grid = ctas < w.max_ctas ? ctas : w.max_ctas;
   a.stream = stream;
   const long long new_dims[4] = {c.d, c.hkv, c.total, 1};
   const int new_box[4] = {64, 1, 16, 1};
   const long long kn[3] = {ks[1], ks[0], ks[0]}, vn[3] = {vs[1], vs[0], vs[0]};
-  if ((rc = encode_queries(&a.q, x, c, qs, nt)) != ATTN_OK || (rc = encode_pages(&a.k, c.k, c, c.k_st, a.p.piece)) != ATTN_OK ||
+  if ((rc = encode_queries(&a.q, x, c, qs, w.nt)) != ATTN_OK || (rc = encode_pages(&a.k, c.k, c, c.k_st, a.p.piece)) != ATTN_OK ||
       (rc = encode_pages(&a.v, c.v, c, c.v_st, a.p.piece)) != ATTN_OK ||
       (rc = attn::encode_bf16_4d(&a.kn, x->k, new_dims, kn, new_box)) != ATTN_OK ||
       (rc = attn::encode_bf16_4d(&a.vn, x->v, new_dims, vn, new_box)) != ATTN_OK)

@@ -17,13 +17,22 @@
 // second kernel joins the parts of a tile in order.  The ranges follow from the
 // lengths on the device: the host reads nothing back.
 //
-// Two CTAs share an SM (256 TMEM columns and under half of its shared memory
-// each).  Warps: 0 loads (TMA boxes of a page's rows, one lane a box), 1 issues
-// the MMAs, 2-5 compute the softmax, one thread a row (TMEM lane).  Two CTAs
-// rather than one deep pipeline: one CTA's copies and MMAs run under the
-// other's exponentials, with K and V of one block each in flight.
+// Row tiles: MT = 1, up to 128 rows a sequence and key head: two CTAs share an SM (256
+// TMEM columns and under half of its shared memory each), K and V of one block each
+// (d = 64: two) in flight, one CTA's copies and MMAs under the other's exponentials.
+// MT = 2, more rows: one CTA an SM works on two tiles of 128 rows at once, which share
+// every block of K and V, two blocks in flight, one tile's MMAs under the other's
+// exponentials.  (With MT = 1 such a call waits for copies: a block took ~4200 cycles a
+// CTA, of which the copies' latency, 2500, showed almost whole.)  One thread issues
+// P·V and the next S of one tile, then those of the other, which keeps the tiles half
+// a period apart; an issuer a tile let them fall into step, both at the tensor core,
+// then both at the exponentials (4700 cycles a block).
 //
-// d = 128: TMEM S [0,128), with P (bf16) over its first half; O [128,256).
+// Warps: 0 loads (TMA boxes of a page's rows, one lane a box), 1 issues the MMAs, and
+// four per tile compute its softmax, one thread a row (TMEM lane).
+//
+// TMEM columns of a tile (256·tile + …):
+// d = 128: S [0,128), with P (bf16) over its first half; O [128,256).
 //          S(g+1) is issued once P(g)·V has completed.
 // d = 64:  S [0,128), P [128,192), O [192,256): S(g+1) is issued once the softmax
 //          has read S(g).
@@ -34,10 +43,12 @@
 #include "attn_fwd_kernel.cuh"
 #include "cache_device.cuh"
 
+#include <type_traits>
+
 namespace attn {
 namespace {
 
-constexpr int kThreadsCA = 192;
+constexpr int kWideRows = 64;  // parts of more rows lie chunk by chunk, [D/4][rows][4]
 constexpr float kTau = 8.0f;  // log2: a row's reference maximum moves when exceeded by more (p ≤ 2^8)
 
 // The key blocks of one sequence: `nfull` full ones, then the cached tail and the
@@ -60,7 +71,8 @@ __device__ __forceinline__ KeyPlan key_plan(const CacheAttnParams& p, int s) {
   k.db = k.nfull + (joined ? 0 : 1);
   return k;
 }
-__device__ __forceinline__ int row_tiles(const CacheAttnParams& p, int n) { return (n + p.nt - 1) / p.nt; }
+// Row tiles of a CTA (MT · nt tokens) that n new tokens make.
+__device__ __forceinline__ int row_tiles(const CacheAttnParams& p, int n) { return (n + p.ntt - 1) / p.ntt; }
 
 __device__ __forceinline__ int units_of(const CacheAttnParams& p, int s) {
   const KeyPlan k = key_plan(p, s);
@@ -92,27 +104,29 @@ __device__ __forceinline__ int cached_in(const KeyPlan& k, int b) {
   return b < k.nfull ? 128 : (b == k.nfull ? k.tail : 0);
 }
 
-template <int D>
+template <int D, int MT>
 struct CL {
+  static constexpr int kThreads = MT == 1 ? 192 : 384;
+  static constexpr int kSoftmax0 = MT == 1 ? 2 : 4;  // first softmax warp
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = 128u * D * 2;  // 128 rows of Q, K or V: [half][128 rows][128 B]
-  static constexpr int kStages = D == 128 ? 1 : 2;
-  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
-  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full, s_free, p_full, pv_done, done
-  static constexpr int kNumBars = 2 + 4 * kStages + 5;
+  static constexpr int kStages = MT == 2 ? (D == 128 ? 2 : 3) : (D == 128 ? 1 : 2);
+  static constexpr uint32_t kQ = 0, kK = MT * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
+  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], then a tile's s_full, s_free, p_full, pv_done; done
+  static constexpr int kNumBars = 3 + 4 * kStages + 4 * MT;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;       // TMEM base, abort flag
   static constexpr uint32_t kSums = kMisc + 8;                 // one int per warp
-  static constexpr uint32_t kTable = (kSums + 32 + 15) & ~15u;
+  static constexpr uint32_t kTable = (kSums + 48 + 15) & ~15u;
   static constexpr uint32_t kBytes = kTable + 1024;            // + alignment; the table comes on top
   static constexpr uint32_t kColS = 0, kColP = D == 128 ? 0 : 128, kColO = D == 128 ? 128 : 192;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsCA, 2)
+template <int D, int MT>
+__global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
                       const __grid_constant__ CUtensorMap tm_vn, const CacheAttnParams p) {
-  using L = CL<D>;
+  using L = CL<D, MT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -124,8 +138,11 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
   auto v_full = [&](int s) { return bars + 8u * (2 + 2 * L::kStages + s); };
   auto v_empty = [&](int s) { return bars + 8u * (2 + 3 * L::kStages + s); };
   constexpr uint32_t kB = 2 + 4 * L::kStages;
-  const uint32_t s_full = bars + 8u * kB, s_free = bars + 8u * (kB + 1), p_full = bars + 8u * (kB + 2);
-  const uint32_t pv_done = bars + 8u * (kB + 3), done = bars + 8u * (kB + 4);
+  auto s_full = [&](int i) { return bars + 8u * (kB + 4 * i); };
+  auto s_free = [&](int i) { return bars + 8u * (kB + 4 * i + 1); };
+  auto p_full = [&](int i) { return bars + 8u * (kB + 4 * i + 2); };
+  auto pv_done = [&](int i) { return bars + 8u * (kB + 4 * i + 3); };
+  const uint32_t done = bars + 8u * (kB + 4 * MT);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
@@ -135,7 +152,7 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
 
   // TMEM and barriers are set up while the lengths are on their way.
   if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_alloc(smem_u32(tmem_slot), 256 * MT);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -149,10 +166,12 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
       mbar_init(v_full(s), 1);
       mbar_init(v_empty(s), 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
-    mbar_init(p_full, 4);
-    mbar_init(pv_done, 1);
+    for (int i = 0; i < MT; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 4);
+      mbar_init(p_full(i), 4);
+      mbar_init(pv_done(i), 1);
+    }
     mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -168,11 +187,11 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
   tc_fence_after();
   const int units = tab[p.c.n_seq];
   if (cta == 0)
-    for (int i = threadIdx.x; i <= p.c.n_seq; i += kThreadsCA) p.ws_table[i] = tab[i];
+    for (int i = threadIdx.x; i <= p.c.n_seq; i += L::kThreads) p.ws_table[i] = tab[i];
   const int grid = min(static_cast<int>(gridDim.x), units);  // CTAs with work: each of them at least one unit
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= grid) {
-    if (warp == 0) tmem_dealloc(*tmem_slot, 256);
+    if (warp == 0) tmem_dealloc(*tmem_slot, 256 * MT);
     return;
   }
   const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
@@ -197,9 +216,11 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
       ok = waited(q_empty, (ns & 1) ^ 1u);
       if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.nt * p.c.group) * 128u * L::kHalves);
-        for (int hf = 0; hf < L::kHalves; ++hf)
-          tma_load_4d(base + L::kQ + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + sg.m * p.nt, q_full);
+        const int t0 = sg.m * p.ntt, tiles = MT == 2 && sg.k.n - t0 > p.nt ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * p.nt * p.c.group) * 128u * L::kHalves);
+        for (int i = 0; i < tiles; ++i)
+          for (int hf = 0; hf < L::kHalves; ++hf)
+            tma_load_4d(base + L::kQ + i * L::kTile + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + t0 + i * p.nt, q_full);
       }
       ++nq;
       const int nd = (sg.k.n + 15) >> 4;  // 16-row pieces of new keys
@@ -257,75 +278,99 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(128, 128, false);
       constexpr uint32_t idPV = idesc_bf16(128, D, true);
-      const uint64_t dQ = sdesc_kmajor_sw128(base + L::kQ);
-      const uint32_t tS = tmem + L::kColS, tP = tmem + L::kColP, tO = tmem + L::kColO;
-      int g = 0, ns = 0;
+      int g = 0, ns = 0;          // blocks and segments of the CTA
+      int e[MT] = {};             // blocks of each tile: fewer, where a segment has rows for the first tile only
+      bool before[MT] = {};       // the tile has a product of block g − 1 to come
+      bool before_first = false;  // which opens its segment
       bool ok = true;
-      // O (+)= P(n)·V; `first`: the block opens its segment.
-      auto issue_pv = [&](int n, bool first) -> bool {
-        const int st = n % L::kStages;
-        if (!wait_bar(v_full(st), (n / L::kStages) & 1, wc) || !wait_bar(p_full, n & 1, wc)) return false;
+      // O (+)= P·V of block g − 1 for a tile; `last`: no other tile needs its V.
+      auto issue_pv = [&](int i, bool last) -> bool {
+        const int st = (g - 1) % L::kStages;
+        if (!wait_bar(v_full(st), ((g - 1) / L::kStages) & 1, wc) || !wait_bar(p_full(i), (e[i] - 1) & 1, wc))
+          return false;
         tc_fence_after();
         const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
+        const uint32_t t = tmem + 256 * i;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tO, tP + kk * 8, dv + ((kk * 2048) >> 4), idPV, (!first || kk > 0) ? 1u : 0u);
-        mma_commit(pv_done);
-        mma_commit(v_empty(st));
+          mma_ts(t + L::kColO, t + L::kColP + kk * 8, dv + ((kk * 2048) >> 4), idPV, (!before_first || kk > 0) ? 1u : 0u);
+        mma_commit(pv_done(i));
+        if (last) mma_commit(v_empty(st));
         return true;
       };
-      bool prev_first = false;
+      auto issue_s = [&](int i) {
+        tc_fence_after();
+        const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ + i * L::kTile);
+        const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + (g % L::kStages) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + 256 * i + L::kColS, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full(i));
+      };
       for (int u = u0; u < u1 && ok; ++ns) {
         const Segment sg = segment_at(p, tab, u, u1);
         u += sg.b1 - sg.b0;
-        for (int b = sg.b0; b < sg.b1; ++b, ++g) {
+        const int tiles = MT == 2 && sg.k.n - sg.m * p.ntt > p.nt ? 2 : 1;
+        for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
           const int st = g % L::kStages;
-          if constexpr (D == 128) {
-            // P(g−1) lies over S: its product has to be done first.
-            if (g > 0) ok = issue_pv(g - 1, prev_first) && wait_bar(pv_done, (g - 1) & 1, wc);
-          } else {
-            if (g > 0) ok = wait_bar(s_free, (g - 1) & 1, wc);
-          }
-          if (ok && b == sg.b0) ok = wait_bar(q_full, ns & 1, wc);
-          ok = ok && wait_bar(k_full(st), (g / L::kStages) & 1, wc);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            mma_ss(tS, dQ + o, dk + o, idS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(s_full);
-          mma_commit(k_empty(st));
-          if (b == sg.b1 - 1) mma_commit(q_empty);
-          if constexpr (D == 64) {
-            if (g > 0) ok = issue_pv(g - 1, prev_first);
+          for (int i = 0; i < MT; ++i) {
+            const bool now = i < tiles;
+            const bool last_pv = i == MT - 1 || !before[MT - 1];
+            // d = 128: the last P lies over S, its product has to be done first.
+            if (D == 128 && before[i]) ok = ok && issue_pv(i, last_pv);
+            if (now && i == 0) {
+              if (b == sg.b0) ok = ok && wait_bar(q_full, ns & 1, wc);
+              ok = ok && wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+            }
+            if (now && e[i] > 0)
+              ok = ok && (D == 128 ? wait_bar(pv_done(i), (e[i] - 1) & 1, wc) : wait_bar(s_free(i), (e[i] - 1) & 1, wc));
             if (!ok) break;
+            if (now) {
+              issue_s(i);
+              if (i == tiles - 1) {
+                mma_commit(k_empty(st));
+                if (b == sg.b1 - 1) mma_commit(q_empty);
+              }
+            }
+            if (D == 64 && before[i]) ok = issue_pv(i, last_pv);
+            if (!ok) break;
+            before[i] = now;
+            if (now) ++e[i];
           }
-          prev_first = b == sg.b0;
+          before_first = b == sg.b0;
         }
       }
-      if (ok) issue_pv(g - 1, prev_first);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        if (before[i]) ok = ok && issue_pv(i, i == MT - 1 || !before[MT - 1]);
       mma_commit(done);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(done, 0))
         if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
-  } else {
+  } else if (warp >= L::kSoftmax0) {
     // ============================================================ softmax
+    const int tile = MT == 1 ? 0 : (warp - L::kSoftmax0) >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + L::kColS + lane_off, tP = tmem + L::kColP + lane_off, tO = tmem + L::kColO + lane_off;
+    const uint32_t t_base = tmem + 256 * tile + lane_off;
+    const uint32_t tS = t_base + L::kColS, tP = t_base + L::kColP, tO = t_base + L::kColO;
     const float sc = p.scale_log2;
     const uint64_t sc2 = pack2(sc, sc);
-    int g = 0;
+    int g = 0, e = 0;  // blocks of the CTA and of this tile, as the issuer counts them
     bool ok = true;
     for (int u = u0; u < u1 && ok;) {
       const Segment sg = segment_at(p, tab, u, u1);
       const bool first_of_cta = u == u0;
       u += sg.b1 - sg.b0;
-      const int t0 = sg.m * p.nt, n_rows = min(sg.k.n - t0, p.nt) * p.c.group;
+      const int t0 = sg.m * p.ntt + tile * p.nt, n_rows = min(sg.k.n - t0, p.nt) * p.c.group;
+      if (MT == 2 && n_rows <= 0) {
+        g += sg.b1 - sg.b0;
+        continue;
+      }
       const bool active = (warp & 3) * 32 < n_rows;
       float m_run = -INFINITY, l_run = 0.f;
       uint32_t anc[4] = {0u, 0u, 0u, 0u};  // the new tokens this row sees
@@ -359,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
       }
       auto block = [&](int b, auto mask_tag) -> bool {
         constexpr bool MASK = decltype(mask_tag)::value;
-        const bool got = wait_bar_cold(s_full, g & 1, wc);
+        const bool got = wait_bar_cold(s_full(tile), e & 1, wc);
         if (__any_sync(0xffffffffu, !got)) return false;
         tc_fence_after();
         uint32_t vis[4];
@@ -429,15 +474,15 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
             const float m_new = need ? mx : m_run;
             if (b > sg.b0) {
               const float alpha = need ? ex2_mufu(m_run - m_new) : 1.f;
-              if (!rescale_o<D>(pv_done, (g - 1) & 1, wc, tO, alpha)) return false;
+              if (!rescale_o<D>(pv_done(tile), (e - 1) & 1, wc, tO, alpha)) return false;
               l_run *= alpha;
             }
             m_run = m_new;
           }
           // ---- exponentials, P in bf16
           if constexpr (D == 64) {
-            if (g > 0) {  // P·V(g−1) has read P
-              const bool landed = wait_bar_cold(pv_done, (g - 1) & 1, wc);
+            if (e > 0) {  // the last P·V has read P
+              const bool landed = wait_bar_cold(pv_done(tile), (e - 1) & 1, wc);
               if (__any_sync(0xffffffffu, !landed)) return false;
               tc_fence_after();
             }
@@ -480,15 +525,15 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
           tmem_wait_st();
         }
         tc_fence_before();
-        if constexpr (D == 64) warp_arrive(s_free, lane);
-        warp_arrive(p_full, lane);
+        if constexpr (D == 64) warp_arrive(s_free(tile), lane);
+        warp_arrive(p_full(tile), lane);
         return true;
       };
-      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g)
+      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g, ++e)
         ok = b < sg.k.nfull ? block(b, std::false_type{}) : block(b, std::true_type{});
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      const bool landed = wait_bar_cold(pv_done, (g - 1) & 1, wc);
+      const bool landed = wait_bar_cold(pv_done(tile), (e - 1) & 1, wc);
       if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
       tc_fence_after();
       if (active) {
@@ -496,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
         const int grp = p.c.group, t = t0 + r / grp, hq = sg.h * grp + r % grp, H = p.c.hkv * grp;
         const long long token = sg.k.q0 + t;
         const int slot = 2 * cta + (first_of_cta ? 0 : 1);
-        const long long part = static_cast<long long>(slot) * p.rows + r;
+        const long long part = static_cast<long long>(slot) * p.rows + tile * p.nt * grp + r;
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -518,9 +563,18 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
                 dst[i] = w;
               }
             } else {
-              uint4* const dst = reinterpret_cast<uint4*>(p.ws_o + part * D + 32 * c);
+              // Row by row, or (many rows) four values of every row side by side, so
+              // that a warp's store is one run of bytes: as 32 pieces of 16 bytes the
+              // parts of a tile of 256 rows took 6 us to leave the SM.
+              const bool wide = p.rows > kWideRows;
+              uint4* dst = reinterpret_cast<uint4*>(p.ws_o) +
+                           (wide ? (static_cast<long long>(slot) * (D / 4) + 8 * c) * p.rows + tile * p.nt * grp + r
+                                 : part * (D / 4) + 8 * c);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) {
+                *dst = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                dst += wide ? p.rows : 1;
+              }
             }
           }
         }
@@ -540,32 +594,33 @@ __global__ void __launch_bounds__(kThreadsCA, 2)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 256 * MT);
   }
 }
 
 // Joins the parts of the tiles that were split.  With the parts' maxima m_i and
 // sums l_i:  m = max m_i,  O = Σ 2^(m_i − m) O_i / Σ 2^(m_i − m) l_i.
-// A block of eight warps takes kJoinRows rows of a tile, a warp a row (SPLIT = 1:
-// many rows, few parts each), or one row with the parts dealt out to the warps
-// (SPLIT = 8: few rows; one long sequence leaves a part on every CTA).
-constexpr int kJoinRows = 32;
+// WAY = kJoinFew: a block takes one row, its eight warps deal out the parts (few rows;
+// one long sequence leaves a part on every CTA).  kJoinRows: a block takes 32 rows, a
+// warp four at once.  kJoinWide: parts that lie chunk by chunk; a block takes 32 rows,
+// a lane a row, a warp a quarter of its values.
+enum { kJoinFew, kJoinRows, kJoinWide };
 
-template <int D, int SPLIT>
+template <int D, int WAY>
 __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max) {
-  constexpr int kPer = D / 32;
-  __shared__ float s_acc[SPLIT][D];
+  constexpr int kPer = D / 32, SPLIT = 8;
+  __shared__ float s_acc[WAY == kJoinFew ? SPLIT : 1][D];
   __shared__ float2 s_ml[SPLIT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned int chunks = SPLIT == 1 ? (p.rows + kJoinRows - 1) / kJoinRows : p.rows;
+  const unsigned int chunks = WAY == kJoinFew ? p.rows : (p.rows + 31) / 32;
   unsigned int x = blockIdx.x;
-  const int row0 = static_cast<int>(x % chunks) * (SPLIT == 1 ? kJoinRows : 1);
+  const int row0 = static_cast<int>(x % chunks) * (WAY == kJoinFew ? 1 : 32);
   x /= chunks;
   const int m = static_cast<int>(x % mt_max);
   x /= mt_max;
   const int h = static_cast<int>(x % p.c.hkv), s = static_cast<int>(x / p.c.hkv);
   const KeyPlan k = key_plan(p, s);
-  const int grp = p.c.group, t0 = m * p.nt, n_rows = min(k.n - t0, p.nt) * grp;
+  const int grp = p.c.group, t0 = m * p.ntt, n_rows = min(k.n - t0, p.ntt) * grp;
   // The attention kernel's results, complete and visible.  Every block waits, so
   // that this kernel never ends before that one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -580,44 +635,15 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   const int slot0 = 2 * c0 + (range_start(units, c0, grid) >= ua ? 0 : 1);
   auto part_of = [&](int c, int r) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * p.rows + r; };
 
-  auto gather = [&](int r, int first, int step, float& mx, float& sum, float(&acc)[kPer]) {
-    mx = -INFINITY;
-    for (int c = first + lane * step; c <= c1; c += 32 * step) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  auto load = [&](int c, int r) { return *reinterpret_cast<const Vec*>(p.ws_o + part_of(c, r) * D + lane * kPer); };
+  auto add = [&](float(&acc)[kPer], float w, const Vec& y) {
+    const float* v = reinterpret_cast<const float*>(&y);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    for (int cb = first; cb <= c1; cb += 32 * step) {
-      const int c = cb + lane * step;
-      float w = 0.f;
-      if (c <= c1) {
-        const float2 ml = p.ws_ml[part_of(c, r)];
-        w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
-        sum += w * ml.y;
-      }
-      const int n = min(32, (c1 - cb) / step + 1);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float* src = p.ws_o + part_of(cb + i * step, r) * D + lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          acc[0] += wi * y.x;
-          acc[1] += wi * y.y;
-          acc[2] += wi * y.z;
-          acc[3] += wi * y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          acc[0] += wi * y.x;
-          acc[1] += wi * y.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int i = 0; i < kPer; ++i) acc[i] += w * v[i];
   };
-  auto finish = [&](int r, float mx, float sum, const float(&acc)[kPer]) {
+  // Row r's output from the joined sums; one lane writes its LSE.
+  auto finish = [&](int r, float mx, float sum, const float(&acc)[kPer], bool lse) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int hq = h * grp + r % grp;
     const long long token = k.q0 + t0 + r / grp;
@@ -627,19 +653,108 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
           make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
     else
       *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0)
+    if (lse)
       p.lse[static_cast<long long>(hq) * p.c.total + token] =
           sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
   };
 
-  float mx, sum, acc[kPer];
-  if constexpr (SPLIT == 1) {
-    for (int r = row0 + warp; r < min(row0 + kJoinRows, n_rows); r += 8) {
-      gather(r, c0, 1, mx, sum, acc);
-      finish(r, mx, sum, acc);
+  if constexpr (WAY == kJoinWide) {
+    constexpr int kChunks = D / 16;  // of four values, of this warp
+    const int r = min(row0 + lane, n_rows - 1), first = warp * kChunks;
+    float mx = -INFINITY, sum = 0.f, acc2[kChunks][4] = {};
+    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      const float2 ml = p.ws_ml[part_of(c, r)];
+      const float w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+      sum += w * ml.y;
+      const float4* src = reinterpret_cast<const float4*>(p.ws_o) +
+                          (static_cast<long long>(c == c0 ? slot0 : 2 * c) * (D / 4) + first) * p.rows + r;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const float4 y = src[static_cast<long long>(i) * p.rows];
+        acc2[i][0] += w * y.x;
+        acc2[i][1] += w * y.y;
+        acc2[i][2] += w * y.z;
+        acc2[i][3] += w * y.w;
+      }
+    }
+    if (row0 + lane >= n_rows) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int hq = h * grp + r % grp;
+    const long long token = k.q0 + t0 + r / grp;
+    uint4* const dst = reinterpret_cast<uint4*>(p.o + (token * p.c.hkv * grp + hq) * D + first * 4);
+#pragma unroll
+    for (int i = 0; i < kChunks; i += 2)
+      dst[i / 2] = make_uint4(pack_bf16x2(acc2[i][0] * inv, acc2[i][1] * inv), pack_bf16x2(acc2[i][2] * inv, acc2[i][3] * inv),
+                              pack_bf16x2(acc2[i + 1][0] * inv, acc2[i + 1][1] * inv),
+                              pack_bf16x2(acc2[i + 1][2] * inv, acc2[i + 1][3] * inv));
+    if (warp == 0)
+      p.lse[static_cast<long long>(hq) * p.c.total + token] =
+          sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
+  } else if constexpr (WAY == kJoinRows) {
+    // Eight lanes a row look at its parts' maxima and sums.
+    const int r0 = row0 + 4 * warp, mine = min(r0 + (lane >> 3), n_rows - 1);
+    if (r0 >= n_rows) return;
+    float mx = -INFINITY, sum = 0.f, acc[4][kPer] = {};
+    for (int c = c0 + (lane & 7); c <= c1; c += 8) mx = fmaxf(mx, p.ws_ml[part_of(c, mine)].x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int cb = c0; cb <= c1; cb += 8) {
+      const int c = cb + (lane & 7);
+      float w = 0.f;
+      if (c <= c1) {
+        const float2 ml = p.ws_ml[part_of(c, mine)];
+        w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+        sum += w * ml.y;
+      }
+      const int n = min(8, c1 - cb + 1);
+      for (int i = 0; i < n; i += 2) {  // two parts of four rows in flight; behind the last, weight 0
+        Vec y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = load(min(cb + i + (e >> 2), c1), min(r0 + (e & 3), n_rows - 1));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float we = __shfl_sync(0xffffffffu, w, 8 * (e & 3) + i + (e >> 2));
+          if (we != 0.f) add(acc[e & 3], we, y[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float m_j = __shfl_sync(0xffffffffu, mx, 8 * j), s_j = __shfl_sync(0xffffffffu, sum, 8 * j);
+      if (r0 + j < n_rows) finish(r0 + j, m_j, s_j, acc[j], lane == 8 * j);
     }
   } else {
-    gather(row0, c0 + warp, SPLIT, mx, sum, acc);
+    const int r = row0;
+    float mx = -INFINITY, sum = 0.f, acc[kPer] = {};
+    for (int c = c0 + warp + lane * SPLIT; c <= c1; c += 32 * SPLIT) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int cb = c0 + warp; cb <= c1; cb += 32 * SPLIT) {
+      const int c = cb + lane * SPLIT;
+      float w = 0.f;
+      if (c <= c1) {
+        const float2 ml = p.ws_ml[part_of(c, r)];
+        w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+        sum += w * ml.y;
+      }
+      const int n = min(32, (c1 - cb) / SPLIT + 1);
+      for (int i = 0; i < n; i += 16) {  // sixteen parts in flight; behind the last, weight 0
+        Vec y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = load(min(cb + (i + e) * SPLIT, c1), r);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float we = __shfl_sync(0xffffffffu, w, i + e);
+          if (we != 0.f) add(acc, we, y[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
     if (lane == 0) s_ml[warp] = make_float2(mx, sum);
@@ -659,29 +774,31 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
 #pragma unroll
       for (int i = 0; i < kPer; ++i) acc[i] += f * s_acc[w][lane * kPer + i];
     }
-    finish(row0, mx, sum, acc);
+    finish(r, mx, sum, acc, lane == 0);
   }
 }
 
-template <int D>
+template <int D, int MT>
 cudaError_t launch(const CacheAttnLaunch& a) {
+  using L = CL<D, MT>;
   const CacheAttnParams& p = a.p;
-  const unsigned int smem = CL<D>::kBytes + 4u * (p.c.n_seq + 1);
+  const unsigned int smem = L::kBytes + 4u * (p.c.n_seq + 1);
   static volatile bool configured[64] = {};
   if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
   if (!configured[a.device]) {
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               CL<D>::kBytes + 4 * (kCacheMaxSeq + 1));
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               L::kBytes + 4 * (kCacheMaxSeq + 1));
     if (e != cudaSuccess) return e;
     configured[a.device] = true;
   }
-  cache_attn_kernel<D><<<a.grid, kThreadsCA, smem, a.stream>>>(a.q, a.k, a.v, a.kn, a.vn, p);
+  cache_attn_kernel<D, MT><<<a.grid, L::kThreads, smem, a.stream>>>(a.q, a.k, a.v, a.kn, a.vn, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int mt_max = (p.c.max_new + p.nt - 1) / p.nt;
+  const int mt_max = (p.c.max_new + p.ntt - 1) / p.ntt;
   const long long tiles = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max;
-  const bool few = tiles * p.rows <= 16 * a.grid / 2;  // at most 16 blocks an SM, a row each
-  const long long blocks = tiles * (few ? p.rows : (p.rows + kJoinRows - 1) / kJoinRows);
+  const bool wide = p.rows > kWideRows;
+  const bool few = !wide && tiles * p.rows <= 2432;  // a row a block: at most 16 an SM
+  const long long blocks = tiles * (few ? p.rows : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.
   cudaLaunchAttribute attr;
@@ -689,16 +806,20 @@ cudaError_t launch(const CacheAttnLaunch& a) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(blocks));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(wide ? 128 : 256);
   cfg.stream = a.stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 8>, p, a.grid, mt_max)
-             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 1>, p, a.grid, mt_max);
+  if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide>, p, a.grid, mt_max);
+  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew>, p, a.grid, mt_max)
+             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows>, p, a.grid, mt_max);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheAttnLaunch& a) { return a.p.c.d == 64 ? launch<64>(a) : launch<128>(a); }
+cudaError_t launch_cache_attn(const CacheAttnLaunch& a) {
+  if (a.p.c.d == 64) return a.tiles == 2 ? launch<64, 2>(a) : launch<64, 1>(a);
+  return a.tiles == 2 ? launch<128, 2>(a) : launch<128, 1>(a);
+}
 
 }  // namespace attn

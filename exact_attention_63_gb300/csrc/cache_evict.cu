@@ -128,9 +128,11 @@ __global__ void __launch_bounds__(256) cache_compact_kernel(const CacheParams c,
 // One CTA ranks one (sequence, head).  The budget-th largest key is found digit
 // by digit (11, 11 and 10 bits) from histograms in shared memory; one pass then
 // marks the slots that stay in a bit map (of those equal to the threshold, the
-// first ones), and the k-th freed slot below n finds the k-th kept slot behind
-// it by a binary search over the map's counts.  Keys stay in shared memory where
-// a sequence fits, else each pass reads the weights again.
+// first ones), and the k-th freed slot below n takes the k-th kept slot behind it.
+// Keys stay in shared memory where a sequence fits, and the kept slots behind n are
+// then listed over them; else each pass reads the weights again, and a binary search
+// over the map's counts finds the k-th.  Four keys a lane and step: with the loads
+// coalesced the passes are bound by their instructions.
 constexpr int kThreadsSel = 1024;
 constexpr int kBins = 2048;
 constexpr uint32_t kSmemMax = 232448;
@@ -144,19 +146,32 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool newest) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Position of the k-th (from 0) set bit of m.
-__device__ __forceinline__ int nth_bit(uint32_t m, int k) {
-  int at = 0;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    const int below = __popc((m >> at) & ((1u << w) - 1u));
-    if (k >= below) {
-      k -= below;
-      at += w;
-    }
+// The map keeps a group of 128 slots as four ballots: bit l of word e is slot 4l + e.
+struct Group {
+  uint32_t b[4];
+  // Set slots in the lanes given by the mask.
+  __device__ __forceinline__ int count(uint32_t lanes) const {
+    return __popc(b[0] & lanes) + __popc(b[1] & lanes) + __popc(b[2] & lanes) + __popc(b[3] & lanes);
   }
-  return at;
-}
+  __device__ __forceinline__ uint32_t nibble(int l) const {
+    return ((b[0] >> l) & 1u) | (((b[1] >> l) & 1u) << 1) | (((b[2] >> l) & 1u) << 2) | (((b[3] >> l) & 1u) << 3);
+  }
+  // The k-th (from 0) set slot.
+  __device__ __forceinline__ int nth(int k) const {
+    int l = 0;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+      const int below = count(((1u << w) - 1u) << l);
+      if (k >= below) {
+        k -= below;
+        l += w;
+      }
+    }
+    uint32_t x = nibble(l);
+    for (; k > 0; --k) x &= x - 1;
+    return 4 * l + __ffs(x) - 1;
+  }
+};
 
 struct SelectSmem {
   uint32_t words, groups, keys;  // bit-map words, groups of four words, cached keys
@@ -227,6 +242,8 @@ __global__ void __launch_bounds__(kThreadsSel)
   const int* const tab = c.table + static_cast<long long>(s) * c.max_blocks;
   const long long newest = (c.positions != nullptr ? static_cast<long long>(seq_pos[s]) : len) - recent;
   // Four slots at a time: page_size is a multiple of four, so they share a page.
+  // The up to three behind the last slot count as slots with the lowest key: they
+  // come last of all, and more than budget others come before.
   const int quads = (len + 3) / 4;
   auto load_quad = [&](int b, int off, int j) -> uint4 {
     const int page = min(max(tab[b], 0), c.n_pages - 1);
@@ -234,8 +251,9 @@ __global__ void __launch_bounds__(kThreadsSel)
     const float4 w = *reinterpret_cast<const float4*>(c.weights + at);
     int4 pos = make_int4(j, j + 1, j + 2, j + 3);
     if (c.positions != nullptr) pos = *reinterpret_cast<const int4*>(c.positions + at);
-    return make_uint4(rank_key(w.x, pos.x >= newest), rank_key(w.y, pos.y >= newest), rank_key(w.z, pos.z >= newest),
-                      rank_key(w.w, pos.w >= newest));
+    return make_uint4(rank_key(w.x, pos.x >= newest), j + 1 < len ? rank_key(w.y, pos.y >= newest) : 0u,
+                      j + 2 < len ? rank_key(w.z, pos.z >= newest) : 0u,
+                      j + 3 < len ? rank_key(w.w, pos.w >= newest) : 0u);
   };
   const bool cached = len <= static_cast<int>(lay.keys);
   auto quad_of = [&](int q) -> uint4 {
@@ -252,12 +270,12 @@ __global__ void __launch_bounds__(kThreadsSel)
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
     for (int i = tid; i < kBins; i += kThreadsSel) hist[i] = 0;
     __syncthreads();
-    auto count = [&](uint4 k, int q) {
+    const uint32_t digit = (1u << width) - 1u;
+    auto count = [&](uint4 k) {
       const uint32_t x[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (4 * q + e < len && (x[e] & fixed_bits) == prefix)
-          atomicAdd(&hist[(x[e] >> shift) & ((1u << width) - 1u)], 1);
+        if ((x[e] & fixed_bits) == prefix) atomicAdd(&hist[(x[e] >> shift) & digit], 1);
     };
     if (pass == 0) {
       const int db = 4 * kThreadsSel / c.page_size, doff = 4 * kThreadsSel - db * c.page_size;
@@ -280,13 +298,13 @@ __global__ void __launch_bounds__(kThreadsSel)
           const int q = q0 + e * kThreadsSel;
           if (q < quads) {
             if (cached) kq[q] = k[e];
-            count(k[e], q);
+            count(k[e]);
           }
         }
       }
     } else {
-#pragma unroll 2
-      for (int q = tid; q < quads; q += kThreadsSel) count(quad_of(q), q);
+#pragma unroll 4
+      for (int q = tid; q < quads; q += kThreadsSel) count(quad_of(q));
     }
     __syncthreads();
     // Bins from the top: thread t has bins kBins − 1 − 2t and the next lower one.
@@ -297,6 +315,7 @@ __global__ void __launch_bounds__(kThreadsSel)
       const bool in_hi = want <= above + hi;
       scratch[40] = kBins - 1 - 2 * tid - (in_hi ? 0 : 1);
       scratch[41] = above + (in_hi ? 0 : hi);
+      scratch[42] = in_hi ? hi : lo;
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(scratch[40]) << shift;
@@ -305,122 +324,136 @@ __global__ void __launch_bounds__(kThreadsSel)
     __syncthreads();
   }
   const uint32_t thr = prefix;
+  const bool ties = scratch[42] > want;  // more keys equal the threshold than may stay
 
   // ---- the map of the slots that stay; each warp has a run of groups of 128
   // slots, a lane four of them
   const int groups = (len + 127) / 128, per = (groups + 31) / 32;
   const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
-  const unsigned int octet = 0xffu << (lane & 24);
-  auto nibble = [&](int g, uint32_t& gt, uint32_t& eq) {
-    const int q = g * 32 + lane;
-    gt = eq = 0u;
-    if (q < quads) {
-      const uint4 k = quad_of(q);
-      const uint32_t x[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * q + e < len) {
-          gt |= (x[e] > thr ? 1u : 0u) << e;
-          eq |= (x[e] == thr ? 1u : 0u) << e;
-        }
-    }
+  const uint32_t lanes_below = (1u << lane) - 1u;
+  auto quad_in = [&](int g) { return g * 32 + lane < quads ? quad_of(g * 32 + lane) : make_uint4(0u, 0u, 0u, 0u); };
+  auto four = [](bool x, bool y, bool z, bool w) { return (x ? 1u : 0u) | (y ? 2u : 0u) | (z ? 4u : 0u) | (w ? 8u : 0u); };
+  auto ballots = [&](uint32_t nib) -> Group {
+    return {{__ballot_sync(0xffffffffu, nib & 1u), __ballot_sync(0xffffffffu, nib & 2u),
+             __ballot_sync(0xffffffffu, nib & 4u), __ballot_sync(0xffffffffu, nib & 8u)}};
   };
-  int eq = 0;
-  for (int g = g0; g < g1; ++g) {
-    uint32_t ng, ne;
-    nibble(g, ng, ne);
-    const uint32_t word = __reduce_or_sync(octet, ng << (4 * (lane & 7)));
-    if ((lane & 7) == 0) bits[4 * g + (lane >> 3)] = word;
-    eq += __popc(ne);
-  }
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  int total;
-  int eq_before = block_exclusive(lane == 0 ? eq : 0, scratch, &total);
-  eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
+  auto put = [&](int g, const Group& x) {
+    if (lane == 0) reinterpret_cast<uint4*>(bits)[g] = make_uint4(x.b[0], x.b[1], x.b[2], x.b[3]);
+  };
+  auto get = [&](int g) -> Group {
+    const uint4 x = reinterpret_cast<const uint4*>(bits)[g];
+    return {{x.x, x.y, x.z, x.w}};
+  };
+  // Of the nibble of slots 4·lane … of group g: those at or beyond n.
+  auto behind = [&](uint32_t nib, int g) {
+    const int first = g * 128 + 4 * lane;
+    return nib & (0xfu << max(0, min(n - first, 4))) & 0xfu;
+  };
   int src = 0;  // kept slots at or beyond n in this warp's run
-  for (int g = g0; g < g1; ++g) {
-    if (eq > 0 && eq_before < want) {  // of the equal ones the first stay
-      uint32_t ng, ne;
-      nibble(g, ng, ne);
-      const int mine = __popc(ne);
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      int room = want - eq_before - (incl - mine);
-      uint32_t stay = 0u;
+  int total;
+  auto count_behind = [&](int g, const Group& x) {
+    if (lane == 0) before[g] = src;
+    if (g * 128 >= n) src += x.count(0xffffffffu);
+    else if (g * 128 + 128 > n) src += ballots(behind(x.nibble(lane), g)).count(0xffffffffu);
+  };
+  if (!ties) {
+    // (The threshold is not the padding's 0 here: as many keys as may stay equal it.)
+    for (int g = g0; g < g1; ++g) {
+      const uint4 k = quad_in(g);
+      const Group x = ballots(four(k.x >= thr, k.y >= thr, k.z >= thr, k.w >= thr));
+      put(g, x);
+      count_behind(g, x);
+    }
+  } else {
+    int eq = 0;
+    for (int g = g0; g < g1; ++g) {
+      const uint4 k = quad_in(g);
+      eq += g * 32 + lane < quads ? __popc(four(k.x == thr, k.y == thr, k.z == thr, k.w == thr)) : 0;
+    }
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    int eq_before = block_exclusive(lane == 0 ? eq : 0, scratch, &total);
+    eq_before = __shfl_sync(0xffffffffu, eq_before, 0);
+    for (int g = g0; g < g1; ++g) {
+      const uint4 k = quad_in(g);
+      uint32_t nib = four(k.x > thr, k.y > thr, k.z > thr, k.w > thr);
+      const uint32_t ne = g * 32 + lane < quads ? four(k.x == thr, k.y == thr, k.z == thr, k.w == thr) : 0u;
+      const Group equal = ballots(ne);
+      int room = want - eq_before - equal.count(lanes_below);  // of the equal ones the first stay
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if ((ne >> e) & 1u) {
-          if (room > 0) stay |= 1u << e;
+          if (room > 0) nib |= 1u << e;
           --room;
         }
-      const uint32_t word = __reduce_or_sync(octet, stay << (4 * (lane & 7)));
-      if ((lane & 7) == 0) bits[4 * g + (lane >> 3)] |= word;
-      eq_before += __shfl_sync(0xffffffffu, incl, 31);
+      eq_before += equal.count(0xffffffffu);
+      const Group x = ballots(nib);
+      put(g, x);
+      count_behind(g, x);
     }
-    __syncwarp();
-    int cnt = 0;
-    if (lane < 4) {
-      const int lowest = g * 128 + 32 * lane;
-      uint32_t m = bits[4 * g + lane];
-      if (lowest + 32 <= n) m = 0u;
-      else if (lowest < n) m &= ~0u << (n - lowest);
-      cnt = __popc(m);
-    }
-    if (lane == 0) before[g] = src;
-    src += __reduce_add_sync(0xffffffffu, cnt);
   }
   int src_before = block_exclusive(lane == 0 ? src : 0, scratch, &total);
   src_before = __shfl_sync(0xffffffffu, src_before, 0);
   for (int g = g0 + lane; g < g1; g += 32) before[g] += src_before;
+  __syncwarp();
+
+  // ---- the kept slots at or beyond n, listed over the keys
+  int* const list = reinterpret_cast<int*>(kq);
+  if (cached) {
+    for (int g = max(g0, n / 128); g < g1; ++g) {
+      const uint32_t nib = behind(get(g).nibble(lane), g);
+      int at = before[g] + ballots(nib).count(lanes_below);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((nib >> e) & 1u) list[at++] = g * 128 + 4 * lane + e;
+    }
+  }
+  __syncthreads();
 
   // ---- slots below n: kept where they are, or filled by the k-th kept slot behind
-  const int wn = (n + 31) / 32, wper = (wn + 31) / 32;
-  const int w0 = min(wn, warp * wper), w1 = min(wn, w0 + wper);
-  __syncthreads();
+  const int gn = (n + 127) / 128, gper = (gn + 31) / 32;
+  const int h0 = min(gn, warp * gper), h1 = min(gn, h0 + gper);
+  auto freed = [&](int g) {  // this lane's slots below n that do not stay
+    const uint32_t nib = ~get(g).nibble(lane) & 0xfu;
+    return nib & ~behind(0xfu, g);
+  };
   int holes = 0;
-  for (int w = w0 + lane; w < w1; w += 32) {
-    const uint32_t live = w * 32 + 32 <= n ? 0xffffffffu : (1u << (n - w * 32)) - 1u;
-    holes += __popc(~bits[w] & live);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) holes += __shfl_xor_sync(0xffffffffu, holes, o);
+  for (int g = h0; g < h1; ++g) holes += __popc(freed(g));
+  holes = __reduce_add_sync(0xffffffffu, holes);
   int hole_before = block_exclusive(lane == 0 ? holes : 0, scratch, &total);
   hole_before = __shfl_sync(0xffffffffu, hole_before, 0);
-  const int g_first = n / 128;
-  for (int w = w0; w < w1; ++w) {
-    const int j = w * 32 + lane;
-    const uint32_t live = w * 32 + 32 <= n ? 0xffffffffu : (1u << (n - w * 32)) - 1u;
-    const uint32_t free_ = ~bits[w] & live;
-    if (j < n) {
-      int from = j;
-      if ((free_ >> lane) & 1u) {
-        int k = hole_before + __popc(free_ & ((1u << lane) - 1u));
-        int lo = g_first, hi = groups - 1;  // the last group with before[g] <= k
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (before[mid] <= k) lo = mid;
-          else hi = mid - 1;
-        }
-        k -= before[lo];
-        from = -1;
+  for (int g = h0; g < h1; ++g) {
+    const uint32_t nib = freed(g);
+    const Group x = ballots(nib);
+    int k = hole_before + x.count(lanes_below);
+    hole_before += x.count(0xffffffffu);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int lowest = lo * 128 + 32 * e;
-          uint32_t m = bits[4 * lo + e];
-          if (lowest + 32 <= n) m = 0u;
-          else if (lowest < n) m &= ~0u << (n - lowest);
-          const int cnt = __popc(m);
-          if (k >= 0 && k < cnt) from = lowest + nth_bit(m, k);
-          k -= cnt;
+    for (int e = 0; e < 4; ++e) {
+      const int j = g * 128 + 4 * lane + e;
+      int from = j;
+      if ((nib >> e) & 1u) {
+        if (cached) {
+          from = list[k];
+        } else {
+          int lo = n / 128, hi = groups - 1;  // the last group with before[lo] <= k
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] <= k) lo = mid;
+            else hi = mid - 1;
+          }
+          // (the group with slot n has kept slots below n too)
+          Group y = get(lo);
+          const int skip = max(0, n - lo * 128);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int gone = max(0, min((skip - f + 3) / 4, 32));  // lanes whose slot f is below n
+            y.b[f] = gone == 32 ? 0u : y.b[f] & (~0u << gone);
+          }
+          from = lo * 128 + y.nth(k - before[lo]);
         }
+        ++k;
       }
-      out[j] = from;
+      if (j < n) out[j] = from;
     }
-    hole_before += __popc(free_);
   }
 }
 

@@ -10,7 +10,7 @@
 namespace attn {
 
 constexpr int kCacheMaxSeq = 2048;   // sequences of one call: their offsets are kept in shared memory
-constexpr int kCacheMaxCtas = 320;   // CTAs of the attention kernel (two per SM); sizes its workspace
+constexpr int kCacheMaxCtas = 320;   // row tiles at work at a time (two per SM); sizes the attention's workspace
 
 // Division by a number fixed for the launch: x / d = x·mul >> (31 + log), exact
 // for 0 ≤ x < 2^31 (mul = ⌈2^(31 + log) / d⌉, log = ⌈log2 d⌉).  The loaders of short
@@ -55,6 +55,7 @@ struct CacheAttnParams {
   float* ws_o;           // [2 * grid, rows, d] its unnormalised output
   int rows;              // row pitch of the parts
   int nt;                // tokens of a row tile: nt * group <= 128 rows
+  int ntt;               // tokens of a CTA's row tiles
   int piece;             // key rows of one copy: the largest power of two in page_size, at most 64
   float scale_log2;
   unsigned int* status;
@@ -65,6 +66,7 @@ struct CacheAttnParams {
 struct CacheAttnLaunch {
   CUtensorMap q, k, v, kn, vn;  // q box (64, group, 1, nt); cache box (64, 1, piece, 1); new keys box (64, 1, 16, 1)
   CacheAttnParams p;
+  int tiles;             // row tiles of a CTA: 2 where a sequence may have more than 128 rows
   int grid, device;
   cudaStream_t stream;
 };
