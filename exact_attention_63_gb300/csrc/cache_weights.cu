@@ -181,16 +181,13 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
 
   if (warp == 0) {
     // ============================================================= loader
-    auto waited = [&](uint32_t bar, uint32_t parity) -> bool {
-      int ok = 1;
-      if (lane == 0) ok = wait_bar(bar, parity, wc);
-      return __shfl_sync(0xffffffffu, ok, 0) != 0;
-    };
     const int ps = p.piece;
     int nk = 0;
     bool ok = true;
-    // Lane 8w + i copies the i-th piece of half w; its page, a tile ahead.
-    const int my_row = 128 * (lane >> 3) + (lane & 7) * ps;
+    // Lane 8w + i copies the i-th piece of half w, lane 8w waits for its slot; the
+    // pages are looked up two tiles ahead (a load that a tile of few rows would wait
+    // for: one tile ahead, a tile took as long as the look-up).
+    const int half = lane >> 3, my_row = 128 * half + (lane & 7) * ps;
     auto locate = [&](const WTile& t, int& page, int& slot) {
       const int j = t.j0 + my_row;
       if (lane < 16 && (lane & 7) * ps < 128 && j < t.len) {
@@ -199,29 +196,49 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         page = page_for_read(p.c, t.s, blk);
       }
     };
-    int u = tile_of(0, cta, grid, units);
-    WTile t = tile_at(p, tab, u), t_next = t;
-    int page = 0, slot = 0, page_next = 0, slot_next = 0;
-    locate(t, page, slot);
-    for (int n = 0; ok && u >= 0; ++n, t = t_next, page = page_next, slot = slot_next) {
-      u = tile_of(n + 1, cta, grid, units);
-      if (u >= 0) {
-        t_next = tile_at(p, tab, u, t.s);
-        locate(t_next, page_next, slot_next);
+    WTile t[3];
+    int page[3] = {}, slot[3] = {};
+    bool there[3];
+    auto fetch = [&](int i, int n, int from) {
+      const int u = tile_of(n, cta, grid, units);
+      there[i] = u >= 0;
+      if (there[i]) {
+        t[i] = tile_at(p, tab, u, from);
+        locate(t[i], page[i], slot[i]);
       }
-      if (t.c0 == t.c1) continue;  // no row sees it: nothing to multiply
-      const int keys = min(kTileKeys, t.len - t.j0);
-      for (int w = 0; w < 2 && 128 * w < keys; ++w, ++nk) {
-        const int npc = (min(128, keys - 128 * w) + ps - 1) / ps, ks = nk % kst;
-        ok = waited(k_empty(ks), ((nk / kst) & 1) ^ 1u);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
-        __syncwarp();
-        if ((lane >> 3) == w && (lane & 7) < npc)
+    };
+    fetch(0, 0, 0);
+    t[1] = t[0];
+    fetch(1, 1, t[0].s);
+    for (int n = 0; ok && there[0]; ++n) {
+      t[2] = t[1];
+      fetch(2, n + 2, t[1].s);
+      if (t[0].c0 != t[0].c1) {  // else no row sees it: nothing to multiply
+        const int keys = min(kTileKeys, t[0].len - t[0].j0), halves = keys > 128 ? 2 : 1;
+        const int npc = half < halves ? (min(128, keys - 128 * half) + ps - 1) / ps : 0;
+        const int ks = (nk + half) % kst;
+        int mine = 1;
+        if ((lane & 7) == 0 && half < halves) {
+          mine = wait_bar(k_empty(ks), (((nk + half) / kst) & 1) ^ 1u, wc);
+          if (mine) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
+        }
+        // A half whose wait ran out is not announced, so nothing of it is copied.
+        const unsigned int got = __ballot_sync(0xffffffffu, mine);
+        if (half < 2 && (lane & 7) < npc && ((got >> (8 * half)) & 1u))
           for (int hf = 0; hf < L::kHalves; ++hf)
-            tma_load_4d(ring_k + ks * L::kSlot + (lane & 7) * ps * 128 + hf * 16384, &tm_k, 64 * hf, t.h, slot, page,
-                        k_full(ks));
+            tma_load_4d(ring_k + ks * L::kSlot + (lane & 7) * ps * 128 + hf * 16384, &tm_k, 64 * hf, t[0].h, slot[0],
+                        page[0], k_full(ks));
         __syncwarp();
+        ok = got == 0xffffffffu;
+        if (ok) nk += halves;
+        else if ((got & 1u) && halves > 0) ++nk;  // the first half's copies are in flight
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        t[i] = t[i + 1];
+        page[i] = page[i + 1];
+        slot[i] = slot[i + 1];
+        there[i] = there[i + 1];
       }
     }
     if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
@@ -250,7 +267,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         for (int c = t.c0; c < t.c1 && ok; ++c, ++nq) {
           const int qs = nq % qst, buf = nq & 1;
           const uint32_t tS = tmem + 256 * buf + 128 * w;
-          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc) && wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
+          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc);
+          ok = ok && wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
           if (!ok) break;
           if (w < halves) {
             tc_fence_after();
