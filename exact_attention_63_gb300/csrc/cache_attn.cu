@@ -23,17 +23,22 @@
 // MT = 2, more rows: one CTA an SM works on two tiles of 128 rows at once, which share
 // every block of K and V, two blocks in flight, one tile's MMAs under the other's
 // exponentials.  (With MT = 1 such a call waits for copies: a block took ~4200 cycles a
-// CTA, of which the copies' latency, 2500, showed almost whole.)  One thread issues
-// P·V and the next S of one tile, then those of the other, which keeps the tiles half
-// a period apart; an issuer a tile let them fall into step, both at the tensor core,
-// then both at the exponentials (4700 cycles a block).
+// CTA, of which the copies' latency, 2500, showed almost whole.)
+//   At d = 128 a tile's TMEM has no room for a P beside S, and a P over S costs a round
+// trip to the tensor core and back (P·V's commit → barrier → issuer, ~500 cycles) before
+// the next S can be issued; with whole blocks that set the pace, 4100 cycles a block of
+// both tiles.  So (HALVES) the block is taken in two halves of 64 keys, each with an S
+// buffer of its own: S of one half is issued while the softmax is on the other.
+//   One thread issues all MMAs at MT = 1; at MT = 2 each tile has one, with HALVES one
+// for S, and one thread issues both tiles' P·V (a commit or wait costs its thread ~130
+// cycles, an MMA ~75).
 //
-// Warps: 0 loads (TMA boxes of a page's rows, one lane a box), 1 issues the MMAs, and
+// Warps: 0 loads (TMA boxes of a page's rows, one lane a box), then the issuers, and
 // four per tile compute its softmax, one thread a row (TMEM lane).
 //
 // TMEM columns of a tile (256·tile + …):
 // d = 128: S [0,128), with P (bf16) over its first half; O [128,256).
-//          S(g+1) is issued once P(g)·V has completed.
+//          S(g+1) is issued once P(g)·V has completed.  HALVES: S of half x at [64x, 64x + 64).
 // d = 64:  S [0,128), P [128,192), O [192,256): S(g+1) is issued once the softmax
 //          has read S(g).
 //
@@ -106,14 +111,15 @@ __device__ __forceinline__ int cached_in(const KeyPlan& k, int b) {
 
 template <int D, int MT>
 struct CL {
+  static constexpr bool kHalf = MT == 2 && D == 128;
   static constexpr int kThreads = MT == 1 ? 192 : 384;
   static constexpr int kSoftmax0 = MT == 1 ? 2 : 4;  // first softmax warp
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = 128u * D * 2;  // 128 rows of Q, K or V: [half][128 rows][128 B]
   static constexpr int kStages = MT == 2 ? (D == 128 ? 2 : 3) : (D == 128 ? 1 : 2);
   static constexpr uint32_t kQ = 0, kK = MT * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
-  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], then a tile's s_full, s_free, p_full, pv_done; done
-  static constexpr int kNumBars = 3 + 4 * kStages + 4 * MT;
+  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], then a tile's s_full[2], p_full[2], pv_done[2], s_free, done[2]
+  static constexpr int kNumBars = 2 + 4 * kStages + 9 * MT;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;       // TMEM base, abort flag
   static constexpr uint32_t kSums = kMisc + 8;                 // one int per warp
   static constexpr uint32_t kTable = (kSums + 48 + 15) & ~15u;
@@ -138,11 +144,11 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
   auto v_full = [&](int s) { return bars + 8u * (2 + 2 * L::kStages + s); };
   auto v_empty = [&](int s) { return bars + 8u * (2 + 3 * L::kStages + s); };
   constexpr uint32_t kB = 2 + 4 * L::kStages;
-  auto s_full = [&](int i) { return bars + 8u * (kB + 4 * i); };
-  auto s_free = [&](int i) { return bars + 8u * (kB + 4 * i + 1); };
-  auto p_full = [&](int i) { return bars + 8u * (kB + 4 * i + 2); };
-  auto pv_done = [&](int i) { return bars + 8u * (kB + 4 * i + 3); };
-  const uint32_t done = bars + 8u * (kB + 4 * MT);
+  auto s_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + x); };  // tile i, half x (0 without halves)
+  auto p_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 2 + x); };
+  auto pv_done = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 4 + x); };
+  auto s_free = [&](int i) { return bars + 8u * (kB + 9 * i + 6); };
+  auto done = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 7 + x); };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
@@ -159,20 +165,22 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
   if (threadIdx.x == 32) {
     *abort_flag = 0u;
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, MT);  // (each tile's issuer answers for its own reads)
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), MT);
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
+      mbar_init(v_empty(s), L::kHalf ? 1 : MT);
     }
     for (int i = 0; i < MT; ++i) {
-      mbar_init(s_full(i), 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(s_full(i, x), 1);
+        mbar_init(p_full(i, x), 4);
+        mbar_init(pv_done(i, x), 1);
+        mbar_init(done(i, x), 1);
+      }
       mbar_init(s_free(i), 4);
-      mbar_init(p_full(i), 4);
-      mbar_init(pv_done(i), 1);
     }
-    mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -273,85 +281,156 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
       for (int n = max(0, nk - L::kStages); n < nk; ++n) drain(k_full(n % L::kStages), (n / L::kStages) & 1u);
       for (int n = max(0, nv - L::kStages); n < nv; ++n) drain(v_full(n % L::kStages), (n / L::kStages) & 1u);
     }
-  } else if (warp == 1) {
-    // ========================================================= MMA issuer
+  } else if (L::kHalf && warp <= 2) {
+    // =============================================== halves: a tile's S issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16(128, 64, false);
+      const int tile = warp - 1;
+      const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ + tile * L::kTile);
+      int g = 0, ns = 0;  // blocks and segments of the CTA
+      int e = 0;          // blocks of this tile: fewer, where a segment has rows for the first tile only
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; ++ns) {
+        const Segment sg = segment_at(p, tab, u, u1);
+        u += sg.b1 - sg.b0;
+        const bool now = tile == 0 || sg.k.n - sg.m * p.ntt > p.nt;
+        ok = wait_bar(q_full, ns & 1, wc);
+        for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
+          const int st = g % L::kStages;
+          ok = wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+          if (now) {
+            const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // The half's last product has read its P, which lies over S.
+              if (e > 0) ok = ok && wait_bar(pv_done(tile, x), (e - 1) & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + 256 * tile + 64 * x, dq + o, dk + o + ((x * 8192) >> 4), idS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(s_full(tile, x));
+            }
+            ++e;
+          }
+          if (!ok) break;
+          mma_commit(k_empty(st));
+          if (b == sg.b1 - 1) mma_commit(q_empty);
+        }
+      }
+      mma_commit(done(tile, 0));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(done(tile, 0), 0))
+        if (globaltimer_ns() - t0 > p.timeout_ns) break;
+    }
+  } else if (L::kHalf && warp == 3) {
+    // ============================================ halves: both tiles' P·V issuer
+    if (lane == 0) {
+      constexpr uint32_t idPV = idesc_bf16(128, D, true);
+      int g = 0, e1 = 0;  // blocks of the CTA (and of the first tile), blocks of the second
+      bool ok = true;
+      for (int u = u0; u < u1 && ok;) {
+        const Segment sg = segment_at(p, tab, u, u1);
+        u += sg.b1 - sg.b0;
+        const int tiles = sg.k.n - sg.m * p.ntt > p.nt ? 2 : 1;
+        for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
+          const int st = g % L::kStages;
+          ok = wait_bar(v_full(st), (g / L::kStages) & 1, wc);
+          const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            for (int i = 0; i < tiles; ++i) {
+              ok = ok && wait_bar(p_full(i, x), (i == 0 ? g : e1) & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t t = tmem + 256 * i;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(t + L::kColO, t + 64 * x + kk * 8, dv + (((4 * x + kk) * 2048) >> 4), idPV,
+                       (b > sg.b0 || x > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(pv_done(i, x));
+            }
+          if (!ok) break;
+          mma_commit(v_empty(st));
+          if (tiles == 2) ++e1;
+        }
+      }
+      mma_commit(done(0, 1));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(done(0, 1), 0))
+        if (globaltimer_ns() - t0 > p.timeout_ns) break;
+    }
+  } else if (!L::kHalf && warp <= MT) {
+    // ==================================================== a tile's MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16(128, 128, false);
       constexpr uint32_t idPV = idesc_bf16(128, D, true);
-      int g = 0, ns = 0;          // blocks and segments of the CTA
-      int e[MT] = {};             // blocks of each tile: fewer, where a segment has rows for the first tile only
-      bool before[MT] = {};       // the tile has a product of block g − 1 to come
-      bool before_first = false;  // which opens its segment
+      const int tile = warp - 1;
+      const uint32_t t = tmem + 256 * tile;
+      int g = 0, ns = 0, e = 0;  // as above
+      bool before = false;       // this tile's product of block g − 1 is to come
+      bool first = false;        // which opens its segment
       bool ok = true;
-      // O (+)= P·V of block g − 1 for a tile; `last`: no other tile needs its V.
-      auto issue_pv = [&](int i, bool last) -> bool {
+      // O (+)= P·V of block g − 1.
+      auto issue_pv = [&]() -> bool {
         const int st = (g - 1) % L::kStages;
-        if (!wait_bar(v_full(st), ((g - 1) / L::kStages) & 1, wc) || !wait_bar(p_full(i), (e[i] - 1) & 1, wc))
+        if (!wait_bar(v_full(st), ((g - 1) / L::kStages) & 1, wc) || !wait_bar(p_full(tile, 0), (e - 1) & 1, wc))
           return false;
         tc_fence_after();
         const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
-        const uint32_t t = tmem + 256 * i;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(t + L::kColO, t + L::kColP + kk * 8, dv + ((kk * 2048) >> 4), idPV, (!before_first || kk > 0) ? 1u : 0u);
-        mma_commit(pv_done(i));
-        if (last) mma_commit(v_empty(st));
+          mma_ts(t + L::kColO, t + L::kColP + kk * 8, dv + ((kk * 2048) >> 4), idPV, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(pv_done(tile, 0));
+        mma_commit(v_empty(st));
         return true;
-      };
-      auto issue_s = [&](int i) {
-        tc_fence_after();
-        const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ + i * L::kTile);
-        const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + (g % L::kStages) * L::kTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 256 * i + L::kColS, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(s_full(i));
       };
       for (int u = u0; u < u1 && ok; ++ns) {
         const Segment sg = segment_at(p, tab, u, u1);
         u += sg.b1 - sg.b0;
-        const int tiles = MT == 2 && sg.k.n - sg.m * p.ntt > p.nt ? 2 : 1;
-        for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
+        const bool now = tile == 0 || sg.k.n - sg.m * p.ntt > p.nt;
+        for (int b = sg.b0; b < sg.b1; ++b, ++g) {
           const int st = g % L::kStages;
+          if (D == 128 && before) ok = ok && issue_pv();  // the last P lies over S: its product has to be done first
+          if (b == sg.b0) ok = ok && wait_bar(q_full, ns & 1, wc);
+          ok = ok && wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+          if (now && e > 0)
+            ok = ok && (D == 128 ? wait_bar(pv_done(tile, 0), (e - 1) & 1, wc) : wait_bar(s_free(tile), (e - 1) & 1, wc));
+          if (!ok) break;
+          if (now) {
+            tc_fence_after();
+            const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ + tile * L::kTile);
+            const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const bool now = i < tiles;
-            const bool last_pv = i == MT - 1 || !before[MT - 1];
-            // d = 128: the last P lies over S, its product has to be done first.
-            if (D == 128 && before[i]) ok = ok && issue_pv(i, last_pv);
-            if (now && i == 0) {
-              if (b == sg.b0) ok = ok && wait_bar(q_full, ns & 1, wc);
-              ok = ok && wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              mma_ss(t + L::kColS, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
             }
-            if (now && e[i] > 0)
-              ok = ok && (D == 128 ? wait_bar(pv_done(i), (e[i] - 1) & 1, wc) : wait_bar(s_free(i), (e[i] - 1) & 1, wc));
-            if (!ok) break;
-            if (now) {
-              issue_s(i);
-              if (i == tiles - 1) {
-                mma_commit(k_empty(st));
-                if (b == sg.b1 - 1) mma_commit(q_empty);
-              }
-            }
-            if (D == 64 && before[i]) ok = issue_pv(i, last_pv);
-            if (!ok) break;
-            before[i] = now;
-            if (now) ++e[i];
+            mma_commit(s_full(tile, 0));
           }
-          before_first = b == sg.b0;
+          mma_commit(k_empty(st));
+          if (b == sg.b1 - 1) mma_commit(q_empty);
+          if (D == 64 && before) ok = issue_pv();
+          if (!ok) break;
+          if (MT == 2 && !now) {  // no product of this block here
+            ok = wait_bar(v_full(st), (g / L::kStages) & 1, wc);
+            if (!ok) break;
+            mma_commit(v_empty(st));
+          }
+          before = now;
+          first = b == sg.b0;
+          e += now;
         }
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        if (before[i]) ok = ok && issue_pv(i, i == MT - 1 || !before[MT - 1]);
-      mma_commit(done);
+      if (ok && before) issue_pv();
+      mma_commit(done(tile, 0));
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(done, 0))
+      while (!mbar_try_wait(done(tile, 0), 0))
         if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
-  } else if (warp >= L::kSoftmax0) {
+  } else if (warp >= L::kSoftmax0 && warp < L::kSoftmax0 + 4 * MT) {
     // ============================================================ softmax
     const int tile = MT == 1 ? 0 : (warp - L::kSoftmax0) >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
@@ -402,49 +481,55 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
           }
         }
       }
-      auto block = [&](int b, auto mask_tag) -> bool {
+      // A block's keys, or half x of them.
+      constexpr int kCh = L::kHalf ? 2 : 4;  // chunks of 32 keys
+      auto block = [&](int b, int x, auto mask_tag) -> bool {
         constexpr bool MASK = decltype(mask_tag)::value;
-        const bool got = wait_bar_cold(s_full(tile), e & 1, wc);
+        const uint32_t tSx = tS + 64 * x, tPx = L::kHalf ? tSx : tP;
+        const bool got = wait_bar_cold(s_full(tile, x), e & 1, wc);
         if (__any_sync(0xffffffffu, !got)) return false;
         tc_fence_after();
-        uint32_t vis[4];
+        uint32_t vis[kCh];
         if constexpr (MASK) {
           const int cv = cached_in(sg.k, b), dn = b == sg.k.db ? sg.k.n : 0;
           const int sh = sg.k.off >> 5, bit = sg.k.off & 31;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int n = min(max(cv - 32 * c, 0), 32);
+          for (int c = 0; c < kCh; ++c) {
+            const int cc = c + 2 * x;
+            const int n = min(max(cv - 32 * cc, 0), 32);
             vis[c] = n == 32 ? 0xffffffffu : (1u << n) - 1u;
             if (dn > 0) {
               uint32_t lo = 0u, hi = 0u;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                if (i == c - sh) hi = anc[i];
-                if (i == c - sh - 1) lo = anc[i];
+                if (i == cc - sh) hi = anc[i];
+                if (i == cc - sh - 1) lo = anc[i];
               }
               vis[c] |= __funnelshift_l(lo, hi, bit);
             }
           }
-          // Zero the rows of V that hold no key (every warp its 32 rows).
-          const int st = g % L::kStages;
-          const bool in = wait_bar_cold(v_full(st), (g / L::kStages) & 1, wc);
-          if (__any_sync(0xffffffffu, !in)) return false;
-          if (!(r < cv || (r >= sg.k.off && r < sg.k.off + dn))) {
-            uint8_t* const row = smem + L::kV + st * L::kTile + r * 128;
+          if (x == 0) {
+            // Zero the rows of V that hold no key (every warp its 32 rows).
+            const int st = g % L::kStages;
+            const bool in = wait_bar_cold(v_full(st), (g / L::kStages) & 1, wc);
+            if (__any_sync(0xffffffffu, !in)) return false;
+            if (!(r < cv || (r >= sg.k.off && r < sg.k.off + dn))) {
+              uint8_t* const row = smem + L::kV + st * L::kTile + r * 128;
 #pragma unroll
-            for (int i = 0; i < 8 * L::kHalves; ++i)
-              *reinterpret_cast<uint4*>(row + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < 8 * L::kHalves; ++i)
+                *reinterpret_cast<uint4*>(row + (i >> 3) * 16384 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
         if (active) {
           uint32_t a[32], c2[32];
           float mx = -INFINITY;
-          // ---- block maximum
+          // ---- maximum
           if constexpr (MASK) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(tS + 32 * c, a);
+            for (int c = 0; c < kCh; ++c) {
+              tmem_ld32(tSx + 32 * c, a);
               tmem_wait_ld();
               reg_fence32(a);
 #pragma unroll
@@ -452,29 +537,26 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
                 if ((vis[c] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(a[i]));
             }
           } else {
-            float m0, m1;
-            tmem_ld32_max(tS, a, m0);
-            tmem_ld32_max(tS + 32, c2, m1);
-            tmem_wait_ld();
-            asm volatile("" : "+f"(m0), "+f"(m1));
-            reg_fence32(a);
-            reg_fence32(c2);
-            mx = fmaxf(m0, m1);
-            tmem_ld32_max(tS + 64, a, m0);
-            tmem_ld32_max(tS + 96, c2, m1);
-            tmem_wait_ld();
-            asm volatile("" : "+f"(m0), "+f"(m1));
-            reg_fence32(a);
-            reg_fence32(c2);
-            mx = fmax3(mx, m0, m1);
+#pragma unroll
+            for (int c = 0; c < kCh; c += 2) {
+              float m0, m1;
+              tmem_ld32_max(tSx + 32 * c, a, m0);
+              tmem_ld32_max(tSx + 32 * c + 32, c2, m1);
+              tmem_wait_ld();
+              asm volatile("" : "+f"(m0), "+f"(m1));
+              reg_fence32(a);
+              reg_fence32(c2);
+              mx = fmax3(mx, m0, m1);
+            }
           }
           mx *= sc;
           const bool need = r < n_rows && (mx > m_run + kTau || (m_run == -INFINITY && mx > -INFINITY));
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = need ? mx : m_run;
-            if (b > sg.b0) {
+            if (b > sg.b0 || x > 0) {
               const float alpha = need ? ex2_mufu(m_run - m_new) : 1.f;
-              if (!rescale_o<D>(pv_done(tile), (e - 1) & 1, wc, tO, alpha)) return false;
+              // (the product before this one: the other half's, or the last block's)
+              if (!rescale_o<D>(pv_done(tile, L::kHalf ? x ^ 1 : 0), (x > 0 ? e : e - 1) & 1, wc, tO, alpha)) return false;
               l_run *= alpha;
             }
             m_run = m_new;
@@ -482,7 +564,7 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
           // ---- exponentials, P in bf16
           if constexpr (D == 64) {
             if (e > 0) {  // the last P·V has read P
-              const bool landed = wait_bar_cold(pv_done(tile), (e - 1) & 1, wc);
+              const bool landed = wait_bar_cold(pv_done(tile, 0), (e - 1) & 1, wc);
               if (__any_sync(0xffffffffu, !landed)) return false;
               tc_fence_after();
             }
@@ -490,12 +572,12 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
           const float negm = m_run == -INFINITY ? 0.f : -m_run;
           const uint64_t nm2 = pack2(negm, negm);
           uint64_t acc[2] = {0, 0};
-          auto chunk = [&](int c, uint32_t(&x)[32]) {
+          auto chunk = [&](int c, uint32_t(&v)[32]) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x0, x1;
-              unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2), x0, x1);
+              unpack2(ffma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sc2, nm2), x0, x1);
               x0 = ex2_mufu(x0);
               x1 = ex2_mufu(x1);
               if constexpr (MASK) {
@@ -505,18 +587,18 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
               acc[i & 1] = fadd2(acc[i & 1], pack2(x0, x1));
               pk[i] = pack_bf16x2(x0, x1);
             }
-            tmem_st16(tP + 16 * c, pk);
+            tmem_st16(tPx + 16 * c, pk);
           };
-          tmem_ld32(tS, a);
+          tmem_ld32(tSx, a);
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
+          for (int c = 0; c < kCh; c += 2) {
             tmem_wait_ld();
             reg_fence32(a);
-            tmem_ld32(tS + 32 * (c + 1), c2);
+            tmem_ld32(tSx + 32 * (c + 1), c2);
             chunk(c, a);
             tmem_wait_ld();
             reg_fence32(c2);
-            if (c == 0) tmem_ld32(tS + 64, a);
+            if (c + 2 < kCh) tmem_ld32(tSx + 32 * (c + 2), a);
             chunk(c + 1, c2);
           }
           float a0, a1;
@@ -526,14 +608,16 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
         }
         tc_fence_before();
         if constexpr (D == 64) warp_arrive(s_free(tile), lane);
-        warp_arrive(p_full(tile), lane);
+        warp_arrive(p_full(tile, x), lane);
         return true;
       };
       for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g, ++e)
-        ok = b < sg.k.nfull ? block(b, std::false_type{}) : block(b, std::true_type{});
+#pragma unroll 1
+        for (int x = 0; x < (L::kHalf ? 2 : 1) && ok; ++x)
+          ok = b < sg.k.nfull ? block(b, x, std::false_type{}) : block(b, x, std::true_type{});
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      const bool landed = wait_bar_cold(pv_done(tile), (e - 1) & 1, wc);
+      const bool landed = wait_bar_cold(pv_done(tile, L::kHalf), (e - 1) & 1, wc);
       if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
       tc_fence_after();
       if (active) {
