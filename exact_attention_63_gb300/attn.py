@@ -115,7 +115,7 @@ def lib():
     L.attn_fwd_cache_workspace_size.restype = sz
     L.attn_cache_append.argtypes = [vp, vp, vp, i, vp, vp]
     L.attn_cache_append.restype = i
-    L.attn_cache_weights.argtypes = [vp, vp, vp, f, vp, vp]
+    L.attn_cache_weights.argtypes = [vp, vp, vp, f, vp, ctypes.POINTER(Options), vp]
     L.attn_cache_weights.restype = i
     L.attn_cache_select.argtypes = [vp, vp, i, i, vp, vp]
     L.attn_cache_select.restype = i

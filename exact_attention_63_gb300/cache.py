@@ -225,6 +225,13 @@ def _switched(dev, stream):
                 yield
 
 
+def _options(options):
+    if options is None:
+        return None
+    options.struct_size = ctypes.sizeof(attn.Options)
+    return ctypes.byref(options)
+
+
 def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
@@ -248,6 +255,7 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     At most 128 new tokens a sequence; one is the usual decoding step.  q, k_new and
     v_new may be slices of a packed projection.  Returns (o [total, H, d] bf16,
     lse [H, total] fp32); rows that belong to no sequence are not written.
+    ``options`` (attn.make_options): timeout_ms and the test flag apply.
     ``workspace``: a uint8 tensor of workspace_size(...) bytes, else allocated.
     """
     dev = _device("k_cache", k_cache)
@@ -287,12 +295,10 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
         return out, lse
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
-    if options is not None:
-        options.struct_size = ctypes.sizeof(attn.Options)
     rc = attn.lib().attn_fwd_cache(c, _pack_tokens(qr, kn, vn, cu, total, max_seqlen_q, H), par, scale,
                                    out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(),
-                                   ctypes.byref(options) if options is not None else None, _stream(dev))
+                                   _options(options), _stream(dev))
     if rc:
         attn._check(rc)
     return out, lse
@@ -331,7 +337,7 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
 
 
 def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q: int, weights=None,
-                  scale: float | None = None, out=None, stream=None):
+                  scale: float | None = None, out=None, stream=None, options=None):
     """Add the attention weight that each cached key received from packed queries.
 
     The n queries of a sequence belong to its newest n cached tokens: query i sees
@@ -344,7 +350,8 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     dev = _device("k_cache", k_cache)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
-            return cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, weights, scale, out)
+            return cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, weights, scale, out, None,
+                                 options)
     if seq_lens is None:
         raise ValueError("seq_lens is needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, None, block_table, seq_lens, weights, None)
@@ -366,7 +373,7 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     rc = attn.lib().attn_cache_weights(c, _pack_tokens(qr, _NONE, _NONE, cu, total, int(max_seqlen_q), H), lp,
-                                       scale, op, _stream(dev))
+                                       scale, op, _options(options), _stream(dev))
     if rc:
         attn._check(rc)
     return out

@@ -244,7 +244,7 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
 }
 
 int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,
-                       float* weights_out, cudaStream_t stream) {
+                       float* weights_out, const attn_options* opts, cudaStream_t stream) {
   if (lse == nullptr || weights_out == nullptr) return ATTN_ERR_NULL;
   attn::CacheWeightLaunch a;
   std::memset(&a, 0, sizeof(a));
@@ -259,6 +259,7 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   long long qs[2];
   if (!resolve<2>(x->q_strides, dense, qs)) return ATTN_ERR_CACHE;
   if (!aligned(lse, 4) || !aligned(weights_out, 16)) return ATTN_ERR_ALIGN;
+  if ((rc = check_options(opts, &a.p.timeout_ns, &a.p.test_flags)) != ATTN_OK) return rc;
   int sms = 0;
   if ((rc = attn::usable_device(&a.device, &a.p.status, &sms)) != ATTN_OK) return rc;
   a.p.lse = lse;
@@ -271,7 +272,6 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   a.p.piece = piece_of(c.page_size);
   a.p.scale_log2 = scale * 1.4426950408889634f;
   a.p.inv_scale = 1.f / scale;
-  a.p.timeout_ns = kDefaultTimeoutMs * 1000000ull;
   a.grid = tiles < sms ? static_cast<int>(tiles) : sms;
   a.stream = stream;
   if ((rc = encode_queries(&a.q, x, c, qs, a.p.nt)) != ATTN_OK || (rc = encode_pages(&a.k, c.k, c, c.k_st, a.p.piece)) != ATTN_OK)

@@ -84,6 +84,7 @@ struct CacheWeightParams {
   float scale_log2, inv_scale;
   unsigned int* status;
   uint64_t timeout_ns;
+  unsigned int test_flags;
 };
 struct CacheWeightLaunch {
   CUtensorMap q, k;

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         const int ks = (nk + half) % kst;
         int mine = 1;
         if ((lane & 7) == 0 && half < halves) {
-          mine = wait_bar(k_empty(ks), (((nk + half) / kst) & 1) ^ 1u, wc);
+          mine = wait_bar(k_empty(ks), (((nk + half) / kst) & 1) ^ 1u, wc) && !(p.test_flags & 1u);
           if (mine) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
         }
         // A half whose wait ran out is not announced, so nothing of it is copied.

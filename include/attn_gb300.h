@@ -527,9 +527,10 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
  *   weights_out : device, fp32 [n_pages, num_kv_heads, page_size]; may be
  *                 cache->weights.  Every slot in use is written, no other.
  * max_seqlen is not limited (whole prompts).  Sums are fp32, in a fixed order.
+ * opts as for attn_fwd_cache (may be NULL).
  */
 int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,
-                       float* weights_out, cudaStream_t stream);
+                       float* weights_out, const attn_options* opts, cudaStream_t stream);
 
 /*
  * attn_cache_select — which tokens stay when each sequence and head may keep

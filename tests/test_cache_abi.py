@@ -61,7 +61,7 @@ def calls(L, c, x, scale=0.125, o=A, lse=A, ws=A, ws_bytes=1 << 40, opts=None, k
     return {
         "attend": lambda: L.attn_fwd_cache(cp, xp, parents, scale, o, lse, ws, ws_bytes, op, None),
         "append": lambda: L.attn_cache_append(cp, xp, rows, n_rows, seq_pos, None),
-        "weigh": lambda: L.attn_cache_weights(cp, xp, lse, scale, out, None),
+        "weigh": lambda: L.attn_cache_weights(cp, xp, lse, scale, out, op, None),
         "select": lambda: L.attn_cache_select(cp, seq_pos, budget, recent, kept, None),
         "compact": lambda: L.attn_cache_compact(cp, kept, budget, None),
     }
@@ -133,7 +133,8 @@ def test_other_arguments(L, kw, expect, ops):
 
 @pytest.mark.parametrize("opts", [dict(rescale_threshold=4.0), dict(poly_exp2_mask=0x11), dict(test_flags=2)])
 def test_options_that_do_not_apply(L, opts):
-    assert calls(L, a_cache(), tokens(), opts=attn.make_options(**opts))["attend"]() == OPTION
+    run = calls(L, a_cache(), tokens(), opts=attn.make_options(**opts))
+    assert run["attend"]() == OPTION and run["weigh"]() == OPTION
 
 
 def test_good_arguments_reach_the_device(L):

@@ -56,6 +56,10 @@ ATTEND = [
     ("chain128", [130, 260], [128, 100], 4, 4, 128, "chain"),
     ("roots", [9, 250], [40, 128], 6, 3, 16, "roots"),
     ("long", [20011], [2], 4, 1, 128, "random"),
+    ("long_wide", [9000, 130], [80, 3], 8, 1, 64, "random"),
+    ("long_pair", [12000], [33], 8, 2, 16, "random"),
+    ("one_or_two_tiles", [(53 * i) % 700 for i in range(120)], [40 if i % 3 == 1 else 1 + i % 4 for i in range(120)], 8,
+     2, 16, "random"),
     ("many", [(37 * i) % 301 for i in range(333)], [1 + (i % 3 == 0) for i in range(333)], 2, 1, 16, "random"),
 ]
 
@@ -172,6 +176,22 @@ def test_attention_wait_limit():
     check_attention(c, *attend(c))
 
 
+@pytest.mark.parametrize("which", ["attend", "weigh"])
+def test_wait_limit_with_two_tiles(which):
+    """The other kernels' waits run out as cleanly."""
+    c = Case([3000, 40], [60, 1], 8, 2, 128, 16, seed=14).cuda()
+    opts = attn.make_options(timeout_ms=50, test_flags=attn.TEST_WITHHOLD_KV)
+    lse = torch.full((8, c.total), 6.0, device="cuda")
+    start = f64(c.weights)
+    if which == "attend":
+        attend(c, options=opts)
+    else:
+        weigh(c, lse, out=torch.zeros_like(c.weights), options=opts)
+    assert attn.get_status() == -8
+    check_attention(c, *attend(c))
+    check_weights(c, lse, start, weigh(c, lse))
+
+
 # ------------------------------------------------------------------ weights
 def weigh(c: Case, lse, **kw):
     return cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, c.max_new(), c.weights, **kw)
@@ -205,6 +225,8 @@ WEIGH = [
     ("wide_group", [333], [3], 128, 1, 16),
     ("more_queries_than_keys", [5, 20], [9, 20], 2, 1, 16),
     ("many", [1 + (37 * i) % 301 for i in range(333)], [1 for i in range(333)], 2, 1, 16),
+    ("many_prompts", [1 + (97 * i) % 400 for i in range(40)], [1 + (97 * i) % 400 for i in range(40)], 4, 2, 16),
+    ("prompt_and_steps", [1500, 3, 700, 256], [1500, 1, 0, 2], 4, 1, 64),
 ]
 
 
@@ -404,6 +426,25 @@ def test_on_another_stream():
         s.synchronize()
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and torch.equal(want_w, w)
         del junk
+
+
+def test_two_streams_at_once():
+    """Attention and weights side by side (both want the SMs' tensor memory)."""
+    a = Case([5000, 300], [60, 2], 8, 2, 128, 64, seed=23).cuda()
+    b = Case([4000, 900], [4000, 1], 8, 2, 64, 16, seed=24).cuda()
+    lse = torch.full((8, b.total), 7.0, device="cuda")
+    want, want_w = attend(a), weigh(b, lse, out=torch.zeros_like(b.weights))
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        w = torch.zeros_like(b.weights)
+        t.wait_stream(torch.cuda.current_stream())
+        got = attend(a, stream=s)
+        weigh(b, lse, out=w, stream=t)
+        again = attend(a, stream=t)
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and torch.equal(want_w, w)
+        assert torch.equal(want[0], again[0])
 
 
 def test_two_graphs_share_a_workspace():
