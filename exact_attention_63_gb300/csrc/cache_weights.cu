@@ -67,6 +67,19 @@ __device__ __forceinline__ uint64_t sdesc_added(uint32_t saddr) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
+// A ring's next slot and the parity of its use (a division by the run-time number of
+// slots costs an issuing thread as much as three MMAs).
+struct Ring {
+  int slots, at = 0;
+  uint32_t use = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == slots) {
+      at = 0;
+      use ^= 1u;
+    }
+  }
+};
+
 struct WTile {
   int s, h, j0;       // keys [j0, j0 + 256) of sequence s, head h
   int q0, n, rows, len;  // its query rows: first packed row, all of them, those within max_new
@@ -182,7 +195,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   if (warp == 0) {
     // ============================================================= loader
     const int ps = p.piece;
-    int nk = 0;
+    int nk = 0;  // slots filled
+    Ring rk{kst};
     bool ok = true;
     // Lane 8w + i copies the i-th piece of half w, lane 8w waits for its slot; the
     // pages are looked up two tiles ahead (a load that a tile of few rows would wait
@@ -216,10 +230,12 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       if (t[0].c0 != t[0].c1) {  // else no row sees it: nothing to multiply
         const int keys = min(kTileKeys, t[0].len - t[0].j0), halves = keys > 128 ? 2 : 1;
         const int npc = half < halves ? (min(128, keys - 128 * half) + ps - 1) / ps : 0;
-        const int ks = (nk + half) % kst;
+        Ring slot_of = rk;
+        if (half == 1) slot_of.next();
+        const int ks = slot_of.at;
         int mine = 1;
         if ((lane & 7) == 0 && half < halves) {
-          mine = wait_bar(k_empty(ks), (((nk + half) / kst) & 1) ^ 1u, wc) && !(p.test_flags & 1u);
+          mine = wait_bar(k_empty(ks), slot_of.use ^ 1u, wc) && !(p.test_flags & 1u);
           if (mine) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
         }
         // A half whose wait ran out is not announced, so nothing of it is copied.
@@ -230,8 +246,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
                         page[0], k_full(ks));
         __syncwarp();
         ok = got == 0xffffffffu;
-        if (ok) nk += halves;
-        else if ((got & 1u) && halves > 0) ++nk;  // the first half's copies are in flight
+        nk += ok ? halves : static_cast<int>(got & 1u);  // (the first half's copies may be in flight)
+        for (int i = 0; i < halves; ++i) rk.next();
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -254,21 +270,24 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     if (lane == 0) {
       const uint32_t id = idesc_bf16(128, p.n_cols, false);
       const int w = warp - 1;
-      int nk = 0, nq = 0, from = 0;
+      int nq = 0, from = 0;
+      Ring rk{kst}, rq{qst};
       bool ok = true;
       for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
         const WTile t = tile_at(p, tab, u, from);
         from = t.s;
         if (t.c0 == t.c1) continue;
         // A tile's second half may have no keys: its issuer only keeps count.
-        const int halves = t.len - t.j0 > 128 ? 2 : 1, ks = (nk + w) % kst;
-        if (w < halves) ok = wait_bar(k_full(ks), ((nk + w) / kst) & 1, wc);
+        const int halves = t.len - t.j0 > 128 ? 2 : 1;
+        Ring mine = rk;
+        if (w == 1) mine.next();
+        const int ks = mine.at;
+        if (w < halves) ok = wait_bar(k_full(ks), mine.use, wc);
         const uint64_t dk = sdesc_kmajor_sw128(ring_k + ks * L::kSlot);
-        for (int c = t.c0; c < t.c1 && ok; ++c, ++nq) {
-          const int qs = nq % qst, buf = nq & 1;
+        for (int c = t.c0; c < t.c1 && ok; ++c, ++nq, rq.next()) {
+          const int qs = rq.at, buf = nq & 1;
           const uint32_t tS = tmem + 256 * buf + 128 * w;
-          ok = wait_bar(q_full(qs), (nq / qst) & 1, wc);
-          ok = ok && wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
+          ok = wait_bar(q_full(qs), rq.use, wc) && wait_bar(s_free(w, buf), ((nq >> 1) & 1) ^ 1u, wc);
           if (!ok) break;
           if (w < halves) {
             tc_fence_after();
@@ -283,7 +302,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
           mma_commit(q_empty(qs));
         }
         if (ok && w < halves) mma_commit(k_empty(ks));
-        nk += halves;
+        for (int i = 0; i < halves; ++i) rk.next();
       }
       mma_commit(done(w));
       const uint64_t t0 = globaltimer_ns();
@@ -325,11 +344,12 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     bool more = advance(), ok = true;
     if (more) fetch();
     int nq = 0;
-    for (; more; ++nq) {
-      const int qs = nq % qst;
+    Ring rq{qst};
+    for (; more; ++nq, rq.next()) {
+      const int qs = rq.at;
       int go = 1;
       if (lane == 0) {
-        go = wait_bar(q_empty(qs), ((nq / qst) & 1) ^ 1u, wc);
+        go = wait_bar(q_empty(qs), rq.use ^ 1u, wc);
         if (go) {
           mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(nt * grp) * 128u * L::kHalves);
           for (int hf = 0; hf < L::kHalves; ++hf)
