@@ -793,12 +793,12 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
         sum += w * ml.y;
       }
       const int n = min(8, c1 - cb + 1);
-      for (int i = 0; i < n; i += 2) {  // two parts of four rows in flight; behind the last, weight 0
-        Vec y[8];
+      for (int i = 0; i < n; i += 4) {  // four parts of four rows in flight; behind the last, weight 0
+        Vec y[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = load(min(cb + i + (e >> 2), c1), min(r0 + (e & 3), n_rows - 1));
+        for (int e = 0; e < 16; ++e) y[e] = load(min(cb + i + (e >> 2), c1), min(r0 + (e & 3), n_rows - 1));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
           const float we = __shfl_sync(0xffffffffu, w, 8 * (e & 3) + i + (e >> 2));
           if (we != 0.f) add(acc[e & 3], we, y[e]);
         }
@@ -881,7 +881,10 @@ cudaError_t launch(const CacheAttnLaunch& a) {
   const int mt_max = (p.c.max_new + p.ntt - 1) / p.ntt;
   const long long tiles = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max;
   const bool wide = p.rows > kWideRows;
-  const bool few = !wide && tiles * p.rows <= 2432;  // a row a block: at most 16 an SM
+  // A row a block where a tile has 8 parts or more on average (at 512 tiles of 4 rows,
+  // 2048 such blocks took 10 us more than 512 of the other kind; at 2 tiles, 152 parts,
+  // the other kind would read them one after the other).
+  const bool few = !wide && tiles * 8 <= a.grid;
   const long long blocks = tiles * (few ? p.rows : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.

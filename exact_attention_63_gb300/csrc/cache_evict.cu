@@ -349,12 +349,14 @@ __global__ void __launch_bounds__(kThreadsSel)
     const int first = g * 128 + 4 * lane;
     return nib & (0xfu << max(0, min(n - first, 4))) & 0xfu;
   };
+  auto behind_of = [&](int g, const Group& x) -> Group {
+    return g * 128 >= n ? x : ballots(behind(x.nibble(lane), g));
+  };
   int src = 0;  // kept slots at or beyond n in this warp's run
   int total;
   auto count_behind = [&](int g, const Group& x) {
     if (lane == 0) before[g] = src;
-    if (g * 128 >= n) src += x.count(0xffffffffu);
-    else if (g * 128 + 128 > n) src += ballots(behind(x.nibble(lane), g)).count(0xffffffffu);
+    if (g * 128 + 128 > n) src += behind_of(g, x).count(0xffffffffu);
   };
   if (!ties) {
     // (The threshold is not the padding's 0 here: as many keys as may stay equal it.)
@@ -400,8 +402,9 @@ __global__ void __launch_bounds__(kThreadsSel)
   int* const list = reinterpret_cast<int*>(kq);
   if (cached) {
     for (int g = max(g0, n / 128); g < g1; ++g) {
-      const uint32_t nib = behind(get(g).nibble(lane), g);
-      int at = before[g] + ballots(nib).count(lanes_below);
+      const Group x = behind_of(g, get(g));
+      const uint32_t nib = x.nibble(lane);
+      int at = before[g] + x.count(lanes_below);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if ((nib >> e) & 1u) list[at++] = g * 128 + 4 * lane + e;
@@ -412,18 +415,18 @@ __global__ void __launch_bounds__(kThreadsSel)
   // ---- slots below n: kept where they are, or filled by the k-th kept slot behind
   const int gn = (n + 127) / 128, gper = (gn + 31) / 32;
   const int h0 = min(gn, warp * gper), h1 = min(gn, h0 + gper);
-  auto freed = [&](int g) {  // this lane's slots below n that do not stay
-    const uint32_t nib = ~get(g).nibble(lane) & 0xfu;
-    return nib & ~behind(0xfu, g);
+  auto freed = [&](int g) -> Group {  // the slots below n that do not stay
+    const Group x = get(g);
+    if (g * 128 + 128 <= n) return {{~x.b[0], ~x.b[1], ~x.b[2], ~x.b[3]}};
+    return ballots(~x.nibble(lane) & ~behind(0xfu, g));
   };
   int holes = 0;
-  for (int g = h0; g < h1; ++g) holes += __popc(freed(g));
-  holes = __reduce_add_sync(0xffffffffu, holes);
+  for (int g = h0; g < h1; ++g) holes += freed(g).count(0xffffffffu);
   int hole_before = block_exclusive(lane == 0 ? holes : 0, scratch, &total);
   hole_before = __shfl_sync(0xffffffffu, hole_before, 0);
   for (int g = h0; g < h1; ++g) {
-    const uint32_t nib = freed(g);
-    const Group x = ballots(nib);
+    const Group x = freed(g);
+    const uint32_t nib = x.nibble(lane);
     int k = hole_before + x.count(lanes_below);
     hole_before += x.count(0xffffffffu);
 #pragma unroll
