@@ -459,7 +459,7 @@ int fwd_host(const void* q_h, const void* k_h, const void* v_h, void* o_h, float
 
 extern "C" {
 
-int attn_version(void) { return 100; }
+int attn_version(void) { return 200; }
 
 const char* attn_strerror(int status) {
   switch (status) {

@@ -255,6 +255,7 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   const long long tiles = static_cast<long long>(c.n_seq) * c.hkv * ((c.cap + 255) / 256);
   if (tiles > kMaxInt || static_cast<long long>(x->H) * c.total > kMaxInt) return ATTN_ERR_SHAPE;
   if ((rc = check_scale(scale)) != ATTN_OK) return rc;
+  if (!std::isfinite(1.f / scale)) return ATTN_ERR_SCALE;  // (the kernel divides the LSE by it)
   const long long dense[2] = {static_cast<long long>(x->H) * c.d, c.d};
   long long qs[2];
   if (!resolve<2>(x->q_strides, dense, qs)) return ATTN_ERR_CACHE;

@@ -527,6 +527,7 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
  *   weights_out : device, fp32 [n_pages, num_kv_heads, page_size]; may be
  *                 cache->weights.  Every slot in use is written, no other.
  * max_seqlen is not limited (whole prompts).  Sums are fp32, in a fixed order.
+ * scale as for attn_fwd, and 1/scale has to be finite (ATTN_ERR_SCALE).
  * opts as for attn_fwd_cache (may be NULL).
  */
 int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,

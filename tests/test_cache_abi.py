@@ -115,6 +115,7 @@ def test_token_fields(L, field, value, expect, ops):
     (dict(o=None), NULL, ("attend",)), (dict(lse=None), NULL, ("attend", "weigh")), (dict(out=None), NULL, ("weigh",)),
     (dict(kept=None), NULL, ("select", "compact")), (dict(seq_pos=None), NULL, ("select",)),
     (dict(scale=0.0), SCALE, ("attend", "weigh")), (dict(scale=float("nan")), SCALE, ("attend", "weigh")),
+    (dict(scale=1e-40), SCALE, ("weigh",)),
     (dict(o=A + 8), ALIGN, ("attend",)), (dict(lse=A + 2), ALIGN, ("attend", "weigh")),
     (dict(parents=A + 1), ALIGN, ("attend",)), (dict(out=A + 8), ALIGN, ("weigh",)),
     (dict(kept=A + 2), ALIGN, ("select", "compact")), (dict(seq_pos=A + 2), ALIGN, ("append", "select")),
