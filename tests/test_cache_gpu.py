@@ -475,6 +475,82 @@ def test_two_graphs_share_a_workspace():
             c.parents.fill_(-1)
 
 
+def test_step_in_a_graph():
+    """Attention, append, weights, selection and compaction captured once and
+    replayed with other lengths, trees and rows: as the same calls made directly."""
+    H, hkv, d, page, budget = 4, 2, 64, 16, 40
+    base = Case([100, 33, 70], [4, 4, 4], H, hkv, d, page, seed=31, room=8).cuda()
+    base.positions.clamp_(min=0)
+    rows = torch.tensor([0, 1, 4, 8, 9, 11], dtype=torch.int32, device="cuda")
+    cu_acc = torch.tensor([0, 2, 3, 6], dtype=torch.int32, device="cuda")
+    names = ("k", "v", "weights", "positions", "seq_lens", "q", "k_new", "v_new", "parents", "table")
+
+    def step(s):
+        o, lse = cache.attn_fwd_cache(s["q"], s["k_new"], s["v_new"], s["k"], s["v"], s["table"], s["seq_lens"],
+                                      base.cu, 4, parents=s["parents"])
+        after = s["seq_lens"] + (cu_acc[1:] - cu_acc[:-1])
+        cache.cache_append(s["k_new"], s["v_new"], s["k"], s["v"], s["table"], after, cu_acc, rows=rows,
+                           weights=s["weights"], positions=s["positions"], seq_pos=after)
+        r = rows.long()
+        cache.cache_weights(s["q"][r], lse[:, r].contiguous(), s["k"], s["table"], after, cu_acc, 3, s["weights"])
+        kept = cache.cache_evict(s["k"], s["v"], s["weights"], s["table"], after, budget, 8, s["positions"], after)
+        return o, lse, kept
+
+    live = {n: getattr(base, n).clone() for n in names}
+    step({n: t.clone() for n, t in live.items()})
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step(live)
+    for turn, lens in enumerate(([100, 33, 70], [41, 0, 39], [7, 33, 64])):
+        state = {n: getattr(base, n).clone() for n in names}
+        state["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        state["parents"].fill_(-1 if turn else 0)
+        state["q"].copy_(torch.randn(state["q"].shape).bfloat16())
+        for n in names:
+            live[n].copy_(state[n])
+        want = step(state)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            assert torch.equal(a, b)
+        for n in ("k", "v", "weights", "positions"):
+            assert torch.equal(bits(state[n]), bits(live[n])), (turn, n)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages more than 2^32 elements from the first."""
+    hkv, d, page, n_pages = 8, 128, 64, 70000
+    assert n_pages * page * hkv * d > 1 << 32
+    k = torch.empty((n_pages, page, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    w = torch.zeros((n_pages, hkv, page), device="cuda")
+    pos = torch.zeros((n_pages, hkv, page), dtype=torch.int32, device="cuda")
+    c = Case([0], [1], 8, hkv, d, page, seed=32).cuda()
+    n = 100
+    g = torch.Generator().manual_seed(33)
+    table = torch.tensor([[n_pages - 1, n_pages - 7]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    kn, vn = (torch.randn((n, hkv, d), generator=g).bfloat16().cuda() for _ in range(2))
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    cache.cache_append(kn, vn, k, v, table, lens, cu, weights=w, positions=pos)
+    assert torch.equal(k[n_pages - 1], kn[:64]) and torch.equal(v[n_pages - 7, :36], vn[64:])
+    # the same keys in a small cache
+    c.lens, c.seq_lens, c.n_pages = [n], lens, 2
+    c.table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    c.k, c.v = (torch.stack([t[n_pages - 7], t[n_pages - 1]]) for t in (k, v))
+    o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, k, v, table, lens, c.cu, 1)
+    c.parents = None
+    check_attention(c, o, lse)
+    cache.cache_weights(c.q, lse, k, table, lens, c.cu, 1, w)
+    c.weights = torch.stack([w[n_pages - 7], w[n_pages - 1]])
+    check_weights(c, lse, np.zeros(c.weights.shape), c.weights)
+    kept = cache.cache_evict(k, v, w, table, lens, 50, 0)
+    moved = kept[0, 3].tolist()
+    for i in range(50):
+        assert torch.equal(k[n_pages - 1, i, 3], kn[moved[i], 3]) and torch.equal(v[n_pages - 1, i, 3], vn[moved[i], 3])
+
+
 def test_generation_with_drafts_and_eviction():
     """A prompt, then steps of drafting, attention, acceptance, append, weights and
     eviction, as they are used together, against the definitions on plain lists."""
