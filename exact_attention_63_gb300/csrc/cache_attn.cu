@@ -528,13 +528,17 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
           // ---- maximum
           if constexpr (MASK) {
 #pragma unroll
-            for (int c = 0; c < kCh; ++c) {
+            for (int c = 0; c < kCh; c += 2) {
               tmem_ld32(tSx + 32 * c, a);
+              tmem_ld32(tSx + 32 * c + 32, c2);
               tmem_wait_ld();
               reg_fence32(a);
+              reg_fence32(c2);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < 32; ++i) {
                 if ((vis[c] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(a[i]));
+                if ((vis[c + 1] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(c2[i]));
+              }
             }
           } else {
 #pragma unroll
@@ -556,7 +560,26 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
             if (b > sg.b0 || x > 0) {
               const float alpha = need ? ex2_mufu(m_run - m_new) : 1.f;
               // (the product before this one: the other half's, or the last block's)
-              if (!rescale_o<D>(pv_done(tile, L::kHalf ? x ^ 1 : 0), (x > 0 ? e : e - 1) & 1, wc, tO, alpha)) return false;
+              const uint32_t bar = pv_done(tile, L::kHalf ? x ^ 1 : 0), par = (x > 0 ? e : e - 1) & 1;
+              if constexpr (L::kHalf) {  // in line: a call would have to put the scores away
+                const bool landed = wait_bar(bar, par, wc);
+                if (__any_sync(0xffffffffu, !landed)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    asm volatile("" : "+r"(o[i]));
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  }
+                  tmem_st16(tO + 16 * c, o);
+                }
+              } else {
+                if (!rescale_o<D>(bar, par, wc, tO, alpha)) return false;
+              }
               l_run *= alpha;
             }
             m_run = m_new;
@@ -589,17 +612,22 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
             }
             tmem_st16(tPx + 16 * c, pk);
           };
-          tmem_ld32(tSx, a);
+          if constexpr (L::kHalf) {  // a half's scores are in registers since the maximum
+            chunk(0, a);
+            chunk(1, c2);
+          } else {
+            tmem_ld32(tSx, a);
 #pragma unroll
-          for (int c = 0; c < kCh; c += 2) {
-            tmem_wait_ld();
-            reg_fence32(a);
-            tmem_ld32(tSx + 32 * (c + 1), c2);
-            chunk(c, a);
-            tmem_wait_ld();
-            reg_fence32(c2);
-            if (c + 2 < kCh) tmem_ld32(tSx + 32 * (c + 2), a);
-            chunk(c + 1, c2);
+            for (int c = 0; c < kCh; c += 2) {
+              tmem_wait_ld();
+              reg_fence32(a);
+              tmem_ld32(tSx + 32 * (c + 1), c2);
+              chunk(c, a);
+              tmem_wait_ld();
+              reg_fence32(c2);
+              if (c + 2 < kCh) tmem_ld32(tSx + 32 * (c + 2), a);
+              chunk(c + 1, c2);
+            }
           }
           float a0, a1;
           unpack2(fadd2(acc[0], acc[1]), a0, a1);
