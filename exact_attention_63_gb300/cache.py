@@ -73,13 +73,13 @@ class NewTokens(ctypes.Structure):
 # structure takes one per field (a decoding step is short enough to notice).
 _CACHE = struct.Struct("@N2P6q4P6i")
 _TOKENS = struct.Struct("@N3P6qP3i0P")  # (0P: padded to a pointer's alignment, as in C)
-_TOKENS_SIZE = _TOKENS.size
-assert _CACHE.size == ctypes.sizeof(Cache) and _TOKENS_SIZE == ctypes.sizeof(NewTokens)
+_CACHE_SIZE, _TOKENS_SIZE = _CACHE.size, _TOKENS.size
+assert _CACHE_SIZE == ctypes.sizeof(Cache) and _TOKENS_SIZE == ctypes.sizeof(NewTokens)
 
 
-# Checks are written to cost little when they pass (a decoding step's kernels take
-# ~10 us): one call a tensor, which returns its address; the shape comes with it, so
-# that unpacking it checks the number of dimensions.
+# A decoding step's kernels take ~10 us, so the checks are written to cost little when
+# they pass: one expression over all tensors, dense ones first.  Where it does not hold,
+# the tensors are looked at one by one, for strides or for the reason of the refusal.
 
 
 def _refuse(name, t, dtype, dev, contiguous):
@@ -163,8 +163,34 @@ def _device(name, t):
 
 
 def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
-    """attn_cache of checked tensors; (bytes, H_kv, d, n_seq).  What an operator does
-    not use is None."""
+    """attn_cache of the tensors, checked; (bytes, H_kv, d, n_seq).  What an operator
+    does not use is None (k or weights is there)."""
+    try:
+        if (block_table.dtype is _I32 and block_table.get_device() == dev and block_table.is_contiguous()
+                and (seq_lens is None or (seq_lens.dtype is _I32 and seq_lens.get_device() == dev
+                                          and seq_lens.is_contiguous()))
+                and (k is None or (k.dtype is _BF16 and k.get_device() == dev and k.is_contiguous()))
+                and (v is None or (v.dtype is _BF16 and v.get_device() == dev and v.is_contiguous()
+                                   and v.shape == k.shape))
+                and (weights is None or (weights.dtype is _F32 and weights.get_device() == dev
+                                         and weights.is_contiguous()))
+                and (positions is None or (positions.dtype is _I32 and positions.get_device() == dev
+                                           and positions.is_contiguous()))):
+            n_seq, max_blocks = block_table.shape
+            if k is not None:
+                n_pages, page_size, hkv, d = k.shape
+            else:
+                (n_pages, hkv, page_size), d = weights.shape, 0
+            slots = (n_pages, hkv, page_size)
+            if ((seq_lens is None or seq_lens.shape == (n_seq,)) and (weights is None or weights.shape == slots)
+                    and (positions is None or positions.shape == slots)):
+                return (_CACHE.pack(_CACHE_SIZE, 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
+                                    0, 0, 0, 0, 0, 0, 0 if weights is None else weights.data_ptr(),
+                                    0 if positions is None else positions.data_ptr(), block_table.data_ptr(),
+                                    0 if seq_lens is None else seq_lens.data_ptr(), n_pages, page_size, max_blocks,
+                                    n_seq, hkv, d), hkv, d, n_seq)
+    except (AttributeError, ValueError):
+        pass
     table = _need("block_table", block_table, _I32, dev)
     n_seq, max_blocks = _shape("block_table", block_table, 2)
     vp = wp = pp = lp = 0
@@ -185,23 +211,43 @@ def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
         pp = _per_slot("positions", positions, _I32, (n_pages, hkv, page_size), dev)
     if seq_lens is not None:
         lp = _seq("seq_lens", seq_lens, n_seq, dev)
-    return (_CACHE.pack(_CACHE.size, kp, vp, *ks, *vs, wp, pp, table, lp, n_pages, page_size, max_blocks, n_seq, hkv,
+    return (_CACHE.pack(_CACHE_SIZE, kp, vp, *ks, *vs, wp, pp, table, lp, n_pages, page_size, max_blocks, n_seq, hkv,
                         d), hkv, d, n_seq)
 
 
-def _pack_tokens(q, k, v, cu, total, max_seqlen, H):
-    """attn_new_tokens from (address, strides) pairs."""
-    return _TOKENS.pack(_TOKENS_SIZE, q[0], k[0], v[0], *q[1], *k[1], *v[1], cu, total, max_seqlen, H)
-
-
-_NONE = (0, (0, 0))
-
-
-def _new_kv(k_new, v_new, hkv, d, dev):
-    kn, vn = _rows("k_new", k_new, dev), _rows("v_new", v_new, dev)
-    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.shape[1:] != (hkv, d):
-        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be [total, {hkv}, {d}]")
-    return kn, vn
+def _pack_tokens(dev, q, k, v, cu, n_seq, hkv, d, max_seqlen):
+    """attn_new_tokens of the tensors, checked; (bytes, total, H).  q, or k and v, may
+    be None."""
+    try:
+        if (cu.dtype is _I32 and cu.get_device() == dev and cu.is_contiguous() and cu.shape == (n_seq + 1,)
+                and (q is None or (q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()))
+                and (k is None or (k.dtype is _BF16 and k.get_device() == dev and k.is_contiguous()
+                                   and v.dtype is _BF16 and v.get_device() == dev and v.is_contiguous()
+                                   and k.shape == v.shape))):
+            total, H, dq = q.shape if q is not None else (k.shape[0], hkv, d)
+            if dq == d and hkv and H % hkv == 0 and (k is None or k.shape == (total, hkv, d)):
+                return (_TOKENS.pack(_TOKENS_SIZE, 0 if q is None else q.data_ptr(),
+                                     0 if k is None else k.data_ptr(), 0 if k is None else v.data_ptr(),
+                                     0, 0, 0, 0, 0, 0, cu.data_ptr(), total, max_seqlen, H), total, H)
+    except (AttributeError, ValueError):
+        pass
+    cp = _seq("cu_seqlens", cu, n_seq + 1, dev)
+    qp = kp = vp = 0
+    qs = ks = vs = (0, 0)
+    total, H = None, hkv
+    if q is not None:
+        qp, qs = _rows("q", q, dev)
+        total, H, dq = _shape("q", q, 3)
+        if dq != d or not hkv or H % hkv != 0:
+            raise ValueError(f"q {tuple(q.shape)} must be [total, H, {d}], H a multiple of {hkv}")
+    if k is not None or v is not None:
+        kp, ks = _rows("k_new", k, dev)
+        vp, vs = _rows("v_new", v, dev)
+        if total is None:
+            total = _shape("k_new", k, 3)[0]
+        if k.shape != (total, hkv, d) or v.shape != k.shape:
+            raise ValueError(f"k_new {tuple(k.shape)} and v_new {tuple(v.shape)} must be [{total}, {hkv}, {d}]")
+    return (_TOKENS.pack(_TOKENS_SIZE, qp, kp, vp, *qs, *ks, *vs, cp, total, max_seqlen, H), total, H)
 
 
 def _elsewhere(dev, stream):
@@ -266,12 +312,10 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, None, None)
-    qr = _rows("q", q, dev)
-    kn, vn = _new_kv(k_new, v_new, hkv, d, dev)
-    total, H, dq = _shape("q", q, 3)
-    if k_new.shape[0] != total or dq != d or H % hkv != 0:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k_new {tuple(k_new.shape)}, cache heads {hkv}, d {d}")
-    cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
+    if q is None or k_new is None or v_new is None:
+        raise ValueError("q, k_new and v_new are needed")
+    max_seqlen_q = int(max_seqlen_q)
+    x, total, H = _pack_tokens(dev, q, k_new, v_new, cu_seqlens_q, n_seq, hkv, d, max_seqlen_q)
     par = None if parents is None else _seq("parents", parents, total, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
@@ -285,7 +329,6 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
             raise ValueError("lse must be [H, total]")
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    max_seqlen_q = int(max_seqlen_q)
     device = k_cache.device
     if out is None:
         out = torch.empty((total, H, d), dtype=_BF16, device=device)
@@ -295,8 +338,7 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
         return out, lse
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
-    rc = attn.lib().attn_fwd_cache(c, _pack_tokens(qr, kn, vn, cu, total, max_seqlen_q, H), par, scale,
-                                   out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+    rc = attn.lib().attn_fwd_cache(c, x, par, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(),
                                    _options(options), _stream(dev))
     if rc:
@@ -322,16 +364,17 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     if v_cache is None or seq_lens is None:
         raise ValueError("v_cache and seq_lens are needed")
     c, hkv, d, n_seq = _pack_cache(dev, k_cache, v_cache, block_table, seq_lens, weights, positions)
-    kn, vn = _new_kv(k_new, v_new, hkv, d, dev)
-    cu = _seq("cu_new", cu_new, n_seq + 1, dev)
-    total, n_rows, rp = k_new.shape[0], 0, None
+    if k_new is None or v_new is None:
+        raise ValueError("k_new and v_new are needed")
+    x, total, _ = _pack_tokens(dev, None, k_new, v_new, cu_new, n_seq, hkv, d, 0)
+    n_rows, rp = 0, None
     if rows is not None:
         rp = _need("rows", rows, _I32, dev)
         (n_rows,) = _shape("rows", rows, 1)
     sp = None if seq_pos is None else _seq("seq_pos", seq_pos, n_seq, dev)
     if total == 0 or (rows is not None and n_rows == 0):
         return
-    rc = attn.lib().attn_cache_append(c, _pack_tokens(_NONE, kn, vn, cu, total, 0, 0), rp, n_rows, sp, _stream(dev))
+    rc = attn.lib().attn_cache_append(c, x, rp, n_rows, sp, _stream(dev))
     if rc:
         attn._check(rc)
 
@@ -360,20 +403,17 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     if out is None:
         raise ValueError("one of weights and out is needed")
     op = _per_slot("out", out, _F32, (k_cache.shape[0], hkv, k_cache.shape[1]), dev)
-    qr = _rows("q", q, dev)
-    total, H, dq = _shape("q", q, 3)
-    if dq != d or H % hkv != 0:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, cache heads {hkv}, d {d}")
+    if q is None:
+        raise ValueError("q is needed")
+    x, total, H = _pack_tokens(dev, q, None, None, cu_seqlens_q, n_seq, hkv, d, int(max_seqlen_q))
     if total == 0:
         raise ValueError("q has no rows")
     lp = _need("lse", lse, _F32, dev)
     if lse.shape != (H, total):
         raise ValueError(f"lse must be [H, total] = {(H, total)}")
-    cu = _seq("cu_seqlens_q", cu_seqlens_q, n_seq + 1, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    rc = attn.lib().attn_cache_weights(c, _pack_tokens(qr, _NONE, _NONE, cu, total, int(max_seqlen_q), H), lp,
-                                       scale, op, _options(options), _stream(dev))
+    rc = attn.lib().attn_cache_weights(c, x, lp, scale, op, _options(options), _stream(dev))
     if rc:
         attn._check(rc)
     return out

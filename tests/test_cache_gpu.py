@@ -658,3 +658,49 @@ def test_generation_with_drafts_and_eviction():
                 plain[s][h] += [(f64(k)[j, h], f64(v)[j, h], 0.0, at + i) for i, j in enumerate(paths[s])]
             add_weights(s, f64(qa)[r], f64(la)[:, r])
         check_state(seq_lens)
+
+
+def test_binding_refuses_what_does_not_fit():
+    """Wrong types, shapes, devices and strides are ValueErrors that name the tensor."""
+    c = Case([40, 20], [2, 1], 4, 2, 64, 16, seed=40).cuda()
+    lse = torch.zeros((4, 3), device="cuda")
+    kept = torch.zeros((2, 2, 8), dtype=torch.int32, device="cuda")
+    attend_args = dict(q=c.q, k_new=c.k_new, v_new=c.v_new, k_cache=c.k, v_cache=c.v, block_table=c.table,
+                       seq_lens=c.seq_lens, cu_seqlens_q=c.cu, max_seqlen_q=2, parents=c.parents)
+    calls = {
+        cache.attn_fwd_cache: attend_args,
+        cache.cache_append: dict(k_new=c.k_new, v_new=c.v_new, k_cache=c.k, v_cache=c.v, block_table=c.table,
+                                 seq_lens=c.seq_lens, cu_new=c.cu, weights=c.weights, positions=c.positions,
+                                 seq_pos=c.seq_lens),
+        cache.cache_weights: dict(q=c.q, lse=lse, k_cache=c.k, block_table=c.table, seq_lens=c.seq_lens,
+                                  cu_seqlens_q=c.cu, max_seqlen_q=2, weights=c.weights),
+        cache.cache_select: dict(weights=c.weights, block_table=c.table, seq_lens=c.seq_lens, budget=8,
+                                 positions=c.positions, seq_pos=c.seq_lens),
+        cache.cache_compact: dict(kept=kept, k_cache=c.k, v_cache=c.v, block_table=c.table, weights=c.weights,
+                                  positions=c.positions),
+    }
+    before = [t.clone() for t in (c.k, c.v, c.weights, c.positions)]
+    for f, args in calls.items():
+        for name, t in args.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            bad = [t.cpu(), t.to(torch.float16 if t.dtype.is_floating_point else torch.int64), t[..., None], 3,
+                   t.repeat(*([1] * (t.dim() - 1) + [2]))[..., ::2]]
+            if t.dim() == 1:
+                bad.append(torch.cat([t, t]))
+            if name not in ("parents", "weights", "positions", "seq_pos"):
+                bad.append(None)
+            for x in bad:
+                with pytest.raises(ValueError):
+                    f(**{**args, name: x})
+    with pytest.raises(ValueError):  # 5 heads over 2
+        cache.attn_fwd_cache(**{**attend_args, "q": torch.zeros((3, 5, 64), device="cuda").bfloat16()})
+    with pytest.raises(attn.AttnError) as e:
+        cache.attn_fwd_cache(**{**attend_args, "max_seqlen_q": 129})
+    assert e.value.code == -2
+    with pytest.raises(attn.AttnError) as e:
+        cache.cache_select(c.weights, c.table, c.seq_lens, 0)
+    assert e.value.code == -2
+    torch.cuda.synchronize()
+    for a, b in zip(before, (c.k, c.v, c.weights, c.positions)):
+        assert torch.equal(bits(a), bits(b))
