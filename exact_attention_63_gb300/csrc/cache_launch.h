@@ -79,7 +79,7 @@ struct CacheWeightParams {
   FastDiv by_hkv, by_page, by_nt;
   int nt;                // tokens of a chunk
   int n_cols;            // its rows rounded up to the MMA's multiple of 16
-  int k_stages, q_stages;  // slots of the two rings (set by the launch)
+  int k_stages, q_stages;  // key slots of a half, chunk slots (set by the launch)
   int piece;
   float scale_log2, inv_scale;
   unsigned int* status;

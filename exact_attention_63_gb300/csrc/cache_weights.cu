@@ -29,8 +29,10 @@
 // next two chunks while the exponentials of one run (twice as many sum warps that
 // kept S in TMEM meanwhile were slower: 257 against 214 us on a prompt of 8000 tokens, 32 heads over 8 at d = 128).
 // TMEM: S of half w, buffer i at columns 256·i + 128·w.  Shared memory holds a ring
-// of 128-key slots and one of chunks; a chunk of few rows takes little room, which
-// the key ring gets (more bytes in flight where memory is the bound).
+// of 128-key slots for each half and one of chunks; a chunk of few rows takes little
+// room, which the key rings get (more bytes in flight where memory is the bound).
+//   A half has a ring of its own because its issuer has to see every use of a slot: a
+// wait on a barrier's parity is only right for the phase after the last one seen.
 #include "attn_fwd_kernel.cuh"
 #include "cache_device.cuh"
 
@@ -40,7 +42,7 @@ namespace {
 constexpr int kThreadsCW = 384;
 constexpr int kTileKeys = 256;
 
-constexpr int kMaxStages = 8;
+constexpr int kMaxHalf = 4;    // key slots of a half
 constexpr int kMaxChunks = 4;  // slots of the chunk ring
 
 template <int D>
@@ -48,22 +50,21 @@ struct WL {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kSlot = 128u * D * 2;   // 128 keys: [half][128 rows][128 B]
   static constexpr uint32_t kOnes = 0;              // the keys' side of the added step, 4 KB
-  static constexpr uint32_t kCol = 4096;            // the rows' side, 4 KB for each chunk slot
-  static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxChunks + 10;
-  static constexpr uint32_t kBar = kCol + kMaxChunks * 4096;
+  static constexpr int kNumBars = 4 * kMaxHalf + 2 * kMaxChunks + 10;
+  static constexpr uint32_t kBar = kOnes + 4096;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
   static constexpr uint32_t kSums = kMisc + 8;
   static constexpr uint32_t kTable = (kSums + 80 + 15) & ~15u;
   // then the table of n_seq + 1 ints, three ints a sequence, and from a 1024-byte
-  // boundary the two rings
+  // boundary the key rings, the chunks and the rows' sides of their added steps
   __host__ __device__ static uint32_t rings(int n_seq) { return (kTable + 4u * (4 * n_seq + 1) + 1023u) & ~1023u; }
 };
 
 // Shared-memory matrix descriptor of the added step's operands, without swizzle:
-// [two halves of 8 along K][groups of 8 rows][8 rows][16 bytes], halves 2 KB and
-// groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_added(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(2048 >> 4) << 16) |
+// [two halves of 8 along K][groups of 8 rows][8 rows][16 bytes], the halves 16 bytes a
+// row and the groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_added(uint32_t saddr, int rows) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(rows) << 16) |
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
@@ -121,17 +122,20 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBar;
-  auto k_full = [&](int s) { return bars + 8u * s; };
-  auto k_empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
-  auto q_full = [&](int s) { return bars + 8u * (2 * kMaxStages + s); };
-  auto q_empty = [&](int s) { return bars + 8u * (2 * kMaxStages + kMaxChunks + s); };
-  constexpr uint32_t kB = 2 * kMaxStages + 2 * kMaxChunks;
+  auto k_full = [&](int w, int s) { return bars + 8u * (kMaxHalf * w + s); };  // half w, slot s
+  auto k_empty = [&](int w, int s) { return bars + 8u * (2 * kMaxHalf + kMaxHalf * w + s); };
+  auto q_full = [&](int s) { return bars + 8u * (4 * kMaxHalf + s); };
+  auto q_empty = [&](int s) { return bars + 8u * (4 * kMaxHalf + kMaxChunks + s); };
+  constexpr uint32_t kB = 4 * kMaxHalf + 2 * kMaxChunks;
   auto s_full = [&](int w, int i) { return bars + 8u * (kB + 2 * w + i); };
   auto s_free = [&](int w, int i) { return bars + 8u * (kB + 4 + 2 * w + i); };
   auto done = [&](int w) { return bars + 8u * (kB + 8 + w); };
-  const uint32_t ring_k = base + L::rings(p.c.n_seq), ring_q = ring_k + p.k_stages * L::kSlot;
+  const int kst = p.k_stages, qst = p.q_stages;  // key slots of a half, chunks
   const uint32_t q_half = static_cast<uint32_t>(p.n_cols) * 128u, q_bytes = q_half * L::kHalves;
-  const int kst = p.k_stages, qst = p.q_stages;
+  const uint32_t c_bytes = static_cast<uint32_t>(p.n_cols) * 32u;
+  const uint32_t ring_k = base + L::rings(p.c.n_seq), ring_q = ring_k + 2 * kst * L::kSlot;
+  const uint32_t ring_c = ring_q + qst * q_bytes;
+  auto k_slot = [&](int w, int s) { return ring_k + (w * kst + s) * L::kSlot; };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
@@ -146,10 +150,11 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   }
   if (threadIdx.x == 32) {
     *abort_flag = 0u;
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(k_full(i), 1);
-      mbar_init(k_empty(i), 1);
-    }
+    for (int i = 0; i < kMaxHalf; ++i)
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(k_full(w, i), 1);
+        mbar_init(k_empty(w, i), 1);
+      }
     for (int i = 0; i < kMaxChunks; ++i) {
       mbar_init(q_full(i), 2);   // its rows, its columns
       mbar_init(q_empty(i), 2);  // both issuers
@@ -165,13 +170,11 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     fence_proxy_async_smem();
   }
   // The added step's constant side, and zeros where the other side stays zero.
-  for (int i = threadIdx.x; i < 256; i += kThreadsCW) {
+  for (int i = threadIdx.x; i < 256; i += kThreadsCW)
     *reinterpret_cast<uint4*>(smem + L::kOnes + 16 * i) =
         i < 128 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
-    if (i >= 128)
-      for (int j = 0; j < kMaxChunks; ++j)
-        *reinterpret_cast<uint4*>(smem + L::kCol + j * 4096 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int i = threadIdx.x; i < 2 * qst * p.n_cols; i += kThreadsCW)
+    *reinterpret_cast<uint4*>(smem + (ring_c - base) + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums), [&](int s) {
     const SeqRows r = seq_rows(p.c, s);
@@ -195,12 +198,13 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   if (warp == 0) {
     // ============================================================= loader
     const int ps = p.piece;
-    int nk = 0;  // slots filled
-    Ring rk{kst};
+    int filled[2] = {0, 0};   // slots of each half
+    Ring rk[2] = {{kst}, {kst}};
     bool ok = true;
     // Lane 8w + i copies the i-th piece of half w, lane 8w waits for its slot; the
-    // pages are looked up two tiles ahead (a load that a tile of few rows would wait
-    // for: one tile ahead, a tile took as long as the look-up).
+    // pages are looked up three tiles ahead, in turn into three sets of registers
+    // (moving one set's load results to the next would wait for them: a tile of few
+    // rows then took as long as its look-up).
     const int half = lane >> 3, my_row = 128 * half + (lane & 7) * ps;
     auto locate = [&](const WTile& t, int& page, int& slot) {
       const int j = t.j0 + my_row;
@@ -221,40 +225,47 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         locate(t[i], page[i], slot[i]);
       }
     };
-    fetch(0, 0, 0);
-    t[1] = t[0];
-    fetch(1, 1, t[0].s);
-    for (int n = 0; ok && there[0]; ++n) {
-      t[2] = t[1];
-      fetch(2, n + 2, t[1].s);
-      if (t[0].c0 != t[0].c1) {  // else no row sees it: nothing to multiply
-        const int keys = min(kTileKeys, t[0].len - t[0].j0), halves = keys > 128 ? 2 : 1;
-        const int npc = half < halves ? (min(128, keys - 128 * half) + ps - 1) / ps : 0;
-        Ring slot_of = rk;
-        if (half == 1) slot_of.next();
-        const int ks = slot_of.at;
-        int mine = 1;
-        if ((lane & 7) == 0 && half < halves) {
-          mine = wait_bar(k_empty(ks), slot_of.use ^ 1u, wc) && !(p.test_flags & 1u);
-          if (mine) mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
-        }
-        // A half whose wait ran out is not announced, so nothing of it is copied.
-        const unsigned int got = __ballot_sync(0xffffffffu, mine);
-        if (half < 2 && (lane & 7) < npc && ((got >> (8 * half)) & 1u))
-          for (int hf = 0; hf < L::kHalves; ++hf)
-            tma_load_4d(ring_k + ks * L::kSlot + (lane & 7) * ps * 128 + hf * 16384, &tm_k, 64 * hf, t[0].h, slot[0],
-                        page[0], k_full(ks));
-        __syncwarp();
-        ok = got == 0xffffffffu;
-        nk += ok ? halves : static_cast<int>(got & 1u);  // (the first half's copies may be in flight)
-        for (int i = 0; i < halves; ++i) rk.next();
+    auto copy = [&](const WTile& t, int page, int slot) {
+      const int keys = min(kTileKeys, t.len - t.j0), halves = keys > 128 ? 2 : 1;
+      const int npc = half < halves ? (min(128, keys - 128 * half) + ps - 1) / ps : 0;
+      const Ring mine_of = half == 1 ? rk[1] : rk[0];
+      int mine = 1;
+      if ((lane & 7) == 0 && half < halves) {
+        mine = wait_bar(k_empty(half, mine_of.at), mine_of.use ^ 1u, wc) && !(p.test_flags & 1u);
+        if (mine) mbar_arrive_expect_tx(k_full(half, mine_of.at), static_cast<uint32_t>(npc * ps) * 128u * L::kHalves);
       }
+      // A half whose wait ran out is not announced, so nothing of it is copied.
+      const unsigned int got = __ballot_sync(0xffffffffu, mine);
+      if (half < 2 && (lane & 7) < npc && ((got >> (8 * half)) & 1u))
+        for (int hf = 0; hf < L::kHalves; ++hf)
+          tma_load_4d(k_slot(half, mine_of.at) + (lane & 7) * ps * 128 + hf * 16384, &tm_k, 64 * hf, t.h, slot, page,
+                      k_full(half, mine_of.at));
+      __syncwarp();
+      ok = got == 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        t[i] = t[i + 1];
-        page[i] = page[i + 1];
-        slot[i] = slot[i + 1];
-        there[i] = there[i + 1];
+      for (int w = 0; w < 2; ++w)
+        if (w < halves && ((got >> (8 * w)) & 1u)) {
+          ++filled[w];
+          rk[w].next();
+        }
+    };
+    int from = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      fetch(i, i, from);
+      if (there[i]) from = t[i].s;
+    }
+    bool more = true;
+    for (int n = 3; ok && more; n += 3) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (!ok || !there[i]) {
+          more = false;
+          break;
+        }
+        if (t[i].c0 != t[i].c1) copy(t[i], page[i], slot[i]);  // else no row sees it: nothing to multiply
+        fetch(i, n + i, from);
+        if (there[i]) from = t[i].s;
       }
     }
     if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
@@ -263,7 +274,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         while (!mbar_try_wait(bar, parity))
           if (globaltimer_ns() - t0 > p.timeout_ns) break;
       };
-      for (int n = max(0, nk - kst); n < nk; ++n) drain(k_full(n % kst), (n / kst) & 1u);
+      for (int w = 0; w < 2; ++w)
+        for (int n = max(0, filled[w] - kst); n < filled[w]; ++n) drain(k_full(w, n % kst), (n / kst) & 1u);
     }
   } else if (warp == 1 || warp == 2) {
     // ======================================================== MMA issuers
@@ -279,11 +291,9 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         if (t.c0 == t.c1) continue;
         // A tile's second half may have no keys: its issuer only keeps count.
         const int halves = t.len - t.j0 > 128 ? 2 : 1;
-        Ring mine = rk;
-        if (w == 1) mine.next();
-        const int ks = mine.at;
-        if (w < halves) ok = wait_bar(k_full(ks), mine.use, wc);
-        const uint64_t dk = sdesc_kmajor_sw128(ring_k + ks * L::kSlot);
+        const int ks = rk.at;
+        if (w < halves) ok = wait_bar(k_full(w, ks), rk.use, wc);
+        const uint64_t dk = sdesc_kmajor_sw128(k_slot(w, ks));
         for (int c = t.c0; c < t.c1 && ok; ++c, ++nq, rq.next()) {
           const int qs = rq.at, buf = nq & 1;
           const uint32_t tS = tmem + 256 * buf + 128 * w;
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
           if (!ok) break;
           if (w < halves) {
             tc_fence_after();
-            mma_ss(tS, sdesc_added(base + L::kOnes), sdesc_added(base + L::kCol + qs * 4096), id, 0u);
+            mma_ss(tS, sdesc_added(base + L::kOnes, 128), sdesc_added(ring_c + qs * c_bytes, p.n_cols), id, 0u);
             const uint64_t dq = sdesc_kmajor_sw128(ring_q + qs * q_bytes);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -301,8 +311,10 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
           mma_commit(s_full(w, buf));
           mma_commit(q_empty(qs));
         }
-        if (ok && w < halves) mma_commit(k_empty(ks));
-        for (int i = 0; i < halves; ++i) rk.next();
+        if (w < halves) {
+          if (ok) mma_commit(k_empty(w, ks));
+          rk.next();
+        }
       }
       mma_commit(done(w));
       const uint64_t t0 = globaltimer_ns();
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       }
       more = advance();
       if (more) fetch();
-      uint8_t* const col = smem + L::kCol + qs * 4096;
+      uint8_t* const col = smem + (ring_c - base) + qs * c_bytes;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // x = hi + mid + lo, each a rounding to bf16 of what the ones before leave.
@@ -374,7 +386,8 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         if (x[i] == -INFINITY) rest = 0.f;
         const uint32_t mid = pack_bf16x2(rest, 0.f) & 0xffffu;
         const uint32_t lo = pack_bf16x2(rest - __uint_as_float(mid << 16), 0.f) & 0xffffu;
-        *reinterpret_cast<uint4*>(col + 16 * (lane + 32 * i)) = make_uint4(hi | (mid << 16), lo, 0u, 0u);
+        if (lane + 32 * i < p.n_cols)
+          *reinterpret_cast<uint4*>(col + 16 * (lane + 32 * i)) = make_uint4(hi | (mid << 16), lo, 0u, 0u);
       }
       fence_proxy_async_smem();
       warp_arrive(q_full(qs), lane);
@@ -501,13 +514,15 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
 template <int D>
 cudaError_t launch(const CacheWeightLaunch& a) {
   CacheWeightParams p = a.p;
-  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq), q_bytes = static_cast<uint32_t>(p.n_cols) * D * 2;
-  // Four chunks in flight, and the keys get the rest: two slots (one tile) at least.
-  p.q_stages = 4;
-  while (room - p.q_stages * q_bytes < 2 * WL<D>::kSlot) --p.q_stages;  // many sequences: their table takes room
-  const uint32_t k_stages = (room - p.q_stages * q_bytes) / WL<D>::kSlot;
-  p.k_stages = static_cast<int>(k_stages < kMaxStages ? k_stages : kMaxStages);
-  const uint32_t smem = WL<D>::rings(p.c.n_seq) + p.k_stages * WL<D>::kSlot + p.q_stages * q_bytes + 1024u;
+  // Up to four chunks in flight, and the keys get the rest: a slot for each half (one
+  // tile) at least.
+  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq);
+  const uint32_t chunk = static_cast<uint32_t>(p.n_cols) * (D * 2 + 32);
+  p.q_stages = kMaxChunks;
+  while (room - p.q_stages * chunk < 2 * WL<D>::kSlot) --p.q_stages;  // many sequences: their table takes room
+  const uint32_t k_stages = (room - p.q_stages * chunk) / (2 * WL<D>::kSlot);
+  p.k_stages = static_cast<int>(k_stages < kMaxHalf ? k_stages : kMaxHalf);
+  const uint32_t smem = WL<D>::rings(p.c.n_seq) + 2 * p.k_stages * WL<D>::kSlot + p.q_stages * chunk + 1024u;
   static volatile bool configured[64] = {};
   if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
   if (!configured[a.device]) {

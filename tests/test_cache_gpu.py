@@ -270,6 +270,26 @@ def test_weights_of_every_query_sum_to_its_heads():
     assert abs(float(out.double().sum()) - 8 * c.total) < 1e-5 * 8 * c.total
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("prompt", [False, True])
+def test_weights_of_short_and_long_tiles_in_turn(d, prompt):
+    """Tiles of one half and of two follow each other on every CTA in any order, many
+    of them and each launch with its own timing: the halves run apart and meet again."""
+    g = torch.Generator().manual_seed(21)
+    n = 90 if prompt else 260
+    pick = [100, 300, 60, 400, 128, 129, 17, 256] if prompt else [100, 300, 60, 512, 128, 129, 17, 700, 384, 90]
+    lens = [pick[int(i)] for i in torch.randint(0, len(pick), (n,), generator=g)]
+    new = lens if prompt else [1] * n
+    c = Case(lens, new, 8 if prompt else 4, 4, d, 16, seed=22).cuda()
+    start = f64(c.weights)
+    lse = (torch.randn((c.H, c.total), generator=g) * 0.1 + 6.0).cuda()
+    first = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, start, first)
+    for _ in range(200):
+        out = weigh(c, lse, out=torch.zeros_like(c.weights))
+        assert torch.equal(out, first)
+
+
 def test_weights_strided_queries_and_pages():
     H, hkv, d = 6, 2, 64
     c = Case([300, 70], [40, 1], H, hkv, d, 16, seed=4).cuda()
