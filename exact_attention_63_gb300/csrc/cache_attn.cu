@@ -314,6 +314,14 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
               mma_commit(s_full(tile, x));
             }
             ++e;
+          } else {
+            // No rows here.  V is waited for all the same: the softmax looks at v_full in
+            // some blocks only, and a wait on a parity is right only for the phase after
+            // one that is known to be over.  So S of a block is issued when V of all
+            // blocks before it is known to have arrived: by this wait, or by the product
+            // of this tile's last block.
+            if (e > 0) ok = ok && wait_bar(pv_done(tile, 1), (e - 1) & 1, wc);
+            ok = ok && wait_bar(v_full(st), (g / L::kStages) & 1, wc);
           }
           if (!ok) break;
           mma_commit(k_empty(st));
@@ -645,10 +653,10 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
           ok = b < sg.k.nfull ? block(b, x, std::false_type{}) : block(b, x, std::true_type{});
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      const bool landed = wait_bar_cold(pv_done(tile, L::kHalf), (e - 1) & 1, wc);
-      if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
-      tc_fence_after();
       if (active) {
+        const bool landed = wait_bar_cold(pv_done(tile, L::kHalf), (e - 1) & 1, wc);
+        if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
+        tc_fence_after();
         const bool whole = sg.b0 == 0 && sg.b1 == sg.k.db + 1;
         const int grp = p.c.group, t = t0 + r / grp, hq = sg.h * grp + r % grp, H = p.c.hkv * grp;
         const long long token = sg.k.q0 + t;

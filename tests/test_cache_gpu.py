@@ -74,6 +74,22 @@ def test_attention(case, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_one_row_tile_and_two_in_turn(d):
+    """Runs of blocks without rows for the second tile, between blocks that have some and
+    end in a tail (whose unused rows of V are zeroed): launches with their own timing."""
+    g = torch.Generator().manual_seed(23)
+    n = 150
+    lens = [int(x) for x in torch.randint(0, 900, (n,), generator=g)]
+    new = [40 if x else 3 for x in torch.randint(0, 2, (n,), generator=g).tolist()]
+    c = Case(lens, new, 8, 2, d, 16, seed=24).cuda()
+    o, lse = attend(c)
+    check_attention(c, o, lse)
+    for _ in range(200):
+        o2, lse2 = attend(c)
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_attention_peaky_scores(d):
     """Standard deviation 6 in q: the reference maximum moves between blocks."""
     c = Case([1500, 700], [3, 20], 8, 2, d, 32, seed=5, sigma=6.0).cuda()
