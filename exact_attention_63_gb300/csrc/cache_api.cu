@@ -228,7 +228,7 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
   int rc = check_cache(cache, 3, &p.c);
   if (rc != ATTN_OK || (rc = check_tokens(x, false, &p.c)) != ATTN_OK) return rc;
   if (x->k == nullptr || x->v == nullptr || p.c.lens == nullptr) return ATTN_ERR_NULL;
-  if (rows != nullptr && n_rows < 1) return ATTN_ERR_SHAPE;
+  if ((rows != nullptr && n_rows < 1) || x->total > kMaxCapacity || n_rows > kMaxCapacity) return ATTN_ERR_SHAPE;
   p.n_rows = rows != nullptr ? n_rows : x->total;
   const long long kd = static_cast<long long>(p.c.hkv) * p.c.d, dense[2] = {kd, p.c.d};
   if (!resolve<2>(x->k_strides, dense, p.kn_st) || !resolve<2>(x->v_strides, dense, p.vn_st)) return ATTN_ERR_CACHE;
@@ -253,7 +253,8 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   if (rc != ATTN_OK || (rc = check_tokens(x, true, &c)) != ATTN_OK) return rc;
   if (c.lens == nullptr) return ATTN_ERR_NULL;
   const long long tiles = static_cast<long long>(c.n_seq) * c.hkv * ((c.cap + 255) / 256);
-  if (tiles > kMaxInt || static_cast<long long>(x->H) * c.total > kMaxInt) return ATTN_ERR_SHAPE;
+  // (128: the kernel rounds a sequence's rows up to whole chunks)
+  if (tiles > kMaxInt || static_cast<long long>(x->H) * c.total > kMaxInt - 128) return ATTN_ERR_SHAPE;
   if ((rc = check_scale(scale)) != ATTN_OK) return rc;
   if (!std::isfinite(1.f / scale)) return ATTN_ERR_SCALE;  // (the kernel divides the LSE by it)
   const long long dense[2] = {static_cast<long long>(x->H) * c.d, c.d};
@@ -287,7 +288,7 @@ int attn_cache_select(const attn_cache* cache, const int* seq_pos, int budget, i
   int rc = check_cache(cache, 0, &c);
   if (rc != ATTN_OK) return rc;
   if (c.weights == nullptr || c.lens == nullptr || (c.positions != nullptr && seq_pos == nullptr)) return ATTN_ERR_NULL;
-  if (budget < 1 || recent < 0 || recent > budget || c.cap > ATTN_CACHE_MAX_SELECT ||
+  if (budget < 1 || budget > kMaxCapacity || recent < 0 || recent > budget || c.cap > ATTN_CACHE_MAX_SELECT ||
       static_cast<long long>(c.n_seq) * c.hkv > kMaxInt)
     return ATTN_ERR_SHAPE;
   if (!aligned(kept, 4) || !aligned(seq_pos, 4)) return ATTN_ERR_ALIGN;
@@ -302,7 +303,9 @@ int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cud
   CacheParams c;
   int rc = check_cache(cache, 3, &c);
   if (rc != ATTN_OK) return rc;
-  if (budget < 1 || static_cast<long long>(c.n_seq) * c.hkv * ((budget + 31ll) / 32) > kMaxInt) return ATTN_ERR_SHAPE;
+  if (budget < 1 || budget > kMaxCapacity ||
+      static_cast<long long>(c.n_seq) * c.hkv * ((budget + 31) / 32) > kMaxInt)
+    return ATTN_ERR_SHAPE;
   if (!aligned(kept, 4)) return ATTN_ERR_ALIGN;
   int dev = -1, sms = 0;
   unsigned int* status = nullptr;

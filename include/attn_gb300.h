@@ -510,6 +510,7 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
  *             drafted tree); an entry outside [0, total) is skipped.
  *   seq_pos : device, int32 [n_seq], tokens of the sequence that have ever been
  *             appended, the new ones included; NULL: seq_lens.
+ * total and n_rows are at most 2^30.
  */
 int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const int* rows, int n_rows,
                       const int* seq_pos, cudaStream_t stream);
@@ -548,7 +549,7 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
  *             as if positions were slots and seq_pos were seq_lens); k, v are not
  *             used.
  *   seq_pos : device, int32 [n_seq]; needed with positions.
- * budget >= 1, 0 <= recent <= budget, and max_blocks*page_size at most
+ * 1 <= budget <= 2^30, 0 <= recent <= budget, and max_blocks*page_size at most
  * ATTN_CACHE_MAX_SELECT.
  */
 #define ATTN_CACHE_MAX_SELECT (1 << 20)
@@ -561,6 +562,7 @@ int attn_cache_select(const attn_cache* cache, const int* seq_pos, int budget, i
  * slot kept[s, h, i] go to slot i of the same head.  Entries below budget move
  * nothing, so sources and destinations never meet.  Afterwards the caller sets
  * seq_lens to min(seq_lens, budget).  An entry beyond the table is skipped.
+ * 1 <= budget <= 2^30.
  */
 int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cudaStream_t stream);
 

@@ -132,6 +132,19 @@ def test_other_arguments(L, kw, expect, ops):
         assert run[op]() == expect, op
 
 
+def test_sizes_near_the_top_of_32_bits_are_refused(L):
+    """The kernels round them up in 32 bits; up to 2^30 that is fine."""
+    top, most = 2 ** 31 - 1, 2 ** 30
+    one = a_cache(num_kv_heads=1, n_seq=1)
+    for budget in (most + 1, top):
+        run = calls(L, one, tokens(), budget=budget)
+        assert run["select"]() == SHAPE and run["compact"]() == SHAPE
+    assert calls(L, one, tokens(), budget=most, kept=A + 2)["compact"]() == ALIGN  # (not refused for its size)
+    assert calls(L, one, tokens(total=top))["append"]() == SHAPE
+    assert calls(L, one, tokens(), rows=A, n_rows=top)["append"]() == SHAPE
+    assert calls(L, one, tokens(total=top, H=1))["weigh"]() == SHAPE
+
+
 @pytest.mark.parametrize("opts", [dict(rescale_threshold=4.0), dict(poly_exp2_mask=0x11), dict(test_flags=2)])
 def test_options_that_do_not_apply(L, opts):
     run = calls(L, a_cache(), tokens(), opts=attn.make_options(**opts))
