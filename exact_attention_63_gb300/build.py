@@ -1,19 +1,22 @@
-"""Build the sm_103a shared library in-tree with nvcc (no cmake, no torch).
+"""Build the sm_103a shared library in-tree with nvcc (no cmake, no torch), and the
+compiled part of the cache operators' binding (g++, PyTorch's headers).
 
     python -m exact_attention_63_gb300.build
 
 Compiles the translation units in parallel and links
-``exact_attention_63_gb300/libattn_gb300.so``.  The library is linked
+``exact_attention_63_gb300/libattn_gb300.so`` and ``_cache_bind.so`` beside it.  The library is linked
 against the shared CUDA runtime so it uses the same runtime instance as the
 host process (PyTorch loads ``libcudart.so.13`` too).
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +29,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["attn_api.cu", "attn_static.cu", "attn_fwd_d64.cu", "attn_fwd_d64_causal.cu", "attn_fwd_d128.cu",
            "attn_fwd_d128_causal.cu", "attn_bwd.cu", "attn_fwd_fp8.cu", "cache_api.cu", "cache_attn.cu", "cache_weights.cu",
            "cache_evict.cu"]
+BIND_SOURCE = "cache_bind.cpp"
+BIND_PATH = os.path.join(PKG, "_cache_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,6 +50,14 @@ def compile_flags(extra=()):
                    *extra]
 
 
+def run(cmd, what, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stdout.write(r.stdout + r.stderr)
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -52,23 +65,35 @@ def build(verbose: bool = False, extra_flags=()) -> str:
 
     def one(src):
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose:
-            sys.stdout.write(r.stdout + r.stderr)
+        run([nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc for {src}", verbose)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    home = cuda_home(nvcc)
+    bind_obj = os.path.join(BUILD_DIR, "cache_bind.o")
+
+    def bind():
+        inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(home, "include"),
+               INCLUDE]
+        run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *("-I" + i for i in inc), "-c",
+             os.path.join(CSRC, BIND_SOURCE), "-o", bind_obj], f"compiler for {BIND_SOURCE}", verbose)
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bound = ex.submit(bind)
         objs = list(ex.map(one, SOURCES))
-    libdir = os.path.join(cuda_home(nvcc), "lib64")
+        bound.result()
+    libdir = os.path.join(home, "lib64")
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + libdir, "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + libdir, "-o", tmp, *objs], "link")
     os.replace(tmp, LIB_PATH)
+    # (torch's libraries are in the process before this one is loaded; it finds the
+    # library above beside itself)
+    tmp = BIND_PATH + ".tmp"
+    run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, "-L" + os.path.join(torch_dir, "lib"),
+         "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-L" + PKG, "-lattn_gb300",
+         "-Wl,-rpath,$ORIGIN"], "link of the binding")
+    os.replace(tmp, BIND_PATH)
     return LIB_PATH
 
 

@@ -27,7 +27,9 @@ A decoding step reads, in this order::
     kept = cache_evict(k_cache, v_cache, weights, block_table, seq_lens, budget, recent, positions, seq_pos)
     seq_lens.clamp_(max=budget)
 
-Argument marshalling only; the work runs in the library's CUDA kernels.  Lengths
+Argument marshalling only; the work runs in the library's CUDA kernels.  Dense
+tensors take the short way through ``csrc/cache_bind.cpp``; strides, options, another
+stream or device, and every refusal are dealt with here.  Lengths
 and tables stay on the device, so every call can be captured into a CUDA graph and
 replayed with other contents.  ``stream`` (default: the current one) is the stream
 the call runs on, and the one its outputs and workspace are allocated on.
@@ -37,8 +39,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import math
+import os
 import struct
 
 import torch
@@ -69,17 +73,27 @@ class NewTokens(ctypes.Structure):
                 ("max_seqlen", ctypes.c_int), ("H", ctypes.c_int)]
 
 
-# The structs as bytes in native layout: filled in one call, where a ctypes
-# structure takes one per field (a decoding step is short enough to notice).
+# The structs as bytes in native layout.
 _CACHE = struct.Struct("@N2P6q4P6i")
 _TOKENS = struct.Struct("@N3P6qP3i0P")  # (0P: padded to a pointer's alignment, as in C)
 _CACHE_SIZE, _TOKENS_SIZE = _CACHE.size, _TOKENS.size
 assert _CACHE_SIZE == ctypes.sizeof(Cache) and _TOKENS_SIZE == ctypes.sizeof(NewTokens)
 
+_BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_cache_bind.so")
+_bind = None
 
-# A decoding step's kernels take ~10 us, so the checks are written to cost little when
-# they pass: one expression over all tensors, dense ones first.  Where it does not hold,
-# the tensors are looked at one by one, for strides or for the reason of the refusal.
+
+def _load():
+    """The compiled binding (raises if it is missing)."""
+    global _bind
+    if not os.path.exists(_BIND_PATH):
+        raise RuntimeError(f"{_BIND_PATH} is missing: build it with `python -m exact_attention_63_gb300.build`")
+    attn.lib()
+    loader = importlib.machinery.ExtensionFileLoader("_cache_bind", _BIND_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache_bind", loader))
+    loader.exec_module(module)
+    _bind = module
+    return module
 
 
 def _refuse(name, t, dtype, dev, contiguous):
@@ -165,32 +179,6 @@ def _device(name, t):
 def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
     """attn_cache of the tensors, checked; (bytes, H_kv, d, n_seq).  What an operator
     does not use is None (k or weights is there)."""
-    try:
-        if (block_table.dtype is _I32 and block_table.get_device() == dev and block_table.is_contiguous()
-                and (seq_lens is None or (seq_lens.dtype is _I32 and seq_lens.get_device() == dev
-                                          and seq_lens.is_contiguous()))
-                and (k is None or (k.dtype is _BF16 and k.get_device() == dev and k.is_contiguous()))
-                and (v is None or (v.dtype is _BF16 and v.get_device() == dev and v.is_contiguous()
-                                   and v.shape == k.shape))
-                and (weights is None or (weights.dtype is _F32 and weights.get_device() == dev
-                                         and weights.is_contiguous()))
-                and (positions is None or (positions.dtype is _I32 and positions.get_device() == dev
-                                           and positions.is_contiguous()))):
-            n_seq, max_blocks = block_table.shape
-            if k is not None:
-                n_pages, page_size, hkv, d = k.shape
-            else:
-                (n_pages, hkv, page_size), d = weights.shape, 0
-            slots = (n_pages, hkv, page_size)
-            if ((seq_lens is None or seq_lens.shape == (n_seq,)) and (weights is None or weights.shape == slots)
-                    and (positions is None or positions.shape == slots)):
-                return (_CACHE.pack(_CACHE_SIZE, 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
-                                    0, 0, 0, 0, 0, 0, 0 if weights is None else weights.data_ptr(),
-                                    0 if positions is None else positions.data_ptr(), block_table.data_ptr(),
-                                    0 if seq_lens is None else seq_lens.data_ptr(), n_pages, page_size, max_blocks,
-                                    n_seq, hkv, d), hkv, d, n_seq)
-    except (AttributeError, ValueError):
-        pass
     table = _need("block_table", block_table, _I32, dev)
     n_seq, max_blocks = _shape("block_table", block_table, 2)
     vp = wp = pp = lp = 0
@@ -218,19 +206,6 @@ def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
 def _pack_tokens(dev, q, k, v, cu, n_seq, hkv, d, max_seqlen):
     """attn_new_tokens of the tensors, checked; (bytes, total, H).  q, or k and v, may
     be None."""
-    try:
-        if (cu.dtype is _I32 and cu.get_device() == dev and cu.is_contiguous() and cu.shape == (n_seq + 1,)
-                and (q is None or (q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()))
-                and (k is None or (k.dtype is _BF16 and k.get_device() == dev and k.is_contiguous()
-                                   and v.dtype is _BF16 and v.get_device() == dev and v.is_contiguous()
-                                   and k.shape == v.shape))):
-            total, H, dq = q.shape if q is not None else (k.shape[0], hkv, d)
-            if dq == d and hkv and H % hkv == 0 and (k is None or k.shape == (total, hkv, d)):
-                return (_TOKENS.pack(_TOKENS_SIZE, 0 if q is None else q.data_ptr(),
-                                     0 if k is None else k.data_ptr(), 0 if k is None else v.data_ptr(),
-                                     0, 0, 0, 0, 0, 0, cu.data_ptr(), total, max_seqlen, H), total, H)
-    except (AttributeError, ValueError):
-        pass
     cp = _seq("cu_seqlens", cu, n_seq + 1, dev)
     qp = kp = vp = 0
     qs = ks = vs = (0, 0)
@@ -287,9 +262,6 @@ def workspace_size(H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
     return int(attn.lib().attn_fwd_cache_workspace_size(H, H_kv, max_seqlen_q, d))
 
 
-_workspace_bytes = functools.lru_cache(maxsize=None)(workspace_size)
-
-
 def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q: int,
                    parents=None, scale: float | None = None, out=None, lse=None, workspace=None, stream=None,
                    options=None):
@@ -304,6 +276,13 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     ``options`` (attn.make_options): timeout_ms and the test flag apply.
     ``workspace``: a uint8 tensor of workspace_size(...) bytes, else allocated.
     """
+    if stream is None and options is None:
+        done = (_bind or _load()).attend(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
+                                         max_seqlen_q, parents, scale, out, lse, workspace)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            attn._check(done)
     dev = _device("k_cache", k_cache)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
@@ -337,7 +316,7 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     if total == 0:
         return out, lse
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
+        workspace = torch.empty(workspace_size(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
     rc = attn.lib().attn_fwd_cache(c, x, par, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(),
                                    _options(options), _stream(dev))
@@ -356,6 +335,11 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     of k_new and v_new, cu_new then counts entries of it: the accepted path of a
     drafted tree.
     """
+    if stream is None:
+        rc = (_bind or _load()).append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, rows, weights,
+                                       positions, seq_pos)
+        if rc is not None:
+            return attn._check(rc)
     dev = _device("k_cache", k_cache)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
@@ -390,6 +374,13 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     (out is then needed).  Any number of queries: a decoded token, the last window
     of a prompt or the whole of it.
     """
+    if stream is None and options is None:
+        into = weights if out is None else out
+        rc = (_bind or _load()).weigh(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, into, weights,
+                                      scale)
+        if rc is not None:
+            attn._check(rc)
+            return into
     dev = _device("k_cache", k_cache)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
@@ -429,6 +420,13 @@ def cache_select(weights, block_table, seq_lens, budget: int, recent: int = 0, p
     behind the last.  Tokens that stay below slot ``budget`` keep their slot; the
     others fill the slots that become free, both ascending.
     """
+    if stream is None:
+        done = (_bind or _load()).select(weights, block_table, seq_lens, budget, recent, positions, seq_pos, kept)
+        if done.__class__ is not int:
+            if done is not None:
+                return done
+        else:
+            attn._check(done)
     dev = _device("weights", weights)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
@@ -457,6 +455,10 @@ def cache_compact(kept, k_cache, v_cache, block_table, weights=None, positions=N
     """Move the tokens that cache_select kept, in place: for every kept[s, h, i] >=
     budget (= kept.shape[2]) the key, value, weight and position of that slot go to
     slot i.  Set seq_lens to min(seq_lens, budget) afterwards."""
+    if stream is None:
+        rc = (_bind or _load()).compact(kept, k_cache, v_cache, block_table, weights, positions)
+        if rc is not None:
+            return attn._check(rc)
     dev = _device("k_cache", k_cache)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):

@@ -180,6 +180,18 @@ def test_limits_match_the_header():
     assert int(m.group(1)) << int(m.group(2)) == cache.MAX_SELECT
 
 
+def test_compiled_binding_leaves_what_it_does_not_know_to_python(L):
+    b = cache._load()
+    t = torch.zeros(2, 2)
+    for name, n, required in (("attend", 14, 9), ("append", 11, 7), ("weigh", 10, 8), ("select", 8, 5),
+                              ("compact", 6, 4)):
+        f = getattr(b, name)
+        for args in ([t] * n, [3] * n, [None] * n, [t] * required + [None] * (n - required)):
+            assert f(*args) is None
+        with pytest.raises(TypeError):
+            f(*[t] * (n - 1))
+
+
 def test_binding_refuses_cpu_tensors_and_overlapping_rows():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     t = torch.zeros(1, 2, dtype=torch.int32)

@@ -696,6 +696,64 @@ def test_generation_with_drafts_and_eviction():
         check_state(seq_lens)
 
 
+def test_both_ways_to_the_library_agree():
+    """A named stream takes the general way, dense tensors without one the short way."""
+    import sys
+
+    c = Case([90, 33, 0], [3, 1, 2], 4, 2, 64, 16, seed=41, room=3).cuda()
+    here = torch.cuda.current_stream()
+    lens = c.seq_lens + (c.cu[1:] - c.cu[:-1])
+    rows = torch.arange(c.total - 1, -1, -1, dtype=torch.int32, device="cuda")
+
+    def state():
+        return [t.clone() for t in (c.k, c.v, torch.nan_to_num(c.weights), c.positions)]
+
+    for scale in (None, 0.25):
+        for parents in (None, c.parents):
+            ways = [cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 3, parents=parents,
+                                         scale=scale, stream=s) for s in (None, here)]
+            o, lse = ways[0]
+            assert torch.equal(o, ways[1][0]) and torch.equal(lse, ways[1][1])
+        out, ls = torch.empty_like(o), torch.empty_like(lse)
+        ws = torch.empty(cache.workspace_size(4, 2, 3, 64), dtype=torch.uint8, device="cuda")
+        refs = [sys.getrefcount(t) for t in (out, ls, ws, c.q, c.table)]
+        got = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 3, parents=c.parents,
+                                   scale=scale, out=out, lse=ls, workspace=ws)
+        assert got[0] is out and got[1] is ls and torch.equal(out, o) and torch.equal(ls, lse)
+        del got
+        assert refs == [sys.getrefcount(t) for t in (out, ls, ws, c.q, c.table)]
+        w0 = torch.rand_like(c.weights)
+        a = cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 3, w0, scale=scale, out=w0.clone())
+        b = cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 3, w0, scale=scale, out=w0.clone(), stream=here)
+        assert torch.equal(a, b)
+
+    w = torch.rand_like(c.weights)
+    for kw in (dict(positions=c.positions, seq_pos=c.seq_lens), dict()):
+        kept = [cache.cache_select(w, c.table, c.seq_lens, 20, 4, stream=s, **kw) for s in (None, here)]
+        assert torch.equal(*kept)
+        given = torch.empty_like(kept[0])
+        assert cache.cache_select(w, c.table, c.seq_lens, 20, 4, kept=given, **kw) is given
+        assert torch.equal(given, kept[0])
+
+    first = [t.clone() for t in (c.k, c.v, c.weights, c.positions)]
+    results = []
+    for s in (None, here):
+        for t, t0 in zip((c.k, c.v, c.weights, c.positions), first):
+            t.copy_(t0)
+        cache.cache_append(c.k_new, c.v_new, c.k, c.v, c.table, lens, c.cu, rows=rows, weights=c.weights,
+                           positions=c.positions, seq_pos=lens, stream=s)
+        cache.cache_compact(kept[0], c.k, c.v, c.table, c.weights, c.positions, stream=s)
+        results.append(state())
+    for x, y in zip(*results):
+        assert torch.equal(bits(x), bits(y))
+    for f, args in ((cache.cache_select, (w, c.table, c.seq_lens, 8, 9)),
+                    (cache.cache_append, (c.k_new, c.v_new, c.k.view(-1, 8, 2, 64), c.v.view(-1, 8, 2, 64), c.table,
+                                          c.seq_lens, c.cu))):
+        for s in (None, here):
+            with pytest.raises(attn.AttnError):
+                f(*args, stream=s)
+
+
 def test_binding_refuses_what_does_not_fit():
     """Wrong types, shapes, devices and strides are ValueErrors that name the tensor."""
     c = Case([40, 20], [2, 1], 4, 2, 64, 16, seed=40).cuda()
