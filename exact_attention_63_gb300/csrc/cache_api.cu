@@ -274,7 +274,18 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   a.p.piece = piece_of(c.page_size);
   a.p.scale_log2 = scale * 1.4426950408889634f;
   a.p.inv_scale = 1.f / scale;
+  a.tiles = static_cast<int>(tiles);
   a.grid = tiles < sms ? static_cast<int>(tiles) : sms;
+  // CTAs that share a tile, where its rows make 8 chunks and more (of 4, a second CTA
+  // cost more than it gave).  The tiles are known on the device only.  As many as the
+  // table has room for decide on clusters of 8 and 4, which leave SMs without work if
+  // there are more tiles than expected.  Clusters of 2 fill the GPU and part where the
+  // tiles are many; they are launched if whole prompts of these rows make few enough.
+  // At 1.5 tiles an SM one CTA a tile is as fast (times in cache_weights.cu).
+  const long long prompts = c.hkv * (c.total / 256ll + c.n_seq);
+  a.p.share_most = 3 * sms / 2;
+  if ((c.max_new + a.p.nt - 1) / a.p.nt >= 8 && (tiles < prompts ? tiles : prompts) <= a.p.share_most)
+    a.p.log_split = 8 * tiles <= 2ll * sms ? 3 : (4 * tiles <= 2ll * sms ? 2 : 1);
   a.stream = stream;
   if ((rc = encode_queries(&a.q, x, c, qs, a.p.nt)) != ATTN_OK || (rc = encode_pages(&a.k, c.k, c, c.k_st, a.p.piece)) != ATTN_OK)
     return rc;

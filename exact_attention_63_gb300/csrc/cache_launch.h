@@ -81,6 +81,8 @@ struct CacheWeightParams {
   int n_cols;            // its rows rounded up to the MMA's multiple of 16
   int k_stages, q_stages;  // key slots of a half, chunk slots (set by the launch)
   int piece;
+  int log_split;         // 2^log_split CTAs share a tile,
+  int share_most;        // if there are no more tiles than these
   float scale_log2, inv_scale;
   unsigned int* status;
   uint64_t timeout_ns;
@@ -89,7 +91,8 @@ struct CacheWeightParams {
 struct CacheWeightLaunch {
   CUtensorMap q, k;
   CacheWeightParams p;
-  int grid, device;
+  int tiles;             // at most, by the table's capacity
+  int grid, device;      // grid: of CTAs that share no tiles
   cudaStream_t stream;
 };
 cudaError_t launch_cache_weights(const CacheWeightLaunch& a);

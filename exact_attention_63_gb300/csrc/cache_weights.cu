@@ -15,6 +15,14 @@
 // tiles, which most rows see, first, and every second round of CTAs in reverse,
 // so that the heaviest tiles and the lightest go to the same CTA.
 //
+// Where there are few tiles for the SMs (a prompt of 1000 tokens, 8 key heads: 32), a
+// cluster of 2, 4 or 8 CTAs takes a tile together (SHARED): each has a run of the tile's
+// chunks, and the first adds the others' sums, written into its shared memory, in order.
+// Whole prompts, 8 key heads, group 4, d = 128, one CTA a tile and then 2, 4, 8 (us):
+// 1500 tokens 48, 32, 22, 28; 2500 tokens 74, 46, 39, 55; 5000 tokens 136, 93, 112, 154;
+// 8000 tokens 211, 215, 238, 334.  (Each CTA loads the tile's keys, and clusters of 8
+// leave a third of the SMs without work.)
+//
 // The −LSE of a column comes out of the tensor core with the score: one more step
 // of 16 along the product's inner dimension multiplies a constant (1, 1, 1, 0, …) on
 // the keys' side with (hi, mid, lo, 0, …) on the rows', three bf16 numbers that add
@@ -50,13 +58,14 @@ struct WL {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kSlot = 128u * D * 2;   // 128 keys: [half][128 rows][128 B]
   static constexpr uint32_t kOnes = 0;              // the keys' side of the added step, 4 KB
-  static constexpr int kNumBars = 4 * kMaxHalf + 2 * kMaxChunks + 10;
+  static constexpr int kNumBars = 4 * kMaxHalf + 2 * kMaxChunks + 26;
   static constexpr uint32_t kBar = kOnes + 4096;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
   static constexpr uint32_t kSums = kMisc + 8;
   static constexpr uint32_t kTable = (kSums + 80 + 15) & ~15u;
   // then the table of n_seq + 1 ints, three ints a sequence, and from a 1024-byte
-  // boundary the key rings, the chunks and the rows' sides of their added steps
+  // boundary the key rings, the chunks, the rows' sides of their added steps and the
+  // other CTAs' sums of a tile
   __host__ __device__ static uint32_t rings(int n_seq) { return (kTable + 4u * (4 * n_seq + 1) + 1023u) & ~1023u; }
 };
 
@@ -66,6 +75,24 @@ struct WL {
 __device__ __forceinline__ uint64_t sdesc_added(uint32_t saddr, int rows) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(rows) << 16) |
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// The address in CTA `rank` of the cluster of what is at `saddr` here.
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_in_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Every thread of the cluster's CTAs comes here.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // A ring's next slot and the parity of its use (a division by the run-time number of
@@ -84,11 +111,13 @@ struct Ring {
 struct WTile {
   int s, h, j0;       // keys [j0, j0 + 256) of sequence s, head h
   int q0, n, rows, len;  // its query rows: first packed row, all of them, those within max_new
-  int c0, c1;         // chunks that see a key of the tile
+  int c0, c1;         // chunks that see a key of the tile: this CTA's share of them
+  bool seen;          // whether there are any
 };
 
-// `from`: a sequence known to begin at or before tile u (the last one asked for).
-__device__ __forceinline__ WTile tile_at(const CacheWeightParams& p, const int* tab, int u, int from = 0) {
+// `rank`: in the cluster of 2^log_split CTAs that share the tile.  `from`: a sequence
+// known to begin at or before tile u (the last one asked for).
+__device__ __forceinline__ WTile tile_at(const CacheWeightParams& p, const int* tab, int u, int rank, int log_split, int from = 0) {
   WTile t;
   t.s = u < tab[from + 1] ? from : find_seq(tab, p.c.n_seq, u, from);
   const int* const seq = tab + p.c.n_seq + 1 + 3 * t.s;  // its first row, rows and length
@@ -103,16 +132,25 @@ __device__ __forceinline__ WTile tile_at(const CacheWeightParams& p, const int* 
   const int first = max(0, t.j0 - t.len + t.n);
   t.c0 = p.by_nt(first);
   t.c1 = max(t.c0, p.by_nt(t.rows + p.nt - 1));
+  t.seen = t.c0 < t.c1;
+  if (log_split > 0) {
+    const int begin = t.c0;
+    const long long all = t.c1 - t.c0;
+    t.c0 = begin + static_cast<int>(all * rank >> log_split);
+    t.c1 = begin + static_cast<int>(all * (rank + 1) >> log_split);
+  }
   return t;
 }
 
-// The n-th tile of a CTA, or -1: rounds of `grid` tiles, every second in reverse.
+// The n-th tile of a CTA (or cluster), or -1: rounds of `grid` tiles, every second in
+// reverse.
 __device__ __forceinline__ int tile_of(int n, int cta, int grid, int units) {
   const long long u = static_cast<long long>(n) * grid + ((n & 1) ? grid - 1 - cta : cta);
   return u < units ? static_cast<int>(u) : -1;
 }
 
-template <int D>
+// SHARED: clusters share the tiles.
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreadsCW, 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const CacheWeightParams p) {
@@ -130,18 +168,22 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   auto s_full = [&](int w, int i) { return bars + 8u * (kB + 2 * w + i); };
   auto s_free = [&](int w, int i) { return bars + 8u * (kB + 4 + 2 * w + i); };
   auto done = [&](int w) { return bars + 8u * (kB + 8 + w); };
+  // Of sum warp i: in the first CTA, the others' sums of its keys are there; in the
+  // others, the first has taken them.
+  auto part_full = [&](int i) { return bars + 8u * (kB + 10 + i); };
+  auto part_free = [&](int i) { return bars + 8u * (kB + 18 + i); };
   const int kst = p.k_stages, qst = p.q_stages;  // key slots of a half, chunks
   const uint32_t q_half = static_cast<uint32_t>(p.n_cols) * 128u, q_bytes = q_half * L::kHalves;
   const uint32_t c_bytes = static_cast<uint32_t>(p.n_cols) * 32u;
   const uint32_t ring_k = base + L::rings(p.c.n_seq), ring_q = ring_k + 2 * kst * L::kSlot;
   const uint32_t ring_c = ring_q + qst * q_bytes;
+  const uint32_t parts = ring_c + qst * c_bytes;  // [others][256]
   auto k_slot = [&](int w, int s) { return ring_k + (w * kst + s) * L::kSlot; };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, grid = gridDim.x;
 
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -166,6 +208,10 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       }
       mbar_init(done(w), 1);
     }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(part_full(i), SHARED ? (1 << p.log_split) - 1 : 1);
+      mbar_init(part_free(i), 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -185,8 +231,12 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     seq[2] = len;
     return p.c.hkv * ((len + kTileKeys - 1) / kTileKeys);
   });
+  if constexpr (SHARED) cluster_sync();  // (the barriers are ready for the other CTAs)
   tc_fence_after();
   const int units = tab[p.c.n_seq];
+  // Tiles are dealt out to clusters, `cta` of `grid`; more tiles than p.share_most to single CTAs.
+  const int log_split = SHARED && units <= p.share_most ? p.log_split : 0, split = 1 << log_split;
+  const int rank = blockIdx.x & (split - 1), cta = blockIdx.x >> log_split, grid = gridDim.x >> log_split;
   if (tile_of(0, cta, grid, units) < 0) {
     if (warp == 0) tmem_dealloc(*tmem_slot, 512);
     return;
@@ -221,7 +271,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       const int u = tile_of(n, cta, grid, units);
       there[i] = u >= 0;
       if (there[i]) {
-        t[i] = tile_at(p, tab, u, from);
+        t[i] = tile_at(p, tab, u, rank, log_split, from);
         locate(t[i], page[i], slot[i]);
       }
     };
@@ -286,7 +336,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       Ring rk{kst}, rq{qst};
       bool ok = true;
       for (int n = 0, u; ok && (u = tile_of(n, cta, grid, units)) >= 0; ++n) {
-        const WTile t = tile_at(p, tab, u, from);
+        const WTile t = tile_at(p, tab, u, rank, log_split, from);
         from = t.s;
         if (t.c0 == t.c1) continue;
         // A tile's second half may have no keys: its issuer only keeps count.
@@ -335,14 +385,14 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     }
     // The chunk after (n, t, c) of this CTA; false at the end.
     int n = 0, u = tile_of(0, cta, grid, units);
-    WTile t = tile_at(p, tab, u);
+    WTile t = tile_at(p, tab, u, rank, log_split);
     int c = t.c0 - 1;
     auto advance = [&]() -> bool {
       ++c;
       while (c >= t.c1) {
         u = tile_of(++n, cta, grid, units);
         if (u < 0) return false;
-        t = tile_at(p, tab, u, t.s);
+        t = tile_at(p, tab, u, rank, log_split, t.s);
         c = t.c0;
       }
       return true;
@@ -406,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2);
     // The weight gathered so far by this thread's key of tile t: where it is, and
     // the load, issued a tile ahead (under a full memory pipe it takes as long as a
-    // tile of few rows).
+    // tile of few rows; shared tiles have many, and registers are short there).
     auto fetch = [&](const WTile& t, long long& at, float& start) {
       const int key = t.j0 + row;
       at = -1;
@@ -420,18 +470,20 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         }
       }
     };
-    int nq = 0;
+    int nq = 0, given = 0;  // chunks; tiles whose sums went from CTA to CTA
     bool ok = true;
     int u = tile_of(0, cta, grid, units);
-    WTile t = tile_at(p, tab, u), t_next = t;
-    long long at, at_next = -1;
-    float start, start_next = 0.f;
-    fetch(t, at, start);
+    WTile t = tile_at(p, tab, u, rank, log_split), t_next = t;
+    long long at = -1, at_next = -1;
+    float start = 0.f, start_next = 0.f;
+    if constexpr (!SHARED) fetch(t, at, start);
     for (int n = 0; u >= 0; ++n, t = t_next, at = at_next, start = start_next) {
       u = tile_of(n + 1, cta, grid, units);
-      if (u >= 0) {
-        t_next = tile_at(p, tab, u, t.s);
-        fetch(t_next, at_next, start_next);
+      if constexpr (!SHARED) {
+        if (u >= 0) {
+          t_next = tile_at(p, tab, u, rank, log_split, t.s);
+          fetch(t_next, at_next, start_next);
+        }
       }
       const int key = t.j0 + row;
       const bool live = t.j0 + 128 * w + (warp & 3) * 32 < t.len;  // this warp has a key
@@ -499,6 +551,30 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         total += a0 + a1;
       }
       if (!ok) break;
+      if constexpr (SHARED) {
+        if (rank == 0) fetch(t, at, start);
+        if (u >= 0) t_next = tile_at(p, tab, u, rank, log_split, t.s);
+      }
+      if (SHARED && split > 1 && t.seen && live) {
+        const int i = warp - 4;
+        if (rank > 0) {
+          if (given > 0 && __any_sync(0xffffffffu, !wait_bar_cold(part_free(i), (given - 1) & 1, wc))) break;
+          fence_cluster();
+          store_in_cluster(in_cta(parts + 4u * (256 * (rank - 1) + row), 0), total);
+          fence_cluster();
+          __syncwarp();
+          if (lane == 0) arrive_in_cluster(in_cta(part_full(i), 0));
+        } else {
+          if (__any_sync(0xffffffffu, !wait_bar_cold(part_full(i), given & 1, wc))) break;
+          fence_cluster();
+          for (int r = 1; r < split; ++r)
+            total += *reinterpret_cast<volatile float*>(smem + (parts - base) + 4 * (256 * (r - 1) + row));
+          fence_cluster();
+          __syncwarp();
+          if (lane > 0 && lane < split) arrive_in_cluster(in_cta(part_free(i), lane));
+        }
+        ++given;
+      }
       if (at >= 0) p.out[at] = start + total;
     }
   }
@@ -509,34 +585,69 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (SHARED) cluster_sync();  // no CTA ends while another may write into it
 }
 
+// Clusters of 2^log CTAs that run at a time (they do not cross the GPU's processor
+// clusters, so larger ones leave some SMs without work), or 0.
 template <int D>
+int clusters_at_a_time(int device, int log, const cudaLaunchConfig_t& cfg) {
+  static volatile int known[64][4] = {};
+  int n = known[device][log];
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, cache_weights_kernel<D, true>, &cfg) != cudaSuccess) return 0;
+    known[device][log] = n;
+  }
+  return n;
+}
+
+template <int D, bool SHARED>
 cudaError_t launch(const CacheWeightLaunch& a) {
   CacheWeightParams p = a.p;
+  if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
+  static volatile bool configured[64] = {};
+  if (!configured[a.device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(cache_weights_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e != cudaSuccess) return e;
+    configured[a.device] = true;
+  }
   // Up to four chunks in flight, and the keys get the rest: a slot for each half (one
   // tile) at least.
-  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq);
+  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq) - ((1u << p.log_split) - 1u) * 1024u;
   const uint32_t chunk = static_cast<uint32_t>(p.n_cols) * (D * 2 + 32);
   p.q_stages = kMaxChunks;
   while (room - p.q_stages * chunk < 2 * WL<D>::kSlot) --p.q_stages;  // many sequences: their table takes room
   const uint32_t k_stages = (room - p.q_stages * chunk) / (2 * WL<D>::kSlot);
   p.k_stages = static_cast<int>(k_stages < kMaxHalf ? k_stages : kMaxHalf);
-  const uint32_t smem = WL<D>::rings(p.c.n_seq) + 2 * p.k_stages * WL<D>::kSlot + p.q_stages * chunk + 1024u;
-  static volatile bool configured[64] = {};
-  if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
-  if (!configured[a.device]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(cache_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-    if (e != cudaSuccess) return e;
-    configured[a.device] = true;
+  const uint32_t smem = 232448u - room + 2 * p.k_stages * WL<D>::kSlot + p.q_stages * chunk;
+  if constexpr (!SHARED) {
+    cache_weights_kernel<D, false><<<a.grid, kThreadsCW, smem, a.stream>>>(a.q, a.k, p);
+    return cudaGetLastError();
+  } else {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << p.log_split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << p.log_split);
+    cfg.blockDim = dim3(kThreadsCW);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int n = clusters_at_a_time<D>(a.device, p.log_split, cfg);
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    cfg.gridDim.x = static_cast<unsigned int>(n < a.tiles ? n : a.tiles) << p.log_split;
+    return cudaLaunchKernelEx(&cfg, cache_weights_kernel<D, true>, a.q, a.k, p);
   }
-  cache_weights_kernel<D><<<a.grid, kThreadsCW, smem, a.stream>>>(a.q, a.k, p);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_weights(const CacheWeightLaunch& a) { return a.p.c.d == 64 ? launch<64>(a) : launch<128>(a); }
+cudaError_t launch_cache_weights(const CacheWeightLaunch& a) {
+  if (a.p.c.d == 64) return a.p.log_split > 0 ? launch<64, true>(a) : launch<64, false>(a);
+  return a.p.log_split > 0 ? launch<128, true>(a) : launch<128, false>(a);
+}
 
 }  // namespace attn

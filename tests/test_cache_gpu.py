@@ -306,6 +306,47 @@ def test_weights_of_short_and_long_tiles_in_turn(d, prompt):
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,H,hkv,slack", [
+    ([700], [700], 8, 1, 0),                # 3 tiles: clusters of 8
+    ([1300, 40], [1300, 30], 16, 2, 0),     # 24: 8, some CTAs without a chunk
+    ([2300, 513, 1], [600, 513, 0], 4, 2, 0),    # 60: 4; no new rows in one
+    ([700, 300, 130], [700, 300, 130], 14, 2, 40000),  # a large table: clusters of 2
+    ([900] * 60, [9] * 60, 128, 1, 0),      # more tiles than the clusters share
+])
+def test_weights_of_shared_tiles(lens, new, H, hkv, slack, d):
+    """Few tiles: clusters share them, and the sums come together in a fixed order."""
+    c = Case(lens, new, H, hkv, d, 16, seed=25).cuda()
+    c.table = torch.nn.functional.pad(c.table, (0, slack // 16), value=-1).contiguous()
+    start = f64(c.weights)
+    lse = (torch.randn((H, c.total), generator=torch.Generator().manual_seed(2)) * 0.1 + 6.0).cuda()
+    first = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, start, first)
+    unused = torch.isnan(c.weights)
+    assert (first[unused] == 0).all()
+    for _ in range(50):
+        assert torch.equal(weigh(c, lse, out=torch.zeros_like(c.weights)), first)
+    g, outs = torch.cuda.CUDAGraph(), [torch.zeros_like(first) for _ in range(2)]
+    with torch.cuda.graph(g):
+        for o in outs:
+            weigh(c, lse, out=o)
+    c.seq_lens.sub_(torch.minimum(c.seq_lens - c.cu.diff(), torch.tensor(3, device="cuda")).clamp(min=0))
+    g.replay()
+    c.lens = c.seq_lens.tolist()
+    check_weights(c, lse, start, outs[0])
+    assert torch.equal(outs[0], outs[1])
+
+
+def test_wait_limit_of_shared_tiles():
+    """Copies that never come: every CTA of the cluster gives up and the call returns."""
+    c = Case([900], [900], 8, 1, 64, 16, seed=26).cuda()
+    lse = torch.full((8, 900), 6.0, device="cuda")
+    weigh(c, lse, out=torch.zeros_like(c.weights), options=attn.make_options(timeout_ms=50, test_flags=attn.TEST_WITHHOLD_KV))
+    assert attn.get_status() == -8
+    first = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, f64(c.weights), first)
+
+
 def test_weights_strided_queries_and_pages():
     H, hkv, d = 6, 2, 64
     c = Case([300, 70], [40, 1], H, hkv, d, 16, seed=4).cuda()
