@@ -951,10 +951,12 @@ cudaError_t launch(const CacheAttnLaunch& a) {
   const int mt_max = (p.c.max_new + p.ntt - 1) / p.ntt;
   const long long tiles = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max;
   const bool wide = p.rows > kWideRows;
-  // A row a block where a tile has 8 parts or more on average (at 512 tiles of 4 rows,
-  // 2048 such blocks took 10 us more than 512 of the other kind; at 2 tiles, 152 parts,
-  // the other kind would read them one after the other).
-  const bool few = !wide && tiles * 8 <= a.grid;
+  // A row a block where a tile has many parts on average, which the other kind reads one
+  // after the other, or where there are few such blocks for the GPU (GPU time of a whole
+  // call, so and otherwise: 8 tiles of 48 rows in 152 parts 21 and 34 us at d = 128; 64
+  // tiles of 4 rows 19 and 23 us at d = 64, 23 and 24 us at 128; 256 tiles of 4 rows 57
+  // and 52 us at 128; 32 tiles of 32 rows 22 and 20 us at 128, 16 and 20 us at 64).
+  const bool few = !wide && (tiles * D <= 8ll * a.grid || tiles * p.rows * D <= 128ll * a.grid);
   const long long blocks = tiles * (few ? p.rows : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.
