@@ -281,11 +281,13 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   // table has room for decide on clusters of 8 and 4, which leave SMs without work if
   // there are more tiles than expected.  Clusters of 2 fill the GPU and part where the
   // tiles are many; they are launched if whole prompts of these rows make few enough.
-  // At 1.5 tiles an SM one CTA a tile is as fast (times in cache_weights.cu).
+  // The bounds are where the times in cache_weights.cu cross: 512 tiles of up to 63
+  // chunks take 150 us shared by two and 185 otherwise, of up to 32 chunks 91 and 84.
+  const int chunks = (c.max_new + a.p.nt - 1) / a.p.nt;
   const long long prompts = c.hkv * (c.total / 256ll + c.n_seq);
-  a.p.share_most = 3 * sms / 2;
-  if ((c.max_new + a.p.nt - 1) / a.p.nt >= 8 && (tiles < prompts ? tiles : prompts) <= a.p.share_most)
-    a.p.log_split = 8 * tiles <= 2ll * sms ? 3 : (4 * tiles <= 2ll * sms ? 2 : 1);
+  a.p.share_most = (chunks >= 48 ? 4 : 2) * sms;
+  if (chunks >= 8 && (tiles < prompts ? tiles : prompts) <= a.p.share_most)
+    a.p.log_split = chunks >= 64 && 4 * tiles <= sms ? 3 : (8 * tiles <= 5ll * sms ? 2 : 1);
   a.stream = stream;
   if ((rc = encode_queries(&a.q, x, c, qs, a.p.nt)) != ATTN_OK || (rc = encode_pages(&a.k, c.k, c, c.k_st, a.p.piece)) != ATTN_OK)
     return rc;

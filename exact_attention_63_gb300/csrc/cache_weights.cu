@@ -19,9 +19,11 @@
 // cluster of 2, 4 or 8 CTAs takes a tile together (SHARED): each has a run of the tile's
 // chunks, and the first adds the others' sums, written into its shared memory, in order.
 // Whole prompts, 8 key heads, group 4, d = 128, one CTA a tile and then 2, 4, 8 (us):
-// 1500 tokens 48, 32, 22, 28; 2500 tokens 74, 46, 39, 55; 5000 tokens 136, 93, 112, 154;
-// 8000 tokens 211, 215, 238, 334.  (Each CTA loads the tile's keys, and clusters of 8
-// leave a third of the SMs without work.)
+// 1000 tokens 32, 21, 15, 18; 2500 tokens 70, 41, 34, 43; 5000 tokens 133, 85, 95, 122;
+// 8000 tokens 210, 202, 213, 275; 4000 tokens, 2 key heads, group 8 206, 111, 60, 44.
+// (Each CTA loads the tile's keys, and clusters of 8 leave SMs without work.)
+//   On the diagonal a warp skips the groups of 32 columns that none of its keys is seen
+// by: its chunks have a CTA of their own in a cluster, which the others would wait for.
 //
 // The −LSE of a column comes out of the tensor core with the score: one more step
 // of 16 along the product's inner dimension multiplies a constant (1, 1, 1, 0, …) on
@@ -527,19 +529,23 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
             const int first = masked ? max(0, min(key - (t.len - t.n) - tok0, 128)) * grp : 0;
 #pragma unroll 1
             for (int cc = 0; cc < valid; cc += 32) {
+              const int from = min(max(first - cc, 0), 32), to = min(valid - cc, 32);
+              const uint32_t sees = (from == 32 ? 0u : ~0u << from) & (to == 32 ? ~0u : (1u << to) - 1u);
+              if (!__any_sync(0xffffffffu, sees != 0u)) continue;
               tmem_ld32(tS + cc, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
               tmem_wait_ld();
               loaded(0);
-              if (cc + 32 <= valid && !masked) {
+              if (__all_sync(0xffffffffu, sees == ~0u)) {
                 sum_all(0);
               } else {
-                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float a = ex2_mufu(__uint_as_float(x[i]) * p.scale_log2);
-                  sum += cc + i < valid && cc + i >= first ? a : 0.f;
+                for (int i = 0; i < 16; ++i) {
+                  float a, b;
+                  unpack2(fmul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2), a, b);
+                  a = ex2_mufu(a);
+                  b = ex2_mufu(b);
+                  acc[i & 1] = fadd2(acc[i & 1], pack2((sees >> (2 * i)) & 1u ? a : 0.f, (sees >> (2 * i + 1)) & 1u ? b : 0.f));
                 }
-                acc[0] = fadd2(acc[0], pack2(sum, 0.f));
               }
             }
           }

@@ -308,8 +308,9 @@ def test_weights_of_short_and_long_tiles_in_turn(d, prompt):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("lens,new,H,hkv,slack", [
-    ([700], [700], 8, 1, 0),                # 3 tiles: clusters of 8
-    ([1300, 40], [1300, 30], 16, 2, 0),     # 24: 8, some CTAs without a chunk
+    ([700], [700], 8, 1, 0),                # 3 tiles: clusters of 4
+    ([1100, 300], [1100, 90], 8, 1, 0),     # 10 tiles, 69 chunks: clusters of 8, some CTAs without a chunk
+    ([1300, 40], [1300, 30], 16, 2, 0),
     ([2300, 513, 1], [600, 513, 0], 4, 2, 0),    # 60: 4; no new rows in one
     ([700, 300, 130], [700, 300, 130], 14, 2, 40000),  # a large table: clusters of 2
     ([900] * 60, [9] * 60, 128, 1, 0),      # more tiles than the clusters share
