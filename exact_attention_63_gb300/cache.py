@@ -96,6 +96,12 @@ def _load():
     return module
 
 
+def _first(name, t):
+    """The compiled binding, for the first call: t has to be what needs it."""
+    _device(name, t)
+    return _load()
+
+
 def _refuse(name, t, dtype, dev, contiguous):
     """The reason why _need or _rows refused t."""
     if not isinstance(t, torch.Tensor):
@@ -277,8 +283,9 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
     ``workspace``: a uint8 tensor of workspace_size(...) bytes, else allocated.
     """
     if stream is None and options is None:
-        done = (_bind or _load()).attend(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
-                                         max_seqlen_q, parents, scale, out, lse, workspace)
+        bind = _bind or _first("k_cache", k_cache)
+        done = bind.attend(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q,
+                           parents, scale, out, lse, workspace)
         if done.__class__ is tuple:
             return done
         if done is not None:
@@ -336,8 +343,8 @@ def cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, 
     drafted tree.
     """
     if stream is None:
-        rc = (_bind or _load()).append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, rows, weights,
-                                       positions, seq_pos)
+        bind = _bind or _first("k_cache", k_cache)
+        rc = bind.append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_new, rows, weights, positions, seq_pos)
         if rc is not None:
             return attn._check(rc)
     dev = _device("k_cache", k_cache)
@@ -376,8 +383,8 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     """
     if stream is None and options is None:
         into = weights if out is None else out
-        rc = (_bind or _load()).weigh(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, into, weights,
-                                      scale)
+        bind = _bind or _first("k_cache", k_cache)
+        rc = bind.weigh(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, into, weights, scale)
         if rc is not None:
             attn._check(rc)
             return into
@@ -421,12 +428,12 @@ def cache_select(weights, block_table, seq_lens, budget: int, recent: int = 0, p
     others fill the slots that become free, both ascending.
     """
     if stream is None:
-        done = (_bind or _load()).select(weights, block_table, seq_lens, budget, recent, positions, seq_pos, kept)
-        if done.__class__ is not int:
-            if done is not None:
-                return done
-        else:
+        bind = _bind or _first("weights", weights)
+        done = bind.select(weights, block_table, seq_lens, budget, recent, positions, seq_pos, kept)
+        if done.__class__ is int:
             attn._check(done)
+        elif done is not None:
+            return done
     dev = _device("weights", weights)
     if _elsewhere(dev, stream):
         with _switched(dev, stream):
@@ -456,7 +463,8 @@ def cache_compact(kept, k_cache, v_cache, block_table, weights=None, positions=N
     budget (= kept.shape[2]) the key, value, weight and position of that slot go to
     slot i.  Set seq_lens to min(seq_lens, budget) afterwards."""
     if stream is None:
-        rc = (_bind or _load()).compact(kept, k_cache, v_cache, block_table, weights, positions)
+        bind = _bind or _first("k_cache", k_cache)
+        rc = bind.compact(kept, k_cache, v_cache, block_table, weights, positions)
         if rc is not None:
             return attn._check(rc)
     dev = _device("k_cache", k_cache)
