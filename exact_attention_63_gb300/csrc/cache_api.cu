@@ -134,10 +134,12 @@ int tile_tokens(int group, int max_new) {
 }
 
 // The attention kernel's row tiles, and its workspace: the sequences' table, then a
-// part (maximum and sum, output) for each end of each CTA's range.
+// part (maximum and sum, output) for each end of each CTA's range.  One row more than a
+// tile holds halves the CTAs, so more tokens may need less (`bytes`); `most` is what any
+// number of tokens up to max_new needs.
 struct Tiles {
   int nt, per_cta, ntt, rows, max_ctas;
-  size_t ml, o, bytes;
+  size_t ml, o, bytes, most;
 };
 Tiles tiles_of(int group, int max_new, int d) {
   Tiles t;
@@ -149,6 +151,9 @@ Tiles tiles_of(int group, int max_new, int d) {
   t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
   t.o = t.ml + up256(2ull * t.max_ctas * t.rows * sizeof(float2));
   t.bytes = t.o + 2ull * t.max_ctas * t.rows * d * sizeof(float);
+  // With two tiles a CTA 2·160 ends of at most 2·nt·group rows: no more than one full tile's
+  // 2·320 ends of nt·group.
+  t.most = t.per_cta == 2 ? tiles_of(group, t.nt, d).bytes : t.bytes;
   return t;
 }
 
@@ -160,7 +165,7 @@ size_t attn_fwd_cache_workspace_size(int H, int num_kv_heads, int max_seqlen, in
   if (H < 1 || num_kv_heads < 1 || H % num_kv_heads != 0 || H / num_kv_heads > 128 || max_seqlen < 1 ||
       max_seqlen > ATTN_CACHE_MAX_NEW || (d != 64 && d != 128))
     return 0;
-  return tiles_of(H / num_kv_heads, max_seqlen, d).bytes;
+  return tiles_of(H / num_kv_heads, max_seqlen, d).most;
 }
 
 int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int* parents, float scale, void* o,

@@ -483,7 +483,8 @@ typedef struct attn_new_tokens {
  *             as they were.
  *   workspace : device, 256-byte aligned, at least
  *             attn_fwd_cache_workspace_size(H, num_kv_heads, max_seqlen, d)
- *             bytes; its contents on entry do not matter.  Calls that overlap
+ *             bytes, which suffice for every smaller max_seqlen and any total
+ *             too; its contents on entry do not matter.  Calls that overlap
  *             on the GPU need workspaces of their own.
  *   opts    : timeout_ms and ATTN_TEST_WITHHOLD_KV apply; the rest must be zero.
  * max_seqlen is at most ATTN_CACHE_MAX_NEW.  The keys of a sequence are split

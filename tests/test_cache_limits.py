@@ -1,0 +1,28 @@
+"""Calls at the edges of what the cache operators' contract allows, as far as the CPU
+can tell: sizes, build, the host's arithmetic (no GPU needed)."""
+
+from __future__ import annotations
+
+import itertools
+
+import pytest
+import torch
+
+from exact_attention_63_gb300 import cache
+from test_cache_abi import ARCH, WORKSPACE, L, a_cache, calls, tokens  # noqa: F401
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 7, 8, 16, 33, 64, 128])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_workspace_serves_every_smaller_call(L, group, d):  # noqa: F811
+    """The size for a max_seqlen is enough for each call of no larger max_seqlen, and where
+    total is the smaller: the device is reached (here: missing)."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: the calls would reach it")
+    sizes = [cache.workspace_size(2 * group, 2, m, d) for m in range(1, cache.MAX_NEW + 1)]
+    assert sizes == sorted(sizes)
+    for most, total in itertools.product((1, 2, 9, 16, 17, 20, 33, 40, 65, 100, 128), (1, 8, 16, 18, 30, 32, 60, 128)):
+        run = calls(L, a_cache(d=d), tokens(total=total, max_seqlen=most, H=2 * group), ws_bytes=sizes[most - 1])
+        assert run["attend"]() == ARCH, (most, total)
+    run = calls(L, a_cache(d=d), tokens(total=128, max_seqlen=1, H=2 * group), ws_bytes=sizes[0] - 1)
+    assert run["attend"]() == WORKSPACE
