@@ -320,8 +320,10 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
         ++nv;
       }
     }
-    // No copy may be in flight when the CTA ends (only possible after an abort).
-    if (lane == 0 && !ok) {
+    // No copy may be in flight when the CTA ends (the newest of each slot; older ones
+    // landed before their slot was filled again).  Another warp's wait may have run out
+    // after the last copy was issued, so this does not depend on `ok`.
+    if (lane == 0) {
       const uint64_t t0 = globaltimer_ns();
       auto drain = [&](uint32_t bar, uint32_t parity) {
         while (!mbar_try_wait(bar, parity))

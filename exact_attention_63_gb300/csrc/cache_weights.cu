@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         if (there[i]) from = t[i].s;
       }
     }
-    if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
+    if (lane == 0) {  // no copy may be in flight when the CTA ends, even if only another warp's wait ran out
       const uint64_t t0 = globaltimer_ns();
       auto drain = [&](uint32_t bar, uint32_t parity) {
         while (!mbar_try_wait(bar, parity))
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       fence_proxy_async_smem();
       warp_arrive(q_full(qs), lane);
     }
-    if (lane == 0 && !ok) {  // no copy may be in flight when the CTA ends
+    if (lane == 0) {  // no copy may be in flight when the CTA ends, even if only another warp's wait ran out
       const uint64_t t0 = globaltimer_ns();
       for (int i = max(0, nq - qst); i < nq; ++i)
         while (!mbar_try_wait(q_full(i % qst), (i / qst) & 1u))

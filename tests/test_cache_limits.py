@@ -4,11 +4,13 @@ can tell: sizes, build, the host's arithmetic (no GPU needed)."""
 from __future__ import annotations
 
 import itertools
+import os
+import re
 
 import pytest
 import torch
 
-from exact_attention_63_gb300 import cache
+from exact_attention_63_gb300 import build, cache
 from test_cache_abi import ARCH, WORKSPACE, L, a_cache, calls, tokens  # noqa: F401
 
 
@@ -26,3 +28,14 @@ def test_a_workspace_serves_every_smaller_call(L, group, d):  # noqa: F811
         assert run["attend"]() == ARCH, (most, total)
     run = calls(L, a_cache(d=d), tokens(total=128, max_seqlen=1, H=2 * group), ws_bytes=sizes[0] - 1)
     assert run["attend"]() == WORKSPACE
+
+
+@pytest.mark.parametrize("source,loaders", [("cache_attn.cu", 1), ("cache_weights.cu", 2)])
+def test_a_loader_waits_for_its_copies_whatever_ended_it(source, loaders):
+    """A copy that lands in shared memory after its CTA has ended lands in another CTA's.  Where only the
+    consumer's wait ran out the loader has seen nothing of it, so its last waits depend on no flag."""
+    with open(os.path.join(build.CSRC, source)) as f:
+        text = f.read()
+    waits = re.findall(r"if \(([^\n]*)\) \{[^\n]*\n\s*const uint64_t t0 = globaltimer_ns\(\);\n(?:\s*auto drain|\s*for \(int i = max)",
+                       text)
+    assert waits == ["lane == 0"] * loaders
