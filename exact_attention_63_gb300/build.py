@@ -1,5 +1,6 @@
-"""Build the sm_103a shared library in-tree with nvcc (no cmake, no torch), and the
-compiled part of the cache operators' binding (g++, PyTorch's headers).
+"""Build the sm_103a shared library in-tree with nvcc (no cmake, no torch), and, where
+PyTorch is installed, the compiled part of the cache operators' Python binding (g++,
+PyTorch's headers).
 
     python -m exact_attention_63_gb300.build
 
@@ -58,7 +59,28 @@ def run(cmd, what, verbose=False):
         sys.stdout.write(r.stdout + r.stderr)
 
 
+def torch_dir():
+    """Where PyTorch (with CUDA) is installed, or None."""
+    spec = importlib.util.find_spec("torch")
+    for path in (spec.submodule_search_locations or []) if spec else []:
+        if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")):
+            return path
+    return None
+
+
+def compile_bind(torch, cuda, verbose=False):
+    """Object of the binding against the PyTorch in `torch` and the toolkit in `cuda`."""
+    obj = os.path.join(BUILD_DIR, "cache_bind.o")
+    inc = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), INCLUDE]
+    run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *("-I" + i for i in inc), "-c",
+         os.path.join(CSRC, BIND_SOURCE), "-o", obj], f"compiler for {BIND_SOURCE}", verbose)
+    return obj
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
+    """The library, which needs nvcc alone; then the binding, where PyTorch is installed.  What fails of
+    the binding is raised when the library is in place."""
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
     flags = compile_flags(extra_flags)
@@ -68,29 +90,22 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         run([nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc for {src}", verbose)
         return obj
 
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     home = cuda_home(nvcc)
-    bind_obj = os.path.join(BUILD_DIR, "cache_bind.o")
-
-    def bind():
-        inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
-               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(home, "include"),
-               INCLUDE]
-        run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *("-I" + i for i in inc), "-c",
-             os.path.join(CSRC, BIND_SOURCE), "-o", bind_obj], f"compiler for {BIND_SOURCE}", verbose)
-
+    torch = torch_dir()
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bound = ex.submit(bind)
+        bound = None if torch is None else ex.submit(compile_bind, torch, home, verbose)
         objs = list(ex.map(one, SOURCES))
-        bound.result()
     libdir = os.path.join(home, "lib64")
     tmp = LIB_PATH + ".tmp"
     run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath," + libdir, "-o", tmp, *objs], "link")
     os.replace(tmp, LIB_PATH)
+    if bound is None:
+        print("no PyTorch with CUDA here: the cache operators' Python binding is not built", file=sys.stderr)
+        return LIB_PATH
     # (torch's libraries are in the process before this one is loaded; it finds the
     # library above beside itself)
     tmp = BIND_PATH + ".tmp"
-    run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, "-L" + os.path.join(torch_dir, "lib"),
+    run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bound.result(), "-L" + os.path.join(torch, "lib"),
          "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10", "-L" + PKG, "-lattn_gb300",
          "-Wl,-rpath,$ORIGIN"], "link of the binding")
     os.replace(tmp, BIND_PATH)

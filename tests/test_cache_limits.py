@@ -3,6 +3,7 @@ can tell: sizes, build, the host's arithmetic (no GPU needed)."""
 
 from __future__ import annotations
 
+import importlib.util
 import itertools
 import os
 import re
@@ -39,3 +40,52 @@ def test_a_loader_waits_for_its_copies_whatever_ended_it(source, loaders):
     waits = re.findall(r"if \(([^\n]*)\) \{[^\n]*\n\s*const uint64_t t0 = globaltimer_ns\(\);\n(?:\s*auto drain|\s*for \(int i = max)",
                        text)
     assert waits == ["lane == 0"] * loaders
+
+
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    """build.build() whose commands only leave their output file: (commands run, paths of the outputs)."""
+    ran = []
+
+    def run(cmd, what, verbose=False):
+        ran.append(what)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    paths = {"LIB_PATH": str(tmp_path / "lib.so"), "BIND_PATH": str(tmp_path / "bind.so"), "BUILD_DIR": str(tmp_path / "o")}
+    for name, path in paths.items():
+        monkeypatch.setattr(build, name, path)
+    monkeypatch.setattr(build, "run", run)
+    monkeypatch.setattr(build, "nvcc_path", lambda: "/cuda/bin/nvcc")
+    return ran, paths
+
+
+def test_the_library_is_built_without_torch(fake_build, monkeypatch, capsys):
+    ran, paths = fake_build
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build.build() == paths["LIB_PATH"]
+    assert os.path.exists(paths["LIB_PATH"]) and not os.path.exists(paths["BIND_PATH"])
+    assert "link" in ran and not any("bind" in what for what in ran)
+    assert "PyTorch" in capsys.readouterr().err
+
+
+def test_a_binding_that_does_not_build_leaves_the_library(fake_build, monkeypatch):
+    ran, paths = fake_build
+    run = build.run
+
+    def fails(cmd, what, verbose=False):
+        if "bind" in what:
+            raise RuntimeError("no compiler")
+        run(cmd, what, verbose)
+
+    monkeypatch.setattr(build, "run", fails)
+    with pytest.raises(RuntimeError, match="no compiler"):
+        build.build()
+    assert os.path.exists(paths["LIB_PATH"]) and not os.path.exists(paths["BIND_PATH"])
+
+
+def test_both_are_built(fake_build):
+    ran, paths = fake_build
+    assert build.build() == paths["LIB_PATH"]
+    assert all(os.path.exists(paths[name]) for name in ("LIB_PATH", "BIND_PATH"))
+    assert ran.index("link") < ran.index("link of the binding")
