@@ -84,7 +84,7 @@ _bind = None
 
 
 def _load():
-    """The compiled binding (raises if it is missing)."""
+    """The compiled binding (raises if it is missing or was built for another PyTorch)."""
     global _bind
     if not os.path.exists(_BIND_PATH):
         raise RuntimeError(f"{_BIND_PATH} is missing: build it with `python -m exact_attention_63_gb300.build`")
@@ -92,6 +92,9 @@ def _load():
     loader = importlib.machinery.ExtensionFileLoader("_cache_bind", _BIND_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache_bind", loader))
     loader.exec_module(module)
+    if not torch.__version__.startswith(module.torch_version):
+        raise RuntimeError(f"{_BIND_PATH} was built for PyTorch {module.torch_version}, not {torch.__version__}: build it "
+                           "again with `python -m exact_attention_63_gb300.build`")
     _bind = module
     return module
 

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cmath>
 #include <cstring>
@@ -286,4 +287,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_cache_bind", nullptr, -1, kMetho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__cache_bind() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__cache_bind() {
+  PyObject* const m = PyModule_Create(&kModule);
+  // PyTorch's C++ classes differ from version to version: cache.py compares.
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

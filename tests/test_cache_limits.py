@@ -89,3 +89,13 @@ def test_both_are_built(fake_build):
     assert build.build() == paths["LIB_PATH"]
     assert all(os.path.exists(paths[name]) for name in ("LIB_PATH", "BIND_PATH"))
     assert ran.index("link") < ran.index("link of the binding")
+
+
+def test_a_binding_for_another_torch_is_refused(L, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(cache, "_bind", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="built for PyTorch"):
+        cache._load()
+    assert cache._bind is None
+    monkeypatch.undo()
+    assert cache._load() is cache._bind
