@@ -594,14 +594,21 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
   if constexpr (SHARED) cluster_sync();  // no CTA ends while another may write into it
 }
 
+constexpr uint32_t kSmemMax = 232448;
+
 // Clusters of 2^log CTAs that run at a time (they do not cross the GPU's processor
-// clusters, so larger ones leave some SMs without work), or 0.
+// clusters, so larger ones leave some SMs without work), with all the shared memory that a
+// CTA may have; 0 where none does or the runtime does not say.
 template <int D>
-int clusters_at_a_time(int device, int log, const cudaLaunchConfig_t& cfg) {
+int clusters_at_a_time(int device, int log, cudaLaunchConfig_t cfg) {
   static volatile int known[64][4] = {};
   int n = known[device][log];
   if (n == 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, cache_weights_kernel<D, true>, &cfg) != cudaSuccess) return 0;
+    cfg.dynamicSmemBytes = kSmemMax;
+    if (cudaOccupancyMaxActiveClusters(&n, cache_weights_kernel<D, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // (it would be taken for a later launch's)
+      return 0;
+    }
     known[device][log] = n;
   }
   return n;
@@ -614,19 +621,19 @@ cudaError_t launch(const CacheWeightLaunch& a) {
   static volatile bool configured[64] = {};
   if (!configured[a.device]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(cache_weights_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        cudaFuncSetAttribute(cache_weights_kernel<D, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     configured[a.device] = true;
   }
   // Up to four chunks in flight, and the keys get the rest: a slot for each half (one
   // tile) at least.
-  const uint32_t room = 232448u - 1024u - WL<D>::rings(p.c.n_seq) - ((1u << p.log_split) - 1u) * 1024u;
+  const uint32_t room = kSmemMax - 1024u - WL<D>::rings(p.c.n_seq) - ((1u << p.log_split) - 1u) * 1024u;
   const uint32_t chunk = static_cast<uint32_t>(p.n_cols) * (D * 2 + 32);
   p.q_stages = kMaxChunks;
   while (room - p.q_stages * chunk < 2 * WL<D>::kSlot) --p.q_stages;  // many sequences: their table takes room
   const uint32_t k_stages = (room - p.q_stages * chunk) / (2 * WL<D>::kSlot);
   p.k_stages = static_cast<int>(k_stages < kMaxHalf ? k_stages : kMaxHalf);
-  const uint32_t smem = 232448u - room + 2 * p.k_stages * WL<D>::kSlot + p.q_stages * chunk;
+  const uint32_t smem = kSmemMax - room + 2 * p.k_stages * WL<D>::kSlot + p.q_stages * chunk;
   if constexpr (!SHARED) {
     cache_weights_kernel<D, false><<<a.grid, kThreadsCW, smem, a.stream>>>(a.q, a.k, p);
     return cudaGetLastError();
@@ -643,7 +650,11 @@ cudaError_t launch(const CacheWeightLaunch& a) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const int n = clusters_at_a_time<D>(a.device, p.log_split, cfg);
-    if (n < 1) return cudaErrorLaunchOutOfResources;
+    if (n < 1) {  // each CTA takes whole tiles
+      CacheWeightLaunch alone = a;
+      alone.p.log_split = 0;
+      return launch<D, false>(alone);
+    }
     cfg.gridDim.x = static_cast<unsigned int>(n < a.tiles ? n : a.tiles) << p.log_split;
     return cudaLaunchKernelEx(&cfg, cache_weights_kernel<D, true>, a.q, a.k, p);
   }

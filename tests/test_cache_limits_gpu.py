@@ -2,11 +2,16 @@
 
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+import textwrap
+
 import pytest
 import torch
 
 from cache_reference import Case, f64
-from exact_attention_63_gb300 import attn, cache
+from exact_attention_63_gb300 import attn, build, cache
 from gpu_common import need_gpu
 from test_cache_gpu import check_attention, check_weights
 
@@ -53,3 +58,36 @@ def test_wait_limit_where_a_loader_is_done():
         assert attn.get_status() == -8
         out = cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 2, c.weights, out=torch.zeros_like(c.weights))
         check_weights(c, lse, start, out)
+
+
+def test_weights_where_no_cluster_fits(tmp_path):
+    """Sharing a tile is a matter of speed: where the runtime knows of no cluster that fits (here a stand-in for
+    its query that fails and leaves an error behind), single CTAs do the work, and the calls after it are right."""
+    home = build.cuda_home(build.nvcc_path())
+    source, fake = tmp_path / "fake.cpp", tmp_path / "fake.so"
+    source.write_text(textwrap.dedent("""
+        extern "C" int cudaSetDevice(int);
+        extern "C" int cudaOccupancyMaxActiveClusters(int* n, const void*, const void*) {
+          *n = 0;
+          return cudaSetDevice(99999);
+        }
+    """))
+    subprocess.run(["g++", "-shared", "-fPIC", str(source), "-o", str(fake), f"-L{home}/lib64", "-lcudart"], check=True)
+    program = textwrap.dedent("""
+        import torch
+        from cache_reference import Case, f64
+        from exact_attention_63_gb300 import attn, cache
+        from test_cache_gpu import check_attention, check_weights, attend
+        c = Case([900], [900], 8, 1, 64, 16, seed=53).cuda()
+        lse = torch.full((8, 900), 6.0, device="cuda")
+        for _ in range(2):
+            out = cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 900, c.weights, out=torch.zeros_like(c.weights))
+            cache.cache_append(c.k_new, c.v_new, c.k.clone(), c.v.clone(), c.table, c.seq_lens, c.cu)
+            check_weights(c, lse, f64(c.weights), out)
+        assert attn.get_status() == 0
+        print("fine")
+    """)
+    tests = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, LD_PRELOAD=str(fake), PYTHONPATH=os.pathsep.join((os.path.dirname(tests), tests)))
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
