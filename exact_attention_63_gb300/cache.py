@@ -382,7 +382,7 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     and attn_fwd_cache return it.  Writes weights + sums to ``out`` (default: into
     ``weights``) at every slot in use, and returns it; weights None counts as zeros
     (out is then needed).  Any number of queries: a decoded token, the last window
-    of a prompt or the whole of it.
+    of a prompt or the whole of it.  ``scale`` is at least 1e-30.
     """
     if stream is None and options is None:
         into = weights if out is None else out

@@ -261,7 +261,7 @@ int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const 
   // (128: the kernel rounds a sequence's rows up to whole chunks)
   if (tiles > kMaxInt || static_cast<long long>(x->H) * c.total > kMaxInt - 128) return ATTN_ERR_SHAPE;
   if ((rc = check_scale(scale)) != ATTN_OK) return rc;
-  if (!std::isfinite(1.f / scale)) return ATTN_ERR_SCALE;  // (the kernel divides the LSE by it)
+  if (scale < ATTN_CACHE_MIN_SCALE) return ATTN_ERR_SCALE;  // (the kernel divides the LSE by it)
   const long long dense[2] = {static_cast<long long>(x->H) * c.d, c.d};
   long long qs[2];
   if (!resolve<2>(x->q_strides, dense, qs)) return ATTN_ERR_CACHE;

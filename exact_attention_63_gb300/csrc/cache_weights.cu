@@ -424,8 +424,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
       float x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = -v[i] * p.inv_scale;
-        if (x[i] == INFINITY) x[i] = -INFINITY;
+        x[i] = v[i] == -INFINITY ? -INFINITY : -v[i] * p.inv_scale;
       }
       more = advance();
       if (more) fetch();
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsCW, 1)
         // x = hi + mid + lo, each a rounding to bf16 of what the ones before leave.
         const uint32_t hi = pack_bf16x2(x[i], 0.f) & 0xffffu;
         float rest = x[i] - __uint_as_float(hi << 16);
-        if (x[i] == -INFINITY) rest = 0.f;
+        if ((hi & 0x7FFFu) == 0x7F80u) rest = 0.f;  // hi = ±inf
         const uint32_t mid = pack_bf16x2(rest, 0.f) & 0xffffu;
         const uint32_t lo = pack_bf16x2(rest - __uint_as_float(mid << 16), 0.f) & 0xffffu;
         if (lane + 32 * i < p.n_cols)

@@ -529,9 +529,11 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
  *   weights_out : device, fp32 [n_pages, num_kv_heads, page_size]; may be
  *                 cache->weights.  Every slot in use is written, no other.
  * max_seqlen is not limited (whole prompts).  Sums are fp32, in a fixed order.
- * scale as for attn_fwd, and 1/scale has to be finite (ATTN_ERR_SCALE).
+ * scale as for attn_fwd, and at least ATTN_CACHE_MIN_SCALE (ATTN_ERR_SCALE): lse/scale is
+ * an fp32 number.
  * opts as for attn_fwd_cache (may be NULL).
  */
+#define ATTN_CACHE_MIN_SCALE 1e-30f
 int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,
                        float* weights_out, const attn_options* opts, cudaStream_t stream);
 

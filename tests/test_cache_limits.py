@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from exact_attention_63_gb300 import build, cache
-from test_cache_abi import ARCH, WORKSPACE, L, a_cache, calls, tokens  # noqa: F401
+from test_cache_abi import ARCH, SCALE, WORKSPACE, L, a_cache, calls, tokens  # noqa: F401
 
 
 @pytest.mark.parametrize("group", [1, 2, 3, 4, 7, 8, 16, 33, 64, 128])
@@ -99,3 +99,11 @@ def test_a_binding_for_another_torch_is_refused(L, monkeypatch):  # noqa: F811
     assert cache._bind is None
     monkeypatch.undo()
     assert cache._load() is cache._bind
+
+
+def test_weights_refuse_scales_that_no_lse_can_be_divided_by(L):  # noqa: F811
+    """-LSE/scale has to fit into 32 bits: of LSE = 7 it does not at 1e-38."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: the calls would reach it")
+    for scale, expect in ((1e-38, SCALE), (9.9e-31, SCALE), (1.1e-30, ARCH), (1e30, ARCH)):
+        assert calls(L, a_cache(), tokens(), scale=scale)["weigh"]() == expect, scale

@@ -7,10 +7,12 @@ import subprocess
 import sys
 import textwrap
 
+import numpy as np
 import pytest
 import torch
 
-from cache_reference import Case, f64
+import cache_reference as ref
+from cache_reference import HALF_F32, Case, f64
 from exact_attention_63_gb300 import attn, build, cache
 from gpu_common import need_gpu
 from test_cache_gpu import check_attention, check_weights
@@ -91,3 +93,39 @@ def test_weights_where_no_cluster_fits(tmp_path):
     env = dict(os.environ, LD_PRELOAD=str(fake), PYTHONPATH=os.pathsep.join((os.path.dirname(tests), tests)))
     r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+def weigh(c: Case, lse, **kw):
+    return cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, c.max_new(), c.weights, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_at_the_smallest_scale(d):
+    """scale = 1e-30 with queries and keys of 1e15: scores of ordinary size, -LSE/scale of 1e31."""
+    c = Case([300, 70], [40, 70], 4, 2, d, 16, seed=54)
+    c.weights = torch.nan_to_num(c.weights)
+    size = (c.d + 8) * HALF_F32 * max(float(c.q.float().norm(dim=-1).max()) * float(c.k.float().nan_to_num().norm(dim=-1).max()), 8)
+    c.q, c.k, c.scale = (c.q.float() * 1e15).bfloat16(), (c.k.float() * 1e15).bfloat16(), 1.0000001e-30
+    c.cuda()
+    lse = (torch.randn((4, c.total), generator=torch.Generator().manual_seed(3)) + 7).cuda()
+    W, start = ref.weights(c, lse, f64(c.weights)), f64(c.weights)
+    got, used = f64(weigh(c, lse, scale=c.scale, out=torch.zeros_like(c.weights))), ~np.isnan(W)
+    # scores off by `size` (fp32 sums of |q||k|) and the rounding of scale, -LSE/scale in three terms of bf16; fp32 sums
+    tol = (4 * size + 2.0 ** -15) * (W - start) + 2.0 ** -22 * W + 1e-30
+    assert (np.abs(got - W) <= tol)[used].all()
+
+
+def test_weights_of_extreme_lse():
+    """Finite LSEs far from any score, up to the largest: nothing is added, or infinity."""
+    c = Case([200, 130], [3, 130], 4, 2, 64, 16, seed=55).cuda()
+    start = f64(c.weights)
+    lse = torch.full((4, c.total), 5.0, device="cuda")
+    top = torch.finfo(torch.float32).max
+    for value in (1e9, 4.2e37, 4.25e37, 3.4e38, top):  # (over the scale of 1/8: within bf16, within fp32 only, beyond)
+        lse[0, 1::3] = value
+        check_weights(c, lse, start, weigh(c, lse, out=torch.zeros_like(c.weights)))
+        low = lse.clone()
+        low[0, 4] = -value
+        W = ref.weights(c, low, start)
+        got = f64(weigh(c, low, out=torch.zeros_like(c.weights)))
+        assert np.array_equal(np.isinf(W), np.isinf(got) & ~np.isnan(W)) and not np.isnan(got).any()
