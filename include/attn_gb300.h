@@ -524,7 +524,8 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
  *   (the n tokens are the newest in the cache).
  *   x           : q, cu_seqlens, total, max_seqlen, H.  lse: device, fp32
  *                 [H, total], natural log, as attn_fwd_varlen and attn_fwd_cache
- *                 return it.  A row with lse = -inf or +inf adds nothing.
+ *                 return it.  A row with lse = -inf or +inf adds nothing,
+ *                 whatever its q holds.
  *   cache->weights : may be NULL (counts as zeros).  cache->v is not used.
  *   weights_out : device, fp32 [n_pages, num_kv_heads, page_size]; may be
  *                 cache->weights.  Every slot in use is written, no other.

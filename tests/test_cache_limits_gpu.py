@@ -55,7 +55,8 @@ def test_wait_limit_where_a_loader_is_done():
     c = Case([200, 90, 256], [1, 2, 1], 8, 2, 128, 16, seed=52).cuda()
     start, lse = f64(c.weights), torch.full((8, c.total), 6.0, device="cuda")
     opts = attn.make_options(timeout_ms=1, test_flags=attn.TEST_WITHHOLD_KV)
-    for _ in range(10):
+    for i in range(10):
+        lse[:, 1] = float("inf") if i % 2 else 6.0
         cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 2, c.weights, out=torch.zeros_like(c.weights), options=opts)
         assert attn.get_status() == -8
         out = cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 2, c.weights, out=torch.zeros_like(c.weights))
@@ -129,3 +130,24 @@ def test_weights_of_extreme_lse():
         W = ref.weights(c, low, start)
         got = f64(weigh(c, low, out=torch.zeros_like(c.weights)))
         assert np.array_equal(np.isinf(W), np.isinf(got) & ~np.isnan(W)) and not np.isnan(got).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,H,hkv", [([1100, 300], [1100, 90], 8, 1), ([900] * 20, [33] * 20, 12, 3), ([5000, 77], [1, 2], 8, 2)])
+def test_weights_of_rows_left_out(lens, new, H, hkv, d):
+    """An infinite LSE leaves its row out, whatever the row's query holds (the padding of a batch of fixed
+    shape): whole chunks of such rows, some in a chunk, with keys that have no weight in them."""
+    c = Case(lens, new, H, hkv, d, 16, seed=56).cuda()
+    g = torch.Generator().manual_seed(57)
+    start = f64(c.weights)
+    lse = (torch.randn((H, c.total), generator=g) * 0.1 + 6.0).cuda()
+    off = (torch.rand(c.total, generator=g) < 0.2).cuda()
+    off[: min(70, c.total // 2)] = True
+    lse[:, off] = float("inf")
+    lse[0, ::7] = -float("inf")  # (one head of some: its query alone is left out)
+    clean = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, start, clean)
+    for junk in (float("nan"), float("inf"), torch.finfo(torch.bfloat16).max):
+        c.q[off] = junk
+        c.q[::7, 0] = junk
+        assert torch.equal(weigh(c, lse, out=torch.zeros_like(c.weights)), clean)
