@@ -382,7 +382,8 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     and attn_fwd_cache return it.  Writes weights + sums to ``out`` (default: into
     ``weights``) at every slot in use, and returns it; weights None counts as zeros
     (out is then needed).  Any number of queries: a decoded token, the last window
-    of a prompt or the whole of it.  ``scale`` is at least 1e-30.
+    of a prompt or the whole of it; none at all adds nothing.  ``scale`` is at least
+    1e-30.
     """
     if stream is None and options is None:
         into = weights if out is None else out
@@ -407,11 +408,15 @@ def cache_weights(q, lse, k_cache, block_table, seq_lens, cu_seqlens_q, max_seql
     if q is None:
         raise ValueError("q is needed")
     x, total, H = _pack_tokens(dev, q, None, None, cu_seqlens_q, n_seq, hkv, d, int(max_seqlen_q))
-    if total == 0:
-        raise ValueError("q has no rows")
     lp = _need("lse", lse, _F32, dev)
     if lse.shape != (H, total):
         raise ValueError(f"lse must be [H, total] = {(H, total)}")
+    if total == 0:  # what there was at every slot in use
+        if weights is not None and op == weights.data_ptr():
+            return out
+        # (the library takes no empty tensors: a row that adds nothing stands for them)
+        q, lse = q.new_zeros((1, H, d)), lse.new_full((H, 1), math.inf)
+        x, lp = _pack_tokens(dev, q, None, None, cu_seqlens_q, n_seq, hkv, d, 1)[0], lse.data_ptr()
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     rc = attn.lib().attn_cache_weights(c, x, lp, scale, op, _options(options), _stream(dev))

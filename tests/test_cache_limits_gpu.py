@@ -15,7 +15,7 @@ import cache_reference as ref
 from cache_reference import HALF_F32, Case, f64
 from exact_attention_63_gb300 import attn, build, cache
 from gpu_common import need_gpu
-from test_cache_gpu import check_attention, check_weights
+from test_cache_gpu import bits, check_attention, check_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,43 @@ def test_weights_of_rows_left_out(lens, new, H, hkv, d):
         c.q[off] = junk
         c.q[::7, 0] = junk
         assert torch.equal(weigh(c, lse, out=torch.zeros_like(c.weights)), clean)
+
+
+def test_a_step_without_tokens():
+    """No sequence has a new token: every operator takes it, and the weights are what they were."""
+    c = Case([40, 0, 300], [0, 0, 0], 4, 2, 64, 16, seed=58).cuda()
+    here = torch.cuda.current_stream()
+    before = [t.clone() for t in (c.k, c.v, c.weights, c.positions)]
+    used = ~torch.isnan(c.weights)
+    for stream in (None, here):
+        o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 1, stream=stream)
+        assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+        cache.cache_append(c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, weights=c.weights, positions=c.positions,
+                           stream=stream)
+        for most in (0, 1, 5):
+            args = (c.q, lse, c.k, c.table, c.seq_lens, c.cu, most)
+            assert cache.cache_weights(*args, c.weights, stream=stream) is c.weights
+            out = torch.full_like(c.weights, 5.0)
+            assert cache.cache_weights(*args, c.weights, out=out, stream=stream) is out
+            assert torch.equal(out[used], c.weights[used]) and (out[~used] == 5).all()
+            assert cache.cache_weights(*args, out=out, stream=stream) is out
+            assert (out[used] == 0).all() and (out[~used] == 5).all()
+    for a, b in zip(before, (c.k, c.v, c.weights, c.positions)):
+        assert torch.equal(bits(a), bits(b))
+    with pytest.raises(ValueError):
+        cache.cache_weights(c.q, lse[:3], c.k, c.table, c.seq_lens, c.cu, 0, c.weights)
+
+
+def test_an_empty_step_in_a_graph():
+    c = Case([40, 300], [0, 0], 4, 2, 64, 16, seed=59).cuda()
+    lse, out = torch.zeros((4, 0), device="cuda"), torch.zeros_like(c.weights)
+    cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 0, c.weights, out=out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 0, c.weights, out=out)
+    c.weights += 1
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        used = ~torch.isnan(c.weights)
+        assert torch.equal(out[used], c.weights[used])
