@@ -316,7 +316,8 @@ def attn_fwd_cache(q, k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_
         _need("lse", lse, _F32, dev)
         if lse.shape != (H, total):
             raise ValueError("lse must be [H, total]")
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or
+                                  not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     device = k_cache.device
     if out is None:

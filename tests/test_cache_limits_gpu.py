@@ -191,3 +191,24 @@ def test_an_empty_step_in_a_graph():
         g.replay()
         used = ~torch.isnan(c.weights)
         assert torch.equal(out[used], c.weights[used])
+
+
+def test_outputs_and_workspaces_that_do_not_fit():
+    c = Case([40, 20], [2, 1], 4, 2, 64, 16, seed=60).cuda()
+    args = (c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 2)
+    o, lse = cache.attn_fwd_cache(*args)
+    ws = torch.zeros(cache.workspace_size(4, 2, 2, 64) + 512, dtype=torch.uint8, device="cuda")
+    for bad in (3, "ws", ws.cpu(), ws[::2]):
+        with pytest.raises(ValueError):
+            cache.attn_fwd_cache(*args, workspace=bad)
+    for bad in (ws[16:], ws[256:-513]):
+        with pytest.raises(attn.AttnError) as e:
+            cache.attn_fwd_cache(*args, workspace=bad)
+        assert e.value.code == -10
+    for name, t in (("out", o), ("lse", lse)):
+        for bad in (3, t.cpu(), t.double(), t[:-1], t[None], t.transpose(0, 1)):
+            with pytest.raises(ValueError):
+                cache.attn_fwd_cache(*args, **{name: bad})
+    with pytest.raises(ValueError):
+        cache.cache_select(torch.nan_to_num(c.weights), c.table, c.seq_lens, 8, kept=[1])
+    assert torch.equal(cache.attn_fwd_cache(*args, workspace=ws[256:-256])[0], o)
