@@ -212,3 +212,175 @@ def test_outputs_and_workspaces_that_do_not_fit():
     with pytest.raises(ValueError):
         cache.cache_select(torch.nan_to_num(c.weights), c.table, c.seq_lens, 8, kept=[1])
     assert torch.equal(cache.attn_fwd_cache(*args, workspace=ws[256:-256])[0], o)
+
+
+# ------------------------------------------------ values out of range, with margins around every output
+class Guarded:
+    """A tensor inside a larger buffer whose margins hold `fill`."""
+
+    MARGIN = 4096
+
+    def __init__(self, shape, dtype, fill):
+        n = int(np.prod(shape))
+        self.fill = fill
+        self.buffer = torch.full((n + 2 * self.MARGIN,), fill, dtype=dtype, device="cuda")
+        self.t = self.buffer[self.MARGIN:self.MARGIN + n].view(shape)
+
+    def intact(self):
+        return bool((self.buffer[:self.MARGIN] == self.fill).all() and (self.buffer[-self.MARGIN:] == self.fill).all())
+
+
+def malformed(H, hkv, d, page, seed):
+    """(the case as given, the same with every value clamped into its range): lengths, pages and offsets beyond
+    both ends, more rows of a sequence than max_seqlen, rows behind the last one.  All slots hold numbers."""
+    c = Case([5 * page, 3 * page, 2 * page + 1, 9], [2, 3, 1, 1], H, hkv, d, page, seed=seed, slack=4)
+    g = torch.Generator().manual_seed(seed)
+    c.k, c.v = (torch.randn(t.shape, generator=g).bfloat16() for t in (c.k, c.v))
+    c.weights = torch.rand(c.weights.shape, generator=g)
+    c.positions = torch.randint(0, 99, c.positions.shape, generator=g, dtype=torch.int32)
+    c.cuda()
+    n, cap = c.n_pages, c.table.shape[1] * page
+    # pages 0 and n - 1 stand for the bad ones: no sequence has them, and none of the others is in use twice
+    c.table[:] = torch.arange(1, c.table.numel() + 1, device="cuda").view(c.table.shape) % (n - 2) + 1
+    c.table[0, 1], c.table[0, 3], c.table[1, 0], c.table[2, 2] = -5, 1 << 30, n, -(1 << 31)
+    c.seq_lens[:] = torch.tensor([(1 << 31) - 1, -4, 2 * page + 1, 9], dtype=torch.int32, device="cuda")
+    c.cu[:] = torch.tensor([-3, 2, 5, 6, 900], dtype=torch.int32, device="cuda")
+    good = {"table": c.table.clamp(0, n - 1), "seq_lens": c.seq_lens.clamp(0, cap), "cu": c.cu.clamp(0, c.total)}
+    return c, good
+
+
+@pytest.mark.parametrize("H,hkv,d,page", [(8, 2, 64, 16), (6, 2, 128, 48), (64, 1, 128, 32)])
+def test_attention_of_malformed_values_is_that_of_clamped_ones(H, hkv, d, page):
+    c, good = malformed(H, hkv, d, page, seed=61)
+    results = []
+    for v in ({}, good):
+        o, lse = Guarded((c.total, H, d), torch.bfloat16, 7.0), Guarded((H, c.total), torch.float32, 7.0)
+        ws = Guarded((cache.workspace_size(H, hkv, 2, d),), torch.uint8, 171)
+        k0, v0 = c.k.clone(), c.v.clone()
+        cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, v.get("table", c.table), v.get("seq_lens", c.seq_lens),
+                             v.get("cu", c.cu), 2, parents=c.parents, out=o.t, lse=lse.t, workspace=ws.t)
+        assert o.intact() and lse.intact() and ws.intact()
+        assert torch.equal(bits(k0), bits(c.k)) and torch.equal(bits(v0), bits(c.v))
+        assert (o.t[4] == 7).all() and (lse.t[:, 4] == 7).all()  # the second sequence's third row: beyond max_seqlen
+        results.append((o.t, lse.t))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    assert torch.isfinite(results[0][0]).all()
+
+
+@pytest.mark.parametrize("H,hkv,d,page", [(8, 2, 64, 16), (6, 2, 128, 48), (64, 1, 128, 32)])
+def test_weights_of_malformed_values(H, hkv, d, page):
+    """As with clamped lengths and offsets; what lies on a page that is not there is left alone."""
+    c, good = malformed(H, hkv, d, page, seed=62)
+    lse = torch.full((H, c.total), 5.0, device="cuda")
+    outs = []
+    for v in ({}, good):
+        out = Guarded(c.weights.shape, torch.float32, -3.0)
+        cache.cache_weights(c.q, lse, c.k, v.get("table", c.table), v.get("seq_lens", c.seq_lens), v.get("cu", c.cu), 2,
+                            c.weights, out=out.t)
+        assert out.intact()
+        outs.append(out.t)
+    assert (outs[0][0] == -3).all() and (outs[0][-1] == -3).all()
+    assert torch.equal(outs[0][1:-1], outs[1][1:-1])
+    assert (outs[0] != -3).any()
+
+
+@pytest.mark.parametrize("budget", [3, 40, 1000])
+def test_selection_and_compaction_of_malformed_values(budget):
+    c, good = malformed(8, 2, 64, 16, seed=63)
+    kept = []
+    for v in ({}, good):
+        out = Guarded((4, 2, budget), torch.int32, 77)
+        cache.cache_select(c.weights, v.get("table", c.table), v.get("seq_lens", c.seq_lens), budget, 2, c.positions,
+                           c.seq_lens.clamp(0, 99), kept=out.t)
+        assert out.intact()
+        kept.append(out.t)
+    assert torch.equal(*kept)
+    # moves from or to a page that is not there are skipped, and nothing else than the moves changes
+    state = [Guarded(t.shape, t.dtype, 5) for t in (c.k, c.v, c.weights, c.positions)]
+    for s, t in zip(state, (c.k, c.v, c.weights, c.positions)):
+        s.t.copy_(t)
+    cache.cache_compact(kept[0], state[0].t, state[1].t, c.table, state[2].t, state[3].t)
+    assert all(s.intact() for s in state)
+    want, tab = [t.clone() for t in (c.k, c.v, c.weights, c.positions)], c.table.tolist()
+    there = lambda s, j: j // 16 < len(tab[s]) and 0 <= tab[s][j // 16] < c.n_pages  # noqa: E731
+    for s in range(4):
+        for h in range(2):
+            for i, j in enumerate(kept[0][s, h].tolist()):
+                if j >= budget and there(s, i) and there(s, j):
+                    a, b = (tab[s][j // 16], j % 16), (tab[s][i // 16], i % 16)
+                    want[0][b[0], b[1], h], want[1][b[0], b[1], h] = c.k[a[0], a[1], h], c.v[a[0], a[1], h]
+                    want[2][b[0], h, b[1]], want[3][b[0], h, b[1]] = c.weights[a[0], h, a[1]], c.positions[a[0], h, a[1]]
+    for s, w in zip(state, want):
+        assert torch.equal(bits(s.t), bits(w))
+
+
+def test_append_of_malformed_values_stays_inside():
+    c, _ = malformed(4, 2, 64, 16, seed=64)
+    state = [Guarded(t.shape, t.dtype, 5) for t in (c.k, c.v, c.weights, c.positions)]
+    for s, t in zip(state, (c.k, c.v, c.weights, c.positions)):
+        s.t.copy_(t)
+    rows = torch.tensor([0, -1, 1 << 30, c.total, 3, 1, -(1 << 31)], dtype=torch.int32, device="cuda")
+    cache.cache_append(c.k_new, c.v_new, state[0].t, state[1].t, c.table, c.seq_lens, c.cu, rows=rows, weights=state[2].t,
+                       positions=state[3].t)
+    assert all(s.intact() for s in state)
+    # sequence 0 ends at the table's end; the others' slots, pages or rows are not there
+    page = int(c.table[0, 4])
+    want = [t.clone() for t in (c.k, c.v, c.weights, c.positions)]
+    want[0][page, 14], want[1][page, 14], want[2][page, :, 14], want[3][page, :, 14] = c.k_new[0], c.v_new[0], 0.0, 78
+    for s, w in zip(state, want):
+        assert torch.equal(bits(s.t), bits(w))
+
+
+# ------------------------------------------------------------ the largest tables and pages
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_most_sequences(d):
+    """2048 sequences, a third without a new token, some empty; 32 heads a key head make full chunks of rows, of
+    which fewer fit beside the sequences' table."""
+    n = 2048
+    lens = [(37 * i) % 90 for i in range(n)]
+    new = [0 if i % 3 == 2 else 1 + (i % 5 == 0) * 4 for i in range(n)]
+    c = Case(lens, new, 32, 1, d, 16, seed=65, room=8)
+    c.weights = torch.nan_to_num(c.weights)
+    start = f64(c.weights)
+    c.cuda()
+    o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 5, parents=c.parents)
+    check_attention(c, o, lse)
+    out = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, start, out)
+    kept = cache.cache_select(c.weights, c.table, c.seq_lens, 40, 4, c.positions, c.seq_lens)
+    assert np.array_equal(kept.cpu().numpy(), ref.select(c, 40, 4, c.seq_lens.cpu()))
+
+
+@pytest.mark.parametrize("page", [272, 4096, 65536])
+def test_large_pages(page):
+    d, H, hkv = 64, 4, 2
+    c = Case([700, 3, 271], [3, 1, 2], H, hkv, d, page, seed=66, slack=1, room=4)
+    start = f64(torch.nan_to_num(c.weights))
+    c.cuda()
+    o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 3, parents=c.parents)
+    check_attention(c, o, lse)
+    out = weigh(c, lse, out=torch.zeros_like(c.weights))
+    check_weights(c, lse, start, out)
+    pos = c.seq_lens.clone()
+    kept = cache.cache_select(c.weights, c.table, c.seq_lens, 100, 10, c.positions, pos)
+    assert np.array_equal(kept.cpu().numpy(), ref.select(c, 100, 10, pos.cpu()))
+    cache.cache_compact(kept, c.k, c.v, c.table, c.weights, c.positions)
+    c.lens = [100, 3, 100]
+    c.seq_lens.clamp_(max=100)
+    o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 3, parents=c.parents)
+    check_attention(c, o, lse)
+
+
+@pytest.mark.parametrize("width", [20000, 65536, 1 << 20])
+def test_selection_under_a_wide_table(width):
+    """The table has room for far more than the sequences hold, up to the most a selection takes: the bit map then
+    leaves room for fewer keys than the longer sequence has."""
+    c = Case([17000, 300], [1, 1], 1, 1, 64, 16, seed=67)
+    g = torch.Generator().manual_seed(68)
+    c.weights = torch.where(torch.isnan(c.weights), c.weights, torch.round(torch.rand(c.weights.shape, generator=g) * 500))
+    c.table = torch.nn.functional.pad(c.table, (0, width // 16 - c.table.shape[1]), value=-1).contiguous()
+    c.cuda()
+    pos = c.seq_lens.clone()
+    for budget in (1, 200, 9000, 16999):
+        kept = cache.cache_select(c.weights, c.table, c.seq_lens, budget, min(budget, 30), c.positions, pos)
+        assert np.array_equal(kept.cpu().numpy(), ref.select(c, budget, min(budget, 30), pos.cpu()))
