@@ -6,6 +6,7 @@ import os
 import subprocess
 import sys
 import textwrap
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
@@ -384,3 +385,117 @@ def test_selection_under_a_wide_table(width):
     for budget in (1, 200, 9000, 16999):
         kept = cache.cache_select(c.weights, c.table, c.seq_lens, budget, min(budget, 30), c.positions, pos)
         assert np.array_equal(kept.cpu().numpy(), ref.select(c, budget, min(budget, 30), pos.cpu()))
+
+
+# ------------------------------------------------------------ layouts, captures, two at once
+def other_layouts(c, kind):
+    """(k, v, the tensor they are parts of) of the case in another layout of pages."""
+    if kind == "heads first":
+        return [t.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3) for t in (c.k, c.v)] + [None]
+    if kind == "k and v of a page together":
+        both = torch.stack([c.k, c.v], 1)
+        return [both[:, 0], both[:, 1], both]
+    if kind == "k and v of a head together":
+        both = torch.cat([c.k, c.v], -1)
+        return [both[..., :c.d], both[..., c.d:], both]
+    layers = torch.stack([torch.zeros_like(c.k), c.k, c.v], 2)  # other things between the slots
+    return [layers[:, :, 1], layers[:, :, 2], layers]
+
+
+@pytest.mark.parametrize("kind", ["heads first", "k and v of a page together", "k and v of a head together", "apart"])
+@pytest.mark.parametrize("d,hkv", [(64, 2), (128, 1)])
+def test_all_operators_on_other_layouts(kind, d, hkv):
+    """Pages in strided views: every operator does what it does on dense ones, and nothing between the rows changes."""
+    c = Case([100, 33, 300], [4, 1, 2], 4 * hkv, hkv, d, 16, seed=70, room=8).cuda()
+    k, v, whole = other_layouts(c, kind)
+    results = []
+    for kk, vv in ((c.k.clone(), c.v.clone()), (k, v)):
+        w, pos = torch.nan_to_num(c.weights), c.positions.clone()
+        o, lse = cache.attn_fwd_cache(c.q, c.k_new, c.v_new, kk, vv, c.table, c.seq_lens, c.cu, 4, parents=c.parents)
+        after = c.seq_lens + c.cu.diff()
+        cache.cache_append(c.k_new, c.v_new, kk, vv, c.table, after, c.cu, weights=w, positions=pos)
+        cache.cache_weights(c.q, lse, kk, c.table, after, c.cu, 4, w)
+        kept = cache.cache_evict(kk, vv, w, c.table, after, 40, 8, pos, after)
+        results.append((o, lse, kk, vv, w, pos, kept))
+    for a, b in zip(*results):
+        assert torch.equal(bits(a.contiguous()), bits(b.contiguous()))
+    if kind == "apart":
+        assert (whole[:, :, 0] == 0).all()
+    # new tokens as slices of one projection, appended
+    packed = torch.cat([c.q, c.k_new, c.v_new], 1)
+    a, b = [(t[2].clone(), t[3].clone()) for t in results]
+    lens = c.seq_lens + 5
+    cache.cache_append(c.k_new, c.v_new, *a, c.table, lens, c.cu)
+    cache.cache_append(packed[:, 4 * hkv:5 * hkv], packed[:, 5 * hkv:], *b, c.table, lens, c.cu)
+    for x, y in zip(a, b):
+        assert torch.equal(bits(x), bits(y.contiguous()))
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    """Nothing of the library has run before: a capture of all operators, replayed."""
+    program = textwrap.dedent("""
+        import torch
+        from cache_reference import Case
+        from exact_attention_63_gb300 import cache
+        c = Case([900, 40], [900, 40], 8, 1, 64, 16, seed=71, room=8).cuda()
+        t = Case([300, 40], [3, 1], 8, 2, 128, 16, seed=72, room=8).cuda()
+        c.weights = torch.nan_to_num(c.weights)
+        lse = torch.full((8, c.total), 6.0, device="cuda")
+        out, k, v = torch.zeros_like(c.weights), c.k.clone(), c.v.clone()
+        def step():
+            r = cache.attn_fwd_cache(t.q, t.k_new, t.v_new, t.k, t.v, t.table, t.seq_lens, t.cu, 3, parents=t.parents)
+            cache.cache_append(c.k_new, c.v_new, k, v, c.table, c.seq_lens, c.cu)
+            cache.cache_weights(c.q, lse, c.k, c.table, c.seq_lens, c.cu, 900, c.weights, out=out)
+            kept = cache.cache_select(c.weights, c.table, c.seq_lens, 50, 5)
+            cache.cache_compact(kept, k, v, c.table)
+            return (*r, kept, k.view(torch.int16), v.view(torch.int16))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step()
+        g.replay()
+        torch.cuda.synchronize()
+        first, got = out.clone(), [x.clone() for x in got]
+        k.copy_(c.k)
+        v.copy_(c.v)
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(first, out)
+        print("fine")
+    """)
+    tests = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join((os.path.dirname(tests), tests)))
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+def test_calls_of_two_threads_at_once():
+    """Each thread with its own stream and its own cache."""
+    cases = [Case([700, 90], [5, 40], 8, 2, 64, 16, seed=73).cuda(), Case([900], [900], 8, 1, 128, 16, seed=74).cuda()]
+    lses = [torch.full((8, c.total), 6.0, device="cuda") for c in cases]
+    zeros = [torch.zeros_like(c.weights) for c in cases]
+
+    def work(i):
+        c = cases[i]
+        r = []
+        if i == 0:
+            r += cache.attn_fwd_cache(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.seq_lens, c.cu, 40, parents=c.parents)
+        r.append(weigh(c, lses[i], out=zeros[i].clone()))
+        r.append(cache.cache_select(torch.nan_to_num(c.weights), c.table, c.seq_lens, 30, 5))
+        return r
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def loop(i):
+        with torch.cuda.stream(streams[i]):
+            return [work(i) for _ in range(50)]
+
+    with ThreadPoolExecutor(2) as ex:
+        results = [f.result() for f in [ex.submit(loop, i) for i in range(2)]]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in results[i]:
+            for a, b in zip(r, want[i]):
+                used = ~torch.isnan(cases[i].weights) if a.shape == cases[i].weights.shape else slice(None)
+                assert torch.equal(a[used], b[used])
