@@ -12,10 +12,11 @@ namespace attn {
 constexpr int kCacheMaxSeq = 2048;   // sequences of one call: their offsets are kept in shared memory
 constexpr int kCacheMaxCtas = 320;   // row tiles at work at a time (two per SM); sizes the attention's workspace
 
-// Division by a number fixed for the launch: x / d = x·mul >> (31 + log), exact
-// for 0 ≤ x < 2^31 (mul = ⌈2^(31 + log) / d⌉, log = ⌈log2 d⌉).  The loaders of short
-// tiles do several divisions a tile, one warp alone: the compiler's division, some
-// 30 dependent instructions, showed.
+// Division by a number fixed for the launch, as a multiplication (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994): x / d = x·mul >> (31 + log),
+// exact for 0 ≤ x < 2^31 with mul = ⌈2^(31 + log) / d⌉ < 2^32, log = ⌈log2 d⌉: mul·d exceeds
+// 2^(31 + log) by less than d ≤ 2^log, so x·mul/2^(31 + log) exceeds x/d by less than 1/d.
+// The loaders of short tiles do several divisions a tile, one warp alone, and showed them.
 struct FastDiv {
   unsigned int mul;
   int shift, d;

@@ -7,6 +7,8 @@ import importlib.util
 import itertools
 import os
 import re
+import subprocess
+import textwrap
 
 import pytest
 import torch
@@ -107,3 +109,42 @@ def test_weights_refuse_scales_that_no_lse_can_be_divided_by(L):  # noqa: F811
         pytest.skip("a GPU is present: the calls would reach it")
     for scale, expect in ((1e-38, SCALE), (9.9e-31, SCALE), (1.1e-30, ARCH), (1e30, ARCH)):
         assert calls(L, a_cache(), tokens(), scale=scale)["weigh"]() == expect, scale
+
+
+def test_division_by_multiplication(tmp_path):
+    """FastDiv over the ends of its range: each divisor's multiples and their neighbours up to 2^31 - 1."""
+    source, program = tmp_path / "div.cpp", tmp_path / "div"
+    source.write_text(textwrap.dedent("""
+        #include <cstdio>
+        #include "cache_launch.h"
+        int main() {
+          const long long top = 0x7FFFFFFF;
+          long long bad = 0, n = 0;
+          auto check = [&](int d) {
+            const attn::FastDiv f = attn::fast_div(d);
+            auto at = [&](long long x) {
+              if (x < 0 || x > top) return;
+              ++n;
+              bad += f(static_cast<int>(x)) != x / d;
+            };
+            for (long long q = 0; q < 40; ++q)
+              for (int e = -2; e <= 2; ++e) {
+                at(q * d + e);
+                at((top / d - q) * d + e);
+                at(top - q);
+                at((1ll << (q % 31)) + e);
+              }
+          };
+          for (int d = 1; d < 70000; ++d) check(d);
+          for (int b = 16; b < 31; ++b)
+            for (int e = -3; e <= 3; ++e) check((1 << b) + e);
+          check(top);
+          check(top - 1);
+          std::printf("%lld of %lld\\n", bad, n);
+          return bad != 0;
+        }
+    """))
+    include = os.path.join(build.cuda_home(build.nvcc_path()), "include")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I" + include, "-I" + build.CSRC, str(source), "-o", str(program)], check=True)
+    r = subprocess.run([str(program)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
