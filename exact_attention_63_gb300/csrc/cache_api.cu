@@ -245,7 +245,7 @@ int attn_cache_append(const attn_cache* cache, const attn_new_tokens* x, const i
   p.vn = static_cast<const uint16_t*>(x->v);
   p.rows = rows;
   p.seq_pos = seq_pos;
-  return fail(attn::launch_cache_append(p, sms, stream), "cache append launch");
+  return fail(attn::launch_cache_append(p, stream), "cache append launch");
 }
 
 int attn_cache_weights(const attn_cache* cache, const attn_new_tokens* x, const float* lse, float scale,
@@ -313,7 +313,7 @@ int attn_cache_select(const attn_cache* cache, const int* seq_pos, int budget, i
   int dev = -1, sms = 0;
   unsigned int* status = nullptr;
   if ((rc = attn::usable_device(&dev, &status, &sms)) != ATTN_OK) return rc;
-  return fail(attn::launch_cache_select(c, seq_pos, budget, recent, kept, dev, sms, stream), "cache select launch");
+  return fail(attn::launch_cache_select(c, seq_pos, budget, recent, kept, dev, stream), "cache select launch");
 }
 
 int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cudaStream_t stream) {
@@ -328,7 +328,7 @@ int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cud
   int dev = -1, sms = 0;
   unsigned int* status = nullptr;
   if ((rc = attn::usable_device(&dev, &status, &sms)) != ATTN_OK) return rc;
-  return fail(attn::launch_cache_compact(c, kept, budget, sms, stream), "cache compact launch");
+  return fail(attn::launch_cache_compact(c, kept, budget, stream), "cache compact launch");
 }
 
 }  // extern "C"

@@ -462,20 +462,20 @@ __global__ void __launch_bounds__(kThreadsSel)
 
 }  // namespace
 
-cudaError_t launch_cache_append(const CacheAppendParams& p, int, cudaStream_t stream) {
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream) {
   const long long warps = 2ll * p.n_rows;
   cache_append_kernel<<<static_cast<unsigned int>((warps + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_compact(const CacheParams& c, const int* kept, int budget, int, cudaStream_t stream) {
+cudaError_t launch_cache_compact(const CacheParams& c, const int* kept, int budget, cudaStream_t stream) {
   const long long warps = static_cast<long long>(c.n_seq) * c.hkv * ((budget + 31) / 32);
   cache_compact_kernel<<<static_cast<unsigned int>((warps + 7) / 8), 256, 0, stream>>>(c, kept, budget);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_select(const CacheParams& c, const int* seq_pos, int budget, int recent, int* kept, int device,
-                                int, cudaStream_t stream) {
+                                cudaStream_t stream) {
   static volatile bool configured[64] = {};
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!configured[device]) {

@@ -107,9 +107,9 @@ struct CacheAppendParams {
   int n_rows;            // tokens to place: entries of rows, or total
   const int* seq_pos;
 };
-cudaError_t launch_cache_append(const CacheAppendParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_select(const CacheParams& c, const int* seq_pos, int budget, int recent, int* kept,
-                                int device, int sms, cudaStream_t stream);
-cudaError_t launch_cache_compact(const CacheParams& c, const int* kept, int budget, int sms, cudaStream_t stream);
+                                int device, cudaStream_t stream);
+cudaError_t launch_cache_compact(const CacheParams& c, const int* kept, int budget, cudaStream_t stream);
 
 }  // namespace attn
