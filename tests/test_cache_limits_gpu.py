@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import os
+import random
 import subprocess
 import sys
 import textwrap
@@ -499,3 +500,35 @@ def test_calls_of_two_threads_at_once():
             for a, b in zip(r, want[i]):
                 used = ~torch.isnan(cases[i].weights) if a.shape == cases[i].weights.shape else slice(None)
                 assert torch.equal(a[used], b[used])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    """Attention and weights of random heads, pages, lengths, trees, bounds, padding, table widths and layouts."""
+    rng = random.Random(seed)
+    d, hkv, page = rng.choice([64, 128]), rng.choice([1, 2, 3, 8]), rng.choice([16, 32, 48, 64, 128, 272])
+    H = hkv * rng.choice([1, 2, 3, 4, 5, 6, 7, 8, 16])
+    n, longest = rng.choice([1, 1, 2, 5, 9, 20]), rng.choice([5, 40, 130, 300, 1000])
+    lens = [rng.randint(0, longest) for _ in range(n)]
+    new = [rng.choice([0, 1, 1, 2, 5, rng.randint(1, rng.choice([8, 64, 128]))]) for _ in range(n)]
+    new[0] = max(new[0], 1)
+    c = Case(lens, new, H, hkv, d, page, seed=seed, tree=rng.choice(["random", "chain", "line"]), slack=rng.choice([1, 5]))
+    c.weights = torch.nan_to_num(c.weights)
+    start, pad = f64(c.weights), rng.choice([0, 3])
+    bound = rng.choice([max(new), min(128, max(new) + 7), 128])
+    c.table = torch.nn.functional.pad(c.table, (0, rng.choice([0, 3, 500])), value=-1).contiguous()
+    c.cuda()
+    if rng.random() < 0.4:
+        c.k, c.v, _ = other_layouts(c, rng.choice(["heads first", "k and v of a page together", "apart"]))
+    padded = [torch.cat([t, torch.full((pad, *t.shape[1:]), float("nan"), device="cuda", dtype=t.dtype)])
+              for t in (c.q, c.k_new, c.v_new)]
+    parents = None if c.parents is None else torch.cat([c.parents, torch.full((pad,), 5, dtype=torch.int32, device="cuda")])
+    o = torch.full((c.total + pad, H, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((H, c.total + pad), float("nan"), device="cuda")
+    cache.attn_fwd_cache(*padded, c.k, c.v, c.table, c.seq_lens, c.cu, bound, parents=parents, out=o, lse=lse)
+    assert (o[c.total:] == 7).all() and torch.isnan(lse[:, c.total:]).all()
+    check_attention(c, o[:c.total], lse[:, :c.total])
+    outs = [cache.cache_weights(padded[0], lse, c.k, c.table, c.seq_lens, c.cu, bound, c.weights,
+                                out=torch.full_like(c.weights, -9.0)) for _ in range(2)]
+    check_weights(c, lse[:, :c.total], start, outs[0])
+    assert torch.equal(*outs)
