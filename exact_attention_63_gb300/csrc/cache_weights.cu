@@ -28,8 +28,8 @@
 // The −LSE of a column comes out of the tensor core with the score: one more step
 // of 16 along the product's inner dimension multiplies a constant (1, 1, 1, 0, …) on
 // the keys' side with (hi, mid, lo, 0, …) on the rows', three bf16 numbers that add
-// up to −LSE/scale to 24 bits.  The sums then read no shared memory, whose bandwidth
-// the MMAs' operands fill: with the LSE loaded from there, one value for every four
+// up to −LSE/scale to 24 bits (an infinite hi stands alone).  The sums then read no
+// shared memory, whose bandwidth the MMAs' operands fill: with the LSE loaded from there, one value for every four
 // bytes of operands, the sums of a chunk took 2.3 times as long as the exponentials.
 //
 // Warps: 0 loads keys; 1 and 2 issue the MMAs of a half each; 3 loads the chunks of
@@ -37,7 +37,8 @@
 // and 8-11 sum a half each, a thread a key: it takes all of a chunk's scores into
 // registers at once and gives the S buffer back, so that the tensor core works on the
 // next two chunks while the exponentials of one run (twice as many sum warps that
-// kept S in TMEM meanwhile were slower: 257 against 214 us on a prompt of 8000 tokens, 32 heads over 8 at d = 128).
+// kept S in TMEM meanwhile took 257 us on a prompt of 8000 tokens, 32 heads over 8 at d = 128,
+// where these took 214; now 205).
 // TMEM: S of half w, buffer i at columns 256·i + 128·w.  Shared memory holds a ring
 // of 128-key slots for each half and one of chunks; a chunk of few rows takes little
 // room, which the key rings get (more bytes in flight where memory is the bound).

@@ -420,7 +420,8 @@ int attn_fwd_fp8_ex(const void* q8, const void* k8, const void* v8, void* o, flo
  * [0, max_blocks*page_size] is clamped, a key on a page outside [0, n_pages)
  * is read from a page inside and not written.  A malformed table gives wrong
  * results but no access outside the tensors.  Slots at or beyond seq_lens may
- * hold anything, NaN included.
+ * hold anything, NaN included; in v of the others and of the new tokens a value
+ * that is not finite may spread to rows of its sequence that do not see it (0 * inf).
  * Sequences may share pages as long as nothing writes to them: the pages that
  * attn_cache_append, attn_cache_weights and attn_cache_compact write to must
  * belong to one sequence each.
