@@ -16,7 +16,7 @@ constexpr int kCacheMaxCtas = 320;   // row tiles at work at a time (two per SM)
 // "Division by invariant integers using multiplication", 1994): x / d = x·mul >> (31 + log),
 // exact for 0 ≤ x < 2^31 with mul = ⌈2^(31 + log) / d⌉ < 2^32, log = ⌈log2 d⌉: mul·d exceeds
 // 2^(31 + log) by less than d ≤ 2^log, so x·mul/2^(31 + log) exceeds x/d by less than 1/d.
-// The loaders of short tiles do several divisions a tile, one warp alone, and showed them.
+// The loaders of short tiles do several divisions a tile, one warp alone: it showed in their time.
 struct FastDiv {
   unsigned int mul;
   int shift, d;

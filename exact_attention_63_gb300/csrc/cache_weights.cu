@@ -29,8 +29,9 @@
 // of 16 along the product's inner dimension multiplies a constant (1, 1, 1, 0, …) on
 // the keys' side with (hi, mid, lo, 0, …) on the rows', three bf16 numbers that add
 // up to −LSE/scale to 24 bits (an infinite hi stands alone).  The sums then read no
-// shared memory, whose bandwidth the MMAs' operands fill: with the LSE loaded from there, one value for every four
-// bytes of operands, the sums of a chunk took 2.3 times as long as the exponentials.
+// shared memory, whose bandwidth the MMAs' operands fill: with the LSE loaded from there,
+// one value for every four bytes of operands, the sums of a chunk took 2.3 times as long
+// as the exponentials.
 //
 // Warps: 0 loads keys; 1 and 2 issue the MMAs of a half each; 3 loads the chunks of
 // rows and prepares their columns, a chunk's LSE fetched under the one before; 4-7
