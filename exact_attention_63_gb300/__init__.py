@@ -12,4 +12,4 @@ Importing this package loads nothing native; the shared library is loaded on
 first use and a missing library raises immediately (there is no fallback).
 """
 
-__all__ = ["attn", "cache", "inputs"]
+__all__ = ["attn", "cache", "inputs", "rotary"]

@@ -30,7 +30,9 @@ EXPORTS = ["attn_fwd", "attn_fwd_ex", "attn_fwd_host", "attn_fwd_host_workspace_
            "attn_strerror", "attn_last_cuda_error", "attn_version", "attn_fwd_host_static", "attn_fwd_layout",
            "attn_fwd_varlen", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_layout", "attn_bwd_ex",
            "attn_fwd_fp8", "attn_fwd_fp8_ex", "attn_fwd_cache", "attn_fwd_cache_workspace_size", "attn_cache_append",
-           "attn_cache_weights", "attn_cache_select", "attn_cache_compact"]
+           "attn_cache_weights", "attn_cache_select", "attn_cache_compact", "attn_fwd_cache_fp8",
+           "attn_fwd_cache_fp8_workspace_size", "attn_cache_append_fp8", "attn_cache_gather_fp8", "attn_cache_pages",
+           "attn_rotary"]
 
 CAUSAL_ALIGN = {"top-left": 0, "bottom-right": 1}
 
@@ -121,6 +123,18 @@ def lib():
     L.attn_cache_select.restype = i
     L.attn_cache_compact.argtypes = [vp, vp, i, vp]
     L.attn_cache_compact.restype = i
+    L.attn_fwd_cache_fp8.argtypes = [vp, vp, vp, vp, vp, f, vp, vp, vp, sz, ctypes.POINTER(Options), vp]
+    L.attn_fwd_cache_fp8.restype = i
+    L.attn_fwd_cache_fp8_workspace_size.argtypes = [i, i, i, i]
+    L.attn_fwd_cache_fp8_workspace_size.restype = sz
+    L.attn_cache_append_fp8.argtypes = [vp, vp, vp, vp, vp, i, vp]
+    L.attn_cache_append_fp8.restype = i
+    L.attn_cache_gather_fp8.argtypes = [vp, vp, vp, vp, i, vp, vp, vp]
+    L.attn_cache_gather_fp8.restype = i
+    L.attn_cache_pages.argtypes = [vp, vp, vp, vp, i, vp, vp, vp]
+    L.attn_cache_pages.restype = i
+    L.attn_rotary.argtypes = [vp, vp, i, i, i, vp, ctypes.c_longlong, vp, i, i, f, i, vp]
+    L.attn_rotary.restype = i
     L.attn_get_status.argtypes = [vp]
     L.attn_get_status.restype = i
     L.attn_strerror.argtypes = [i]

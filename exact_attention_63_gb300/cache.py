@@ -27,6 +27,23 @@ A decoding step reads, in this order::
     kept = cache_evict(k_cache, v_cache, weights, block_table, seq_lens, budget, recent, positions, seq_pos)
     seq_lens.clamp_(max=budget)
 
+A cache may also be held in 8 bits, ``k_cache`` and ``v_cache`` as E4M3 codes (torch.float8_e4m3fn,
+or their bytes as uint8) with strides that are multiples of 16, and a power of two for each 16 slots and
+key head:
+
+  k_scales, v_scales  torch.float8_e8m0fnu (or uint8) [n_pages, H_kv, page_size / 16], contiguous
+
+``attn_fwd_cache_fp8`` attends over it, ``cache_append_fp8`` puts tokens in and sets the scales, and
+``cache_gather_fp8`` reads rows back in bf16.  Eviction works on bf16 caches.
+
+``cache_pages`` lets block tables follow the requests' lengths and gives new tokens their slots and
+positions; a step over either kind of cache then reads, in this order::
+
+    missing, slots, positions = cache_pages(lens_after, block_table, n_blocks, free_pages, n_free, page_size, cu, total)
+    q, k_new = rotary.rotary_fwd(q, k_new, positions, inv_freq)
+    o, lse = attn_fwd_cache_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu, max_new)
+    cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, lens_after, cu)
+
 Argument marshalling only; the work runs in the library's CUDA kernels.  Dense
 tensors take the short way through ``csrc/cache_bind.cpp``; strides, options, another
 stream or device, and every refusal are dealt with here.  Lengths
@@ -53,6 +70,7 @@ MAX_NEW = 128          # ATTN_CACHE_MAX_NEW
 MAX_SELECT = 1 << 20   # ATTN_CACHE_MAX_SELECT
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES, _SCALES = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
 
 
 class Cache(ctypes.Structure):
@@ -71,6 +89,13 @@ class NewTokens(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("q_strides", ctypes.c_longlong * 2), ("k_strides", ctypes.c_longlong * 2),
                 ("v_strides", ctypes.c_longlong * 2), ("cu_seqlens", ctypes.c_void_p), ("total", ctypes.c_int),
                 ("max_seqlen", ctypes.c_int), ("H", ctypes.c_int)]
+
+
+class Pages(ctypes.Structure):
+    """Mirror of ``attn_pages``."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("block_table", ctypes.c_void_p), ("n_blocks", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p), ("n_seq", ctypes.c_int),
+                ("max_blocks", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
 # The structs as bytes in native layout.
@@ -139,6 +164,23 @@ def _rows(name, t, dev):
     except AttributeError:
         pass
     _refuse(name, t, _BF16, dev, False)
+
+
+def _codes(name, t, dev):
+    """_rows of a tensor of E4M3 codes."""
+    try:
+        if t.dtype in _CODES and t.get_device() == dev and t.stride(-1) == 1:
+            return t.data_ptr(), _strides(t)
+    except AttributeError:
+        pass
+    _refuse(name, t, t.dtype if getattr(t, "dtype", None) in _CODES else _CODES[0], dev, False)
+
+
+def _scales(name, t, shape, dev):
+    ptr = _need(name, t, t.dtype if getattr(t, "dtype", None) in _SCALES else _SCALES[0], dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [n_pages, H_kv, page_size / 16] = {tuple(shape)}, not {tuple(t.shape)}")
+    return ptr
 
 
 _DENSE = tuple((0,) * max(0, n - 1) for n in range(65))
@@ -210,6 +252,24 @@ def _pack_cache(dev, k, v, block_table, seq_lens, weights, positions):
         lp = _seq("seq_lens", seq_lens, n_seq, dev)
     return (_CACHE.pack(_CACHE_SIZE, kp, vp, *ks, *vs, wp, pp, table, lp, n_pages, page_size, max_blocks, n_seq, hkv,
                         d), hkv, d, n_seq)
+
+
+def _pack_fp8(dev, k, v, k_scales, v_scales, block_table, seq_lens):
+    """attn_cache of a cache in 8 bits, checked; (bytes, k_scales, v_scales, H_kv, d, n_seq)."""
+    if v is None or seq_lens is None or k_scales is None or v_scales is None:
+        raise ValueError("v_cache, k_scales, v_scales and seq_lens are needed")
+    table = _need("block_table", block_table, _I32, dev)
+    n_seq, max_blocks = _shape("block_table", block_table, 2)
+    kp, ks = _codes("k_cache", k, dev)
+    vp, vs = _codes("v_cache", v, dev)
+    n_pages, page_size, hkv, d = _shape("k_cache", k, 4)
+    if v.shape != k.shape:
+        raise ValueError(f"v_cache {tuple(v.shape)} must be shaped like k_cache {tuple(k.shape)}")
+    shape = (n_pages, hkv, page_size // 16)
+    ksp, vsp = _scales("k_scales", k_scales, shape, dev), _scales("v_scales", v_scales, shape, dev)
+    lp = _seq("seq_lens", seq_lens, n_seq, dev)
+    return (_CACHE.pack(_CACHE_SIZE, kp, vp, *ks, *vs, 0, 0, table, lp, n_pages, page_size, max_blocks, n_seq, hkv, d),
+            ksp, vsp, hkv, d, n_seq)
 
 
 def _pack_tokens(dev, q, k, v, cu, n_seq, hkv, d, max_seqlen):
@@ -499,3 +559,202 @@ def cache_evict(k_cache, v_cache, weights, block_table, seq_lens, budget: int, r
     kept = cache_select(weights, block_table, seq_lens, budget, recent, positions, seq_pos, stream=stream)
     cache_compact(kept, k_cache, v_cache, block_table, weights, positions, stream=stream)
     return kept
+
+
+def workspace_size_fp8(H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
+    """Bytes of attn_fwd_cache_fp8's workspace (0: the sizes are not supported)."""
+    return int(attn.lib().attn_fwd_cache_fp8_workspace_size(H, H_kv, max_seqlen_q, d))
+
+
+def attn_fwd_cache_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_seqlens_q,
+                       max_seqlen_q: int, parents=None, scale: float | None = None, out=None, lse=None, workspace=None,
+                       stream=None, options=None):
+    """attn_fwd_cache over a cache held in 8 bits.
+
+    The new tokens (q, and their own k_new and v_new), parents and results are as there,
+    in bf16.  ``workspace``: a uint8 tensor of workspace_size_fp8(...) bytes, else allocated.
+    """
+    if stream is None and options is None:
+        bind = _bind or _first("k_cache", k_cache)
+        done = bind.attend_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_seqlens_q,
+                               max_seqlen_q, parents, scale, out, lse, workspace)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            attn._check(done)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return attn_fwd_cache_fp8(q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
+                                      cu_seqlens_q, max_seqlen_q, parents, scale, out, lse, workspace, None, options)
+    c, ksp, vsp, hkv, d, n_seq = _pack_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens)
+    if q is None or k_new is None or v_new is None:
+        raise ValueError("q, k_new and v_new are needed")
+    max_seqlen_q = int(max_seqlen_q)
+    x, total, H = _pack_tokens(dev, q, k_new, v_new, cu_seqlens_q, n_seq, hkv, d, max_seqlen_q)
+    par = None if parents is None else _seq("parents", parents, total, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is not None:
+        _need("out", out, _BF16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+    if lse is not None:
+        _need("lse", lse, _F32, dev)
+        if lse.shape != (H, total):
+            raise ValueError("lse must be [H, total]")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    device = k_cache.device
+    if out is None:
+        out = torch.empty((total, H, d), dtype=_BF16, device=device)
+    if lse is None:
+        lse = torch.empty((H, total), dtype=_F32, device=device)
+    if total == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(workspace_size_fp8(H, hkv, max_seqlen_q, d), dtype=torch.uint8, device=device)
+    rc = attn.lib().attn_fwd_cache_fp8(c, ksp, vsp, x, par, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _options(options), _stream(dev))
+    if rc:
+        attn._check(rc)
+    return out, lse
+
+
+def cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_new, rows=None,
+                     stream=None):
+    """cache_append into a cache held in 8 bits, in place.
+
+    Every 16 slots share a scale, the smallest power of two that holds their values; where new
+    tokens join older ones in such a block and need a larger one, the older codes are rounded
+    to it.  ``seq_lens`` (after the append), ``cu_new`` and ``rows`` are as for cache_append.
+    """
+    if stream is None:
+        bind = _bind or _first("k_cache", k_cache)
+        rc = bind.append_fp8(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_new, rows)
+        if rc is not None:
+            return attn._check(rc)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_append_fp8(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_new, rows)
+    c, ksp, vsp, hkv, d, n_seq = _pack_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens)
+    if k_new is None or v_new is None:
+        raise ValueError("k_new and v_new are needed")
+    x, total, _ = _pack_tokens(dev, None, k_new, v_new, cu_new, n_seq, hkv, d, 0)
+    n_rows, rp = 0, None
+    if rows is not None:
+        rp = _need("rows", rows, _I32, dev)
+        (n_rows,) = _shape("rows", rows, 1)
+    if total == 0 or (rows is not None and n_rows == 0):
+        return
+    rc = attn.lib().attn_cache_append_fp8(c, ksp, vsp, x, rp, n_rows, _stream(dev))
+    if rc:
+        attn._check(rc)
+
+
+def cache_gather_fp8(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_out, total: int, k_out=None,
+                     v_out=None, stream=None):
+    """The newest rows of each sequence of a cache held in 8 bits, in bf16 (exact) and packed.
+
+    Sequence s gets rows [cu_out[s], cu_out[s + 1]) of k_out and v_out [total, H_kv, d]: its newest
+    so many slots, in order (all of them where the counts are seq_lens).  Rows of no sequence, or
+    beyond its first slot, are not written.  A prompt in pieces attends over them with
+    attn_fwd_varlen, causal from the bottom right.  Returns (k_out, v_out).
+    """
+    if stream is None:
+        bind = _bind or _first("k_cache", k_cache)
+        done = bind.gather_fp8(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_out, total, k_out, v_out)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            attn._check(done)
+    dev = _device("k_cache", k_cache)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_gather_fp8(k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, cu_out, total, k_out, v_out)
+    c, ksp, vsp, hkv, d, n_seq = _pack_fp8(dev, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens)
+    cp = _seq("cu_out", cu_out, n_seq + 1, dev)
+    total = int(total)
+    if total < 0:
+        raise ValueError("total must not be negative")
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _need(name, t, _BF16, dev)
+            if t.shape != (total, hkv, d):
+                raise ValueError(f"{name} must be [total, H_kv, d] = {(total, hkv, d)}")
+    if k_out is None:
+        k_out = torch.empty((total, hkv, d), dtype=_BF16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty((total, hkv, d), dtype=_BF16, device=k_cache.device)
+    if total == 0:
+        return k_out, v_out
+    rc = attn.lib().attn_cache_gather_fp8(c, ksp, vsp, cp, total, k_out.data_ptr(), v_out.data_ptr(), _stream(dev))
+    if rc:
+        attn._check(rc)
+    return k_out, v_out
+
+
+def cache_pages(seq_lens, block_table, n_blocks, free_pages, n_free, page_size: int, cu_new=None, total: int = 0,
+                missing=None, slots=None, positions=None, stream=None):
+    """Let block tables follow the requests' lengths, and place their new tokens.
+
+    ``seq_lens`` (int32 [n_seq]) are the tokens that each sequence wants room for, 0 for one that
+    has ended.  ``block_table`` [n_seq, max_blocks], ``n_blocks`` [n_seq] (the pages each sequence
+    holds) and the stack of free pages, ``free_pages`` [n_pages] of which the first ``n_free`` [1]
+    entries count, all int32, are updated in place: pages that are no longer needed go back first,
+    then the sequences get what they lack, in order, as long as the stack lasts.  Returns
+    (missing, slots, positions): missing int32 [n_seq], the pages a sequence did not get (it then
+    keeps what it had); with ``cu_new`` (int32 [n_seq + 1]), the newest cu_new[s + 1] - cu_new[s]
+    tokens of each sequence get rows of slots, int64 [total], page * page_size + place (-1 where
+    pages lack), and positions, int32 [total], counted in the sequence.
+    """
+    if stream is None:
+        bind = _bind or _first("block_table", block_table)
+        done = bind.pages(seq_lens, block_table, n_blocks, free_pages, n_free, page_size, cu_new, total, missing, slots,
+                          positions)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            attn._check(done)
+    dev = _device("block_table", block_table)
+    if _elsewhere(dev, stream):
+        with _switched(dev, stream):
+            return cache_pages(seq_lens, block_table, n_blocks, free_pages, n_free, page_size, cu_new, total, missing, slots,
+                               positions)
+    t = Pages()
+    t.struct_size = ctypes.sizeof(Pages)
+    t.block_table = _need("block_table", block_table, _I32, dev)
+    n_seq, t.max_blocks = _shape("block_table", block_table, 2)
+    t.n_seq = n_seq
+    t.free_pages = _need("free_pages", free_pages, _I32, dev)
+    (t.n_pages,) = _shape("free_pages", free_pages, 1)
+    t.n_blocks, t.n_free = _seq("n_blocks", n_blocks, n_seq, dev), _seq("n_free", n_free, 1, dev)
+    t.page_size = page_size = int(page_size)
+    lp = _seq("seq_lens", seq_lens, n_seq, dev)
+    cp = None if cu_new is None else _seq("cu_new", cu_new, n_seq + 1, dev)
+    total = int(total)
+    if total < 0 or (total > 0 and cu_new is None):
+        raise ValueError("total must not be negative, and counts new tokens of cu_new")
+    if cu_new is None and (slots is not None or positions is not None):
+        raise ValueError("slots and positions need cu_new")
+    if missing is not None:
+        _seq("missing", missing, n_seq, dev)
+    for name, x, dtype in (("slots", slots, torch.int64), ("positions", positions, _I32)):
+        if x is not None:
+            _need(name, x, dtype, dev)
+            if x.shape != (total,):
+                raise ValueError(f"{name} must have {total} entries, not shape {tuple(x.shape)}")
+    device = block_table.device
+    if missing is None:
+        missing = torch.empty(n_seq, dtype=_I32, device=device)
+    if cu_new is not None:
+        slots = torch.empty(total, dtype=torch.int64, device=device) if slots is None else slots
+        positions = torch.empty(total, dtype=_I32, device=device) if positions is None else positions
+    rc = attn.lib().attn_cache_pages(ctypes.byref(t), lp, missing.data_ptr(), cp, total,
+                                     None if slots is None else slots.data_ptr() or None,
+                                     None if positions is None else positions.data_ptr() or None, _stream(dev))
+    if rc:
+        attn._check(rc)
+    return missing, slots, positions

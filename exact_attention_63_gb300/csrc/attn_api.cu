@@ -256,8 +256,9 @@ int usable_device(int* dev, unsigned int** status, int* sms) {
   return ATTN_OK;
 }
 
-int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
-                   const int box[4]) {
+namespace {
+int encode_4d(CUtensorMap* m, CUtensorMapDataType type, int bytes, CUtensorMapSwizzle swizzle, const void* ptr,
+              const long long dims[4], const long long strides[3], const int box[4]) {
   auto enc = get_encode_fn();
   if (enc == nullptr) {
     std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled unavailable");
@@ -269,17 +270,27 @@ int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], con
   for (int i = 0; i < 4; ++i) {
     gd[i] = static_cast<cuuint64_t>(dims[i]);
     bx[i] = static_cast<cuuint32_t>(box[i]);
-    if (i < 3) gs[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+    if (i < 3) gs[i] = static_cast<cuuint64_t>(strides[i]) * bytes;
   }
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gd, gs, bx, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(m, type, 4, const_cast<void*>(ptr), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (CUresult %d)",
                   static_cast<int>(r));
     return ATTN_ERR_LAUNCH;
   }
   return ATTN_OK;
+}
+}  // namespace
+
+int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
+                   const int box[4]) {
+  return encode_4d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, CU_TENSOR_MAP_SWIZZLE_128B, ptr, dims, strides, box);
+}
+
+int encode_u8_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3], const int box[4]) {
+  return encode_4d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
+                   box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, ptr, dims, strides, box);
 }
 
 namespace {

@@ -21,22 +21,22 @@ constexpr long long kMaxInt = 0x7FFFFFFFll;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// All zero → dense; else positive multiples of 8 below 2^38 (TMA: 16-byte
-// multiples below 2^40 bytes).
+// All zero → dense; else positive multiples of 8 (`unit`: of 16 for elements of a byte)
+// below 2^38 (TMA: 16-byte multiples below 2^40 bytes).
 template <int N>
-bool resolve(const long long in[N], const long long dense[N], long long out[N]) {
+bool resolve(const long long in[N], const long long dense[N], long long out[N], int unit = 8) {
   bool zero = true;
   for (int i = 0; i < N; ++i) zero = zero && in[i] == 0;
   for (int i = 0; i < N; ++i) {
-    if (!zero && (in[i] <= 0 || (in[i] & 7) != 0 || in[i] >= (1ll << 38))) return false;
+    if (!zero && (in[i] <= 0 || (in[i] & (unit - 1)) != 0 || in[i] >= (1ll << 38))) return false;
     out[i] = zero ? dense[i] : in[i];
   }
   return true;
 }
 
 // The cache's fields that every operator needs; k and v where `kv` says so
-// (bit 0: k, bit 1: v).
-int check_cache(const attn_cache* a, int kv, CacheParams* c) {
+// (bit 0: k, bit 1: v), in strides of multiples of `unit` elements.
+int check_cache(const attn_cache* a, int kv, CacheParams* c, int unit = 8) {
   if (a == nullptr) return ATTN_ERR_NULL;
   if (a->struct_size < sizeof(attn_cache)) return ATTN_ERR_CACHE;
   if (a->block_table == nullptr || ((kv & 1) && a->k == nullptr) || ((kv & 2) && a->v == nullptr)) return ATTN_ERR_NULL;
@@ -48,8 +48,8 @@ int check_cache(const attn_cache* a, int kv, CacheParams* c) {
   std::memset(c, 0, sizeof(*c));
   const long long hd = static_cast<long long>(a->num_kv_heads) * a->d;
   const long long dense[3] = {hd * a->page_size, hd, a->d};
-  if ((kv & 1) && !resolve<3>(a->k_strides, dense, c->k_st)) return ATTN_ERR_CACHE;
-  if ((kv & 2) && !resolve<3>(a->v_strides, dense, c->v_st)) return ATTN_ERR_CACHE;
+  if ((kv & 1) && !resolve<3>(a->k_strides, dense, c->k_st, unit)) return ATTN_ERR_CACHE;
+  if ((kv & 2) && !resolve<3>(a->v_strides, dense, c->v_st, unit)) return ATTN_ERR_CACHE;
   if (((kv & 1) && !aligned(a->k, 16)) || ((kv & 2) && !aligned(a->v, 16)) || !aligned(a->weights, 16) ||
       !aligned(a->positions, 16) || !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4))
     return ATTN_ERR_ALIGN;
@@ -154,6 +154,41 @@ Tiles tiles_of(int group, int max_new, int d) {
   // With two tiles a CTA 2·160 ends of at most 2·nt·group rows: no more than one full tile's
   // 2·320 ends of nt·group.
   t.most = t.per_cta == 2 ? tiles_of(group, t.nt, d).bytes : t.bytes;
+  return t;
+}
+
+// A cache of E4M3 codes and its scales.
+int check_fp8(const attn_cache* a, const void* k_scales, const void* v_scales, CacheParams* c, attn::Fp8Pages* f) {
+  const int rc = check_cache(a, 3, c, 16);
+  if (rc != ATTN_OK) return rc;
+  if (k_scales == nullptr || v_scales == nullptr || c->lens == nullptr) return ATTN_ERR_NULL;
+  // (its addresses and strides count bytes: `f` has the addresses)
+  f->k = static_cast<uint8_t*>(a->k);
+  f->v = static_cast<uint8_t*>(a->v);
+  f->ks = static_cast<uint8_t*>(const_cast<void*>(k_scales));
+  f->vs = static_cast<uint8_t*>(const_cast<void*>(v_scales));
+  f->per = c->page_size / attn::kFp8Block;
+  c->k = c->v = nullptr;
+  return ATTN_OK;
+}
+
+int encode_codes(CUtensorMap* m, const void* ptr, const CacheParams& c, const long long st[3], int piece) {
+  const long long dims[4] = {c.d, c.hkv, c.page_size, c.n_pages}, strides[3] = {st[2], st[1], st[0]};
+  const int box[4] = {c.d, 1, piece, 1};
+  return attn::encode_u8_4d(m, ptr, dims, strides, box);
+}
+
+// The 8-bit cache's attention: rows of a tile, and the workspace as above.
+Tiles fp8_tiles(int group, int max_new, int d) {
+  Tiles t;
+  t.nt = t.ntt = 0;
+  t.per_cta = 1;
+  t.rows = static_cast<long long>(group) * max_new <= 8 ? 8 : 16;
+  t.max_ctas = attn::kCacheMaxCtas;
+  t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
+  t.o = t.ml + up256(2ull * t.max_ctas * t.rows * sizeof(float2));
+  t.bytes = t.o + 2ull * t.max_ctas * t.rows * d * sizeof(float);
+  t.most = t.bytes;
   return t;
 }
 
@@ -329,6 +364,147 @@ int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cud
   unsigned int* status = nullptr;
   if ((rc = attn::usable_device(&dev, &status, &sms)) != ATTN_OK) return rc;
   return fail(attn::launch_cache_compact(c, kept, budget, stream), "cache compact launch");
+}
+
+size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen, int d) {
+  if (H < 1 || num_kv_heads < 1 || H % num_kv_heads != 0 || H / num_kv_heads > 128 || max_seqlen < 1 ||
+      max_seqlen > ATTN_CACHE_MAX_NEW || (d != 64 && d != 128))
+    return 0;
+  return fp8_tiles(H / num_kv_heads, max_seqlen, d).most;
+}
+
+int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
+                       const int* parents, float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       const attn_options* opts, cudaStream_t stream) {
+  if (o == nullptr || lse == nullptr) return ATTN_ERR_NULL;
+  attn::CacheAttnFp8Launch a;
+  std::memset(&a, 0, sizeof(a));
+  CacheParams& c = a.p.c;
+  int rc = check_fp8(cache, k_scales, v_scales, &c, &a.f);
+  if (rc != ATTN_OK || (rc = check_tokens(x, true, &c)) != ATTN_OK) return rc;
+  if (x->k == nullptr || x->v == nullptr) return ATTN_ERR_NULL;
+  if (x->max_seqlen > ATTN_CACHE_MAX_NEW) return ATTN_ERR_SHAPE;
+  const Tiles w = fp8_tiles(c.group, c.max_new, c.d);
+  const long long tiles = (static_cast<long long>(c.group) * c.max_new + w.rows - 1) / w.rows;
+  // Units and rows of the two kernels' grids.
+  if (tiles * c.n_seq * c.hkv > kMaxInt / (c.cap / 128 + 3) || tiles * c.n_seq * c.hkv * w.rows > kMaxInt ||
+      static_cast<long long>(x->H) * c.total > kMaxInt)
+    return ATTN_ERR_SHAPE;
+  if ((rc = check_scale(scale)) != ATTN_OK) return rc;
+  const long long hd = static_cast<long long>(x->H) * c.d, kd = static_cast<long long>(c.hkv) * c.d;
+  const long long q_dense[2] = {hd, c.d}, k_dense[2] = {kd, c.d};
+  if (!resolve<2>(x->q_strides, q_dense, a.q_st) || !resolve<2>(x->k_strides, k_dense, a.kn_st) ||
+      !resolve<2>(x->v_strides, k_dense, a.vn_st))
+    return ATTN_ERR_CACHE;
+  if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(parents, 4))
+    return ATTN_ERR_ALIGN;
+  if ((rc = check_options(opts, &a.p.timeout_ns, &a.p.test_flags)) != ATTN_OK) return rc;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.bytes) return ATTN_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = attn::usable_device(&a.device, &a.p.status, &sms)) != ATTN_OK) return rc;
+
+  a.q = static_cast<const uint16_t*>(x->q);
+  a.kn = static_cast<const uint16_t*>(x->k);
+  a.vn = static_cast<const uint16_t*>(x->v);
+  a.p.parents = parents;
+  a.p.o = static_cast<uint16_t*>(o);
+  a.p.lse = lse;
+  char* const ws = static_cast<char*>(workspace);
+  a.p.ws_table = reinterpret_cast<int*>(ws);
+  a.p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
+  a.p.rows = w.rows;
+  const int low = c.page_size & -c.page_size;
+  a.p.piece = low < 128 ? low : 128;
+  a.p.scale_log2 = scale * 1.4426950408889634f;
+  a.grid = sms < w.max_ctas ? sms : w.max_ctas;
+  a.stream = stream;
+  if ((rc = encode_codes(&a.k, a.f.k, c, c.k_st, a.p.piece)) != ATTN_OK ||
+      (rc = encode_codes(&a.v, a.f.v, c, c.v_st, a.p.piece)) != ATTN_OK)
+    return rc;
+  return fail(attn::launch_cache_attn_fp8(a), "8-bit cache attention launch");
+}
+
+int attn_cache_append_fp8(const attn_cache* cache, void* k_scales, void* v_scales, const attn_new_tokens* x,
+                          const int* rows, int n_rows, cudaStream_t stream) {
+  attn::CacheAppendFp8Params p;
+  std::memset(&p, 0, sizeof(p));
+  int rc = check_fp8(cache, k_scales, v_scales, &p.c, &p.f);
+  if (rc != ATTN_OK || (rc = check_tokens(x, false, &p.c)) != ATTN_OK) return rc;
+  if (x->k == nullptr || x->v == nullptr) return ATTN_ERR_NULL;
+  p.n_rows = rows != nullptr ? n_rows : x->total;
+  if ((rows != nullptr && n_rows < 1) || x->total > kMaxCapacity || n_rows > kMaxCapacity ||
+      (p.n_rows / 16 + 2ll * p.c.n_seq) * 2 * p.c.hkv > kMaxInt)
+    return ATTN_ERR_SHAPE;
+  const long long kd = static_cast<long long>(p.c.hkv) * p.c.d, dense[2] = {kd, p.c.d};
+  if (!resolve<2>(x->k_strides, dense, p.kn_st) || !resolve<2>(x->v_strides, dense, p.vn_st)) return ATTN_ERR_CACHE;
+  if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(rows, 4)) return ATTN_ERR_ALIGN;
+  int dev = -1, sms = 0;
+  unsigned int* status = nullptr;
+  if ((rc = attn::usable_device(&dev, &status, &sms)) != ATTN_OK) return rc;
+  p.kn = static_cast<const uint16_t*>(x->k);
+  p.vn = static_cast<const uint16_t*>(x->v);
+  p.rows = rows;
+  return fail(attn::launch_cache_append_fp8(p, stream), "8-bit cache append launch");
+}
+
+int attn_cache_gather_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const int* cu_out,
+                          int total, void* k_out, void* v_out, cudaStream_t stream) {
+  if (cu_out == nullptr || k_out == nullptr || v_out == nullptr) return ATTN_ERR_NULL;
+  attn::CacheGatherFp8Params p;
+  std::memset(&p, 0, sizeof(p));
+  int rc = check_fp8(cache, k_scales, v_scales, &p.c, &p.f);
+  if (rc != ATTN_OK) return rc;
+  if (total < 1 || total > kMaxCapacity) return ATTN_ERR_SHAPE;
+  if (!aligned(cu_out, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return ATTN_ERR_ALIGN;
+  int dev = -1, sms = 0;
+  unsigned int* status = nullptr;
+  if ((rc = attn::usable_device(&dev, &status, &sms)) != ATTN_OK) return rc;
+  p.c.cu = cu_out;
+  p.c.total = total;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  return fail(attn::launch_cache_gather_fp8(p, stream), "8-bit cache gather launch");
+}
+
+int attn_cache_pages(const attn_pages* t, const int* seq_lens, int* missing, const int* cu_new, int total,
+                     long long* slots, int* positions, cudaStream_t stream) {
+  if (t == nullptr || seq_lens == nullptr || missing == nullptr) return ATTN_ERR_NULL;
+  if (t->struct_size < sizeof(attn_pages)) return ATTN_ERR_CACHE;
+  if (t->block_table == nullptr || t->n_blocks == nullptr || t->free_pages == nullptr || t->n_free == nullptr ||
+      (cu_new != nullptr && total > 0 && (slots == nullptr || positions == nullptr)))
+    return ATTN_ERR_NULL;
+  if (t->n_seq < 1 || t->max_blocks < 1 || t->n_pages < 1 || total < 0 || total > kMaxCapacity ||
+      static_cast<long long>(t->n_seq) * t->max_blocks > kMaxInt)
+    return ATTN_ERR_SHAPE;
+  if (t->page_size < 16 || t->page_size > 65536 || t->page_size % 16 != 0 || t->n_seq > attn::kCacheMaxSeq ||
+      static_cast<long long>(t->max_blocks) * t->page_size > kMaxCapacity)
+    return ATTN_ERR_CACHE;
+  if (!aligned(t->block_table, 4) || !aligned(t->n_blocks, 4) || !aligned(t->free_pages, 4) || !aligned(t->n_free, 4) ||
+      !aligned(seq_lens, 4) || !aligned(missing, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) || !aligned(positions, 4))
+    return ATTN_ERR_ALIGN;
+  int dev = -1, sms = 0;
+  unsigned int* status = nullptr;
+  const int rc = attn::usable_device(&dev, &status, &sms);
+  if (rc != ATTN_OK) return rc;
+  attn::CachePagesParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.lens = seq_lens;
+  p.table = t->block_table;
+  p.n_blocks = t->n_blocks;
+  p.free_pages = t->free_pages;
+  p.n_free = t->n_free;
+  p.missing = missing;
+  p.cu = cu_new;
+  p.slots = slots;
+  p.positions = positions;
+  p.n_seq = t->n_seq;
+  p.max_blocks = t->max_blocks;
+  p.n_pages = t->n_pages;
+  p.page_size = t->page_size;
+  p.total = total;
+  p.by_page = attn::fast_div(t->page_size);
+  return fail(attn::launch_cache_pages(p, stream), "page tables launch");
 }
 
 }  // extern "C"

@@ -98,6 +98,64 @@ struct CacheWeightLaunch {
 };
 cudaError_t launch_cache_weights(const CacheWeightLaunch& a);
 
+// A cache of E4M3 codes: k and v of CacheParams are null, its strides count bytes.
+constexpr int kFp8Block = 16;              // slots that share a scale
+constexpr int kFp8Lowest = 127 - 117, kFp8Highest = 127 + 119;  // exponent bytes of a scale
+struct Fp8Pages {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ks;           // [n_pages, hkv, per] exponent bytes: 2^(byte - 127)
+  uint8_t* vs;
+  int per;               // page_size / 16
+};
+
+struct CacheAttnFp8Launch {
+  CUtensorMap k, v;      // box (d, 1, piece, 1) of bytes
+  CacheAttnParams p;
+  Fp8Pages f;
+  const uint16_t* q;
+  const uint16_t* kn;
+  const uint16_t* vn;
+  long long q_st[2], kn_st[2], vn_st[2];  // element strides: token, head
+  int grid, device;
+  cudaStream_t stream;
+};
+cudaError_t launch_cache_attn_fp8(const CacheAttnFp8Launch& a);
+
+struct CacheAppendFp8Params {
+  CacheParams c;
+  Fp8Pages f;
+  const uint16_t* kn;
+  const uint16_t* vn;
+  long long kn_st[2], vn_st[2];
+  const int* rows;       // may be null
+  int n_rows;            // tokens to place: entries of rows, or total
+};
+cudaError_t launch_cache_append_fp8(const CacheAppendFp8Params& p, cudaStream_t stream);
+
+struct CacheGatherFp8Params {
+  CacheParams c;         // cu, total: of the rows that are written
+  Fp8Pages f;
+  uint16_t* k_out;       // [total, hkv, d]
+  uint16_t* v_out;
+};
+cudaError_t launch_cache_gather_fp8(const CacheGatherFp8Params& p, cudaStream_t stream);
+
+struct CachePagesParams {
+  const int* lens;       // [n_seq]
+  int* table;            // [n_seq, max_blocks]
+  int* n_blocks;         // [n_seq]
+  int* free_pages;       // [n_pages]
+  int* n_free;           // [1]
+  int* missing;          // [n_seq]
+  const int* cu;         // [n_seq + 1], may be null
+  long long* slots;      // [total]
+  int* positions;        // [total]
+  int n_seq, max_blocks, n_pages, page_size, total;
+  FastDiv by_page;
+};
+cudaError_t launch_cache_pages(const CachePagesParams& p, cudaStream_t stream);
+
 struct CacheAppendParams {
   CacheParams c;
   const uint16_t* kn;

@@ -571,6 +571,134 @@ int attn_cache_select(const attn_cache* cache, const int* seq_pos, int budget, i
  */
 int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A cache held in 8 bits.
+ *
+ * The same attn_cache, with k and v pointing to E4M3 codes (one byte an element;
+ * strides count elements and are multiples of 16 below 2^38, all zero = dense;
+ * weights and positions are not used), and two tensors of scales:
+ *   k_scales, v_scales : device, bytes [n_pages, num_kv_heads, page_size / 16].
+ *                 Byte b is the scale 2^(b - 127) of 16 slots of a page and key
+ *                 head: a code c stands for c * 2^(b - 127).  Bytes below 10 and
+ *                 above 246 count as those (every value is then a bf16 number).
+ * Lengths and tables are dealt with as above; slots at or beyond seq_lens may hold
+ * any code, NaN included.
+ * ------------------------------------------------------------------------ */
+#define ATTN_FP8_BLOCK 16
+
+/*
+ * attn_fwd_cache_fp8 — attn_fwd_cache over a cache held in 8 bits: the same new
+ * tokens (q and their own k and v in bf16), parents, outputs, options and errors.
+ *   workspace : at least attn_fwd_cache_fp8_workspace_size(...) bytes, which
+ *             suffice for every smaller max_seqlen and any total too.
+ * Codes and scales are exact in the products; P is rounded to 16 bits, statistics
+ * and sums are fp32.
+ */
+size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen, int d);
+int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
+                       const int* parents, float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       const attn_options* opts, cudaStream_t stream);
+
+/*
+ * attn_cache_append_fp8 — put new tokens' keys and values into the cache, as
+ * attn_cache_append places them (seq_lens after the append, rows).
+ *   A block of 16 slots whose first slot is new gets the smallest scale 2^e with
+ *   |x| <= 448 * 2^e for all of its new values (e from -117 to 119); one that holds
+ *   older tokens gets the larger of that and the scale it has, and if that grows,
+ *   the older codes are rounded to the new one.  Values that are not finite do not
+ *   count.  Codes are x / 2^e to nearest even; beyond +-448 (infinities) the largest
+ *   code, NaN stays NaN.
+ * total and n_rows are at most 2^30.
+ */
+int attn_cache_append_fp8(const attn_cache* cache, void* k_scales, void* v_scales, const attn_new_tokens* x,
+                          const int* rows, int n_rows, cudaStream_t stream);
+
+/*
+ * attn_cache_gather_fp8 — the newest rows of each sequence, in bf16 (exact) and
+ * packed: what attn_fwd_varlen attends over when a prompt comes in pieces longer
+ * than attn_fwd_cache_fp8 takes.
+ *   cu_out  : device, int32 [n_seq + 1], ascending from 0, clamped to [0, total]:
+ *             the n rows [cu_out[s], cu_out[s + 1]) are slots seq_lens[s] - n on.
+ *             A row whose slot would be negative is not written, nor is one before
+ *             cu_out[0] or behind cu_out[n_seq].
+ *   k_out, v_out : device, bf16 [total, num_kv_heads, d].
+ * total is at most 2^30.
+ */
+int attn_cache_gather_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const int* cu_out,
+                          int total, void* k_out, void* v_out, cudaStream_t stream);
+
+/*
+ * attn_cache_pages — block tables that follow the requests' lengths, and the slots
+ * of their new tokens.  For any cache above.
+ *   attn_pages (zero-initialise, set struct_size), all of it updated in place:
+ *   block_table : device, int32 [n_seq, max_blocks].
+ *   n_blocks    : device, int32 [n_seq]: the pages that each sequence holds.
+ *   free_pages  : device, int32 [n_pages]; the first n_free[0] entries are a stack
+ *                 of the pages that nobody holds.
+ *   seq_lens    : device, int32 [n_seq]: tokens that each sequence wants room for;
+ *                 0 for one that has ended.
+ * With want = ceil(seq_lens / page_size): first every sequence gives back the pages
+ * of its blocks from `want` on (pushed in the order of sequences and blocks; the
+ * entries become -1).  Then, in the sequences' order, each one that holds fewer
+ * takes pages from the top of the stack, if it holds what this sequence and all
+ * before it lack (whether those were served or not); otherwise it keeps what it
+ * has.  A sequence with want > max_blocks gets nothing and is not counted.
+ *   missing     : device, int32 [n_seq] (written): the pages that a sequence lacks.
+ *   cu_new      : device, int32 [n_seq + 1], or NULL: the n new tokens of sequence s
+ *                 are rows [cu_new[s], cu_new[s + 1]) of slots and positions, and
+ *                 the last n of its seq_lens.
+ *   slots       : device, int64 [total]: page * page_size + place of a new token; -1
+ *                 where its sequence lacks pages or the slot would be negative.
+ *   positions   : device, int32 [total]: its slot in the sequence.  Rows of no
+ *                 sequence are not written.
+ * page_size and n_seq as for attn_cache, n_seq * max_blocks below 2^31, total at most
+ * 2^30.  Results do not depend on timing.  Counts out of range are clamped.
+ */
+typedef struct attn_pages {
+  size_t struct_size;
+  int* block_table;
+  int* n_blocks;
+  int* free_pages;
+  int* n_free;
+  int n_seq, max_blocks, n_pages, page_size;
+} attn_pages;
+int attn_cache_pages(const attn_pages* tables, const int* seq_lens, int* missing, const int* cu_new, int total,
+                     long long* slots, int* positions, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * attn_rotary — rotary positions on q and k, before attention or the cache.
+ *   With the angle a = position * inv_freq[i] of pair i < rotary_dim / 2 of a head's
+ *   elements (u, w):  u' = m (u cos a - w sin a),  w' = m (w cos a + u sin a).
+ *   Pair i is elements (2i, 2i + 1) where interleaved, else (i, i + rotary_dim / 2);
+ *   elements from rotary_dim on are copied.  `inverse` turns by -a, with the same
+ *   factor m: the gradient of q and k from that of the results.
+ *   attn_rows (zero-initialise, set struct_size) describes q, and k (k may be NULL):
+ *   x           : device, bf16 [batch, rows, heads, d]; y: the results, shaped alike.
+ *                 y may be x (with the same strides), else they do not overlap.
+ *   x_strides, y_strides : element strides of batch, row and head, positive multiples
+ *                 of 8 below 2^38 (all zero = dense); the d elements are contiguous.
+ *   positions   : device, int32 [batch, rows], batches positions_stride elements
+ *                 apart (0: one row of them for all); NULL: the row's number.
+ *                 May be negative.
+ *   inv_freq    : device, fp64 [rotary_dim / 2], radians a position, finite.
+ *   rotary_dim  : even, 2 to d.  magnitude: m, finite.  d is 64 or 128.
+ * The angle is taken modulo a turn in 64 bits, so far positions lose nothing; sines,
+ * products and sums are fp32, rounded once.  batch * rows is at most 2^30.
+ * Asynchronous on `stream`, allocates nothing; errors as for attn_fwd, and
+ * ATTN_ERR_LAYOUT for strides, rotary_dim or the struct's size.
+ * ------------------------------------------------------------------------ */
+typedef struct attn_rows {
+  size_t struct_size;
+  const void* x;
+  void* y;
+  long long x_strides[3];
+  long long y_strides[3];
+  int heads;
+} attn_rows;
+int attn_rotary(const attn_rows* q, const attn_rows* k, int batch, int rows, int d, const int* positions,
+                long long positions_stride, const double* inv_freq, int rotary_dim, int interleaved, float magnitude,
+                int inverse, cudaStream_t stream);
+
 /*
  * attn_get_status — synchronises `stream`, then returns and clears the current
  * device's status word: ATTN_OK, or ATTN_ERR_TIMEOUT if any kernel launched
