@@ -172,24 +172,39 @@ int check_fp8(const attn_cache* a, const void* k_scales, const void* v_scales, C
   return ATTN_OK;
 }
 
-int encode_codes(CUtensorMap* m, const void* ptr, const CacheParams& c, const long long st[3], int piece) {
-  const long long dims[4] = {c.d, c.hkv, c.page_size, c.n_pages}, strides[3] = {st[2], st[1], st[0]};
-  const int box[4] = {c.d, 1, piece, 1};
+// Pages as (d, slot, head, page): a copy of several heads lies head by head.
+int encode_codes(CUtensorMap* m, const void* ptr, const CacheParams& c, const long long st[3], int piece, int hg) {
+  const long long dims[4] = {c.d, c.page_size, c.hkv, c.n_pages}, strides[3] = {st[1], st[2], st[0]};
+  const int box[4] = {c.d, piece, hg, 1};
   return attn::encode_u8_4d(m, ptr, dims, strides, box);
 }
 
-// The 8-bit cache's attention: rows of a tile, and the workspace as above.
-Tiles fp8_tiles(int group, int max_new, int d) {
+// The 8-bit cache's attention: rows of a tile, key heads that a CTA works on at a time, and
+// the workspace as above.  Any number of rows and heads up to the largest may be asked for,
+// so `most` counts full tiles of eight heads.
+Tiles fp8_tiles(int group, int max_new, int d, int hg) {
   Tiles t;
   t.nt = t.ntt = 0;
   t.per_cta = 1;
   t.rows = static_cast<long long>(group) * max_new <= 8 ? 8 : 16;
-  t.max_ctas = attn::kCacheMaxCtas;
+  t.max_ctas = attn::kCacheMaxCtas / 2;
+  const size_t ends = 2ull * t.max_ctas * t.rows * hg;
   t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
-  t.o = t.ml + up256(2ull * t.max_ctas * t.rows * sizeof(float2));
-  t.bytes = t.o + 2ull * t.max_ctas * t.rows * d * sizeof(float);
+  t.o = t.ml + up256(ends * sizeof(float2));
+  t.bytes = t.o + ends * d * sizeof(float);
   t.most = t.bytes;
   return t;
+}
+
+// Key heads of a run: as many as a CTA's eight warps hold, where the heads allow it; of one
+// sequence alone at most 2, which leaves fewer and larger parts to join (one token over 4000,
+// 8000, 16000 cached ones: 12.3, 14.0, 15.9 us instead of 15.3, 16.2, 18.1; from two sequences on
+// 8 is no slower: 13.7 and 15.5 us for two of 2000, 26 and 37 us for 64 of up to 500).
+int heads_at_once(int hkv, int n_seq) {
+  const int most = n_seq == 1 ? 2 : 8;
+  int hg = 1;
+  while (hg < most && hkv % (2 * hg) == 0) hg *= 2;
+  return hg;
 }
 
 }  // namespace
@@ -242,6 +257,7 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
   a.p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
   a.p.rows = w.rows;
+  a.p.hg = 1;
   a.p.nt = w.nt;
   a.p.ntt = w.ntt;
   a.tiles = w.per_cta;
@@ -370,7 +386,7 @@ size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen
   if (H < 1 || num_kv_heads < 1 || H % num_kv_heads != 0 || H / num_kv_heads > 128 || max_seqlen < 1 ||
       max_seqlen > ATTN_CACHE_MAX_NEW || (d != 64 && d != 128))
     return 0;
-  return fp8_tiles(H / num_kv_heads, max_seqlen, d).most;
+  return fp8_tiles(H / num_kv_heads, max_seqlen, d, heads_at_once(num_kv_heads, 2)).most;
 }
 
 int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
@@ -384,7 +400,8 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   if (rc != ATTN_OK || (rc = check_tokens(x, true, &c)) != ATTN_OK) return rc;
   if (x->k == nullptr || x->v == nullptr) return ATTN_ERR_NULL;
   if (x->max_seqlen > ATTN_CACHE_MAX_NEW) return ATTN_ERR_SHAPE;
-  const Tiles w = fp8_tiles(c.group, c.max_new, c.d);
+  const int hg = heads_at_once(c.hkv, c.n_seq);
+  const Tiles w = fp8_tiles(c.group, c.max_new, c.d, hg);
   const long long tiles = (static_cast<long long>(c.group) * c.max_new + w.rows - 1) / w.rows;
   // Units and rows of the two kernels' grids.
   if (tiles * c.n_seq * c.hkv > kMaxInt / (c.cap / 128 + 3) || tiles * c.n_seq * c.hkv * w.rows > kMaxInt ||
@@ -415,12 +432,13 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
   a.p.rows = w.rows;
   const int low = c.page_size & -c.page_size;
-  a.p.piece = low < 128 ? low : 128;
+  a.p.hg = hg;
+  a.p.piece = low < 128 / hg ? low : 128 / hg;
   a.p.scale_log2 = scale * 1.4426950408889634f;
   a.grid = sms < w.max_ctas ? sms : w.max_ctas;
   a.stream = stream;
-  if ((rc = encode_codes(&a.k, a.f.k, c, c.k_st, a.p.piece)) != ATTN_OK ||
-      (rc = encode_codes(&a.v, a.f.v, c, c.v_st, a.p.piece)) != ATTN_OK)
+  if ((rc = encode_codes(&a.k, a.f.k, c, c.k_st, a.p.piece, hg)) != ATTN_OK ||
+      (rc = encode_codes(&a.v, a.f.v, c, c.v_st, a.p.piece, hg)) != ATTN_OK)
     return rc;
   return fail(attn::launch_cache_attn_fp8(a), "8-bit cache attention launch");
 }

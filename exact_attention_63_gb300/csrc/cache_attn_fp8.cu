@@ -1,4 +1,4 @@
-// Attention of new tokens over a paged cache of E4M3 codes and over each other.
+// Attention of new tokens over a paged cache of E4M3 codes and over each other, few rows.
 //
 //   s_tj = scale·q_t·k_j,  O_t = Σ_j exp(s_tj − LSE_t)·v_j,  LSE_t = ln Σ_j exp(s_tj),
 // with k_j = 2^a·K_j and v_j = 2^b·V_j for the cached keys (codes K, V; a, b of the block of
@@ -6,24 +6,29 @@
 //
 // The rows of one (sequence, key head) are its (token, head of the group) pairs, eight a
 // column tile of the matrix instruction.  With few of them the operator is bound by reading
-// the codes: 2d bytes a key.  So everything between memory and the sums is kept short: a
-// code becomes an f16 number in one instruction for two (its four bits are exact there), and
-// goes from the ring straight into the fragments of m16n8k16 products whose M side is the
-// cache:  Sᵀ = K·Qᵀ (16 keys × 8 rows), Oᵀ += Vᵀ·Pᵀ (16 values × 8 rows).  Codes taken to
-// bf16 tiles in shared memory for tcgen05 would cross it three times more, 6 bytes an
-// element where 5.5 are all that its 128 bytes a cycle leave at the copy rate.
-//   A warp's 16 keys are one block of scales, so 2^a is one factor of its scores and 2^b one
-// of its product, which is added to O in fp32.
+// the codes: 2d bytes a key.  So everything between memory and the sums is kept short.  The
+// M side of the m16n8k16 products is the cache:  Sᵀ = K·Qᵀ (16 keys × 8 rows), Oᵀ += Vᵀ·Pᵀ
+// (16 values × 8 rows); which key or element a fragment's row or column stands for is free
+// as long as both sides agree, so a lane reads whole runs of 16 bytes of the cache, and a code
+// becomes an f16 number (exactly) in one instruction for two.
+//   A warp has a key head and every (16 / hg)-th block of 16 slots of its CTA's range, a block
+// being one block of scales: 2^a is one factor of its scores, 2^b one of its product, which
+// is added to O in fp32.  Each lane copies the bytes that it will read itself, so nothing is
+// handed from thread to thread: no barrier, no wait of one warp for another before the end of a
+// tile, where the warps of a head meet.  (With a loading warp and TMA the copies' issue set the pace, two
+// to four cycles a row of 128 or 64 bytes: 146 us for one token over 64 sequences of up to
+// 8191 at d = 128, 113 at d = 64.)
 //   Q's rows are scaled by a power of two to a maximum of 2^14 … 2^15 before they become f16:
 // values down to 2^−28 of the largest keep all eight bits, the rest are off by less than
 // 2^−39 of it, less than the fp32 sum of the products.  P, in units where the running
 // maximum is 2^7 (at most 2^15 until it is moved), is rounded to f16: 2^−11 relative, and
 // what lies below f16's range is less than 2^−32 of the largest.
 //
-// Work units are blocks of 128 keys of one (sequence, key head, row tile), dealt out evenly
-// as in cache_attn.cu, and the parts of a tile are joined by the same second kernel.  In a
-// CTA one warp loads, the others take 16 keys of every block each, with a maximum, sum and O
-// of their own that meet in shared memory at the end of a tile.
+// Work units are blocks of 128 / hg keys of hg key heads (8 where the number of heads is a
+// multiple of 8) of one sequence and row tile, 32 KB of codes at d = 128, dealt out evenly
+// as in cache_attn.cu; the parts of a tile are joined by the same second kernel.  With all
+// heads of a token in one block the pages are read as they lie (hg = 1: 220 us where 8 takes
+// 146, before the copies).
 #include "cache_join.cuh"
 #include "fp8_device.cuh"
 
@@ -32,6 +37,8 @@ namespace {
 
 constexpr float kShift = 7.0f;  // log2 of P where a score is the reference maximum
 constexpr float kTau = 8.0f;    // log2: the reference moves when exceeded by more
+constexpr float kNone = -3e38f; // the reference before any score
+constexpr int kLookUp = 16;     // blocks looked up at a time
 
 struct CacheAttnFp8Params {
   CacheAttnParams a;
@@ -42,33 +49,39 @@ struct CacheAttnFp8Params {
   long long q_st[2], kn_st[2], vn_st[2];
 };
 
-// The blocks of 128 cached keys; the new tokens go with the last.
+// The blocks of 128 / hg cached keys; the new tokens go with the last.
 struct RowsPlan {
+  static constexpr bool kEight = true;
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) {
     KeyPlan k;
     const SeqRows r = seq_rows(p.c, s);
     k.q0 = r.q0;
     k.n = min(r.n, p.c.max_new);
     k.len = seq_len(p.c, s);
-    k.nfull = k.len >> 7;
-    k.tail = k.len & 127;
-    k.off = 0;
-    k.db = max((k.len + 127) >> 7, 1) - 1;
+    const int keys = 128 / p.hg;
+    k.nfull = k.tail = k.off = 0;  // (of the other kernel's blocks)
+    k.db = max((k.len + keys - 1) / keys, 1) - 1;
     return k;
   }
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D = A·B + C, m16n8k16.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
+                                    float c2, float c3) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool add) {
+  if (add) mma<F16>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+  else mma<F16>(d, a, b0, b1, 0.f, 0.f, 0.f, 0.f);
 }
 // Transposes an 8 × 8 tile of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -87,74 +100,63 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t (&r)[2]) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A block's 16 rows of D bytes in shared memory: where 16-byte run c of row r lies.
+template <int D>
+__device__ __forceinline__ uint32_t run_at(int r, int c) {
+  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+// The key that row (of Sᵀ) or column (of Vᵀ) i < 8 of a fragment stands for, i + 8 for the
+// key 8 further.  With run_at's places neither the rows 2q and 2q + 1 of K that eight lanes
+// read together, nor the columns 2t of V, meet in a bank.
+template <int D>
+__device__ __forceinline__ int key_of(int i) {
+  const int t = i >> 1;
+  return D == 128 ? (2 * t + (t >> 1)) ^ ((i & 1) << 2) : i ^ (t & 1);
 }
 
 template <int D, int NT>
 struct FL {
-  static constexpr int kWarps = 8;                       // of 16 keys each
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr uint32_t kKeys = 128u * D;            // bytes of a block's K or V
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr uint32_t kRing = 0;                   // [stage][K, V]
-  static constexpr int kPitch = D + 8;                   // floats a row of a warp's O: no bank conflicts
-  static constexpr uint32_t kMerge = kStages * 2 * kKeys;        // [warp][8 rows][kPitch]
-  static constexpr uint32_t kMl = kMerge + kWarps * 8 * kPitch * 4;  // [warp][8 NT] reference maximum and sum
-  static constexpr uint32_t kScales = kMl + kWarps * 8 * NT * 8;     // [stage][8 of K, 8 of V]
-  static constexpr uint32_t kBar = kScales + kStages * 16;
-  static constexpr uint32_t kMisc = kBar + 8 * 2 * kStages;  // abort flag
-  static constexpr uint32_t kSums = kMisc + 8;
-  static constexpr uint32_t kTable = (kSums + 4 * (kWarps + 1) + 15) & ~15u;
-  static constexpr uint32_t kBytes = kTable + 1024;      // + alignment; the table comes on top
+  static constexpr int kGroups = NT == 1 ? 2 : 1;        // of eight warps: a unit is one group's
+  static constexpr int kWarps = 8 * kGroups;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr uint32_t kKeys = 16u * D;             // bytes of a block's K or V, of one head
+  static constexpr int kStages = (D == 128 ? 3 : 6) * (2 / kGroups);  // blocks of a warp: one at work, the others on their way
+  static constexpr uint32_t kRing = 0;                   // [warp][stage][K, V][16 rows]
+  static constexpr uint32_t kMergeWarp = NT * D / 32 * 32 * 16;  // half of a warp's O, as its lanes hold it
+  static constexpr uint32_t kMerge = kWarps * kStages * 2 * kKeys;
+  static constexpr uint32_t kMl = kMerge + 4 * kGroups * kMergeWarp;  // [8][NT][2][lane] maximum and sum
+  static constexpr uint32_t kOffsets = kMl + 8 * NT * 2 * 32 * 8;    // [warp][kLookUp] of K and V, bytes
+  static constexpr uint32_t kScales = kOffsets + kWarps * kLookUp * 16;  // [warp][stage] bytes of K and V
+  static constexpr uint32_t kSums = kScales + kWarps * kStages * 2;
+  static constexpr uint32_t kTable = (kSums + 4 * kWarps + 15) & ~15u;
+  static constexpr uint32_t kBytes = kTable + 128;       // + alignment; the table comes on top
 };
 
-// Where 16-byte chunk c of row r lies in a tile of rows of D bytes, as TMA's swizzle of
-// 128 (64) bytes puts it.
-template <int D>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-}
-// Key of fragment row g: two rows that are read together have to differ in the bit that
-// picks the half of the 32 banks.
-template <int D>
-__device__ __forceinline__ int key_of(int g) {
-  return D == 128 ? (g >> 1) | ((g & 1) << 2) : g;
-}
-
 template <int D, int NT>
-__global__ void __launch_bounds__(FL<D, NT>::kThreads, 1)
-    cache_attn_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const CacheAttnFp8Params fp) {
+__global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(const CacheAttnFp8Params fp) {
   using L = FL<D, NT>;
   const CacheAttnParams& p = fp.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t base = (raw + 127u) & ~127u;
   uint8_t* const smem = smem_raw + (base - raw);
-  auto full = [&](int s) { return base + L::kBar + 8u * s; };
-  auto empty = [&](int s) { return base + L::kBar + 8u * (L::kStages + s); };
-  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   int* const tab = reinterpret_cast<int*>(smem + L::kTable);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0u;
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), L::kWarps);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_proxy_async_smem();
-  }
-  if (threadIdx.x == 32) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
   prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums),
                [&](int s) { return units_of<RowsPlan>(p, s); });
   const int units = tab[p.c.n_seq];
@@ -164,95 +166,94 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= grid) return;
   const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
-  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
 
-  if (warp == L::kWarps) {
-    // ============================================================= loader
-    // Lane i < 8 copies the keys of the block's i-th 16 slots (with those behind them, as
-    // many as a copy holds) and lane 8 + i their values; both fetch the scale as well.
-    int g = 0, copies = 0;
-    bool ok = true;
-    const int i16 = lane & 7, ps = p.piece;
-    const bool is_v = lane >= 8;
-    for (int u = u0; u < u1 && ok;) {
-      const Segment sg = segment_at<RowsPlan>(p, tab, u, u1);
-      u += sg.b1 - sg.b0;
-      int page_next = 0, slot_next = 0;  // of the block after the next
-      auto locate = [&](int b) {
-        const int j = (b << 7) + 16 * i16;
-        const int blk = j / p.c.page_size;
-        slot_next = j - blk * p.c.page_size;
-        page_next = lane < 16 && j < sg.k.len ? page_for_read(p.c, sg.s, blk) : 0;
-      };
-      auto scale_of = [&](int b, int page, int slot) -> uint8_t {
-        if (lane >= 16 || (b << 7) + 16 * i16 >= sg.k.len) return 0;
-        return (is_v ? fp.f.vs : fp.f.ks)[(static_cast<long long>(page) * p.c.hkv + sg.h) * fp.f.per + (slot >> 4)];
-      };
-      locate(sg.b0);
-      int page = page_next, slot = slot_next;
-      uint8_t scale = scale_of(sg.b0, page, slot);
-      if (sg.b0 + 1 < sg.b1) locate(sg.b0 + 1);
-      for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
-        const int st = g % L::kStages, ph = (g / L::kStages) & 1;
-        const int cv = min(sg.k.len - (b << 7), 128), npc = (cv + ps - 1) / ps;
-        int got = 1;
-        if (lane == 0) got = wait_bar(empty(st), ph ^ 1u, wc) && !(p.test_flags & 1u);
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-        if (!ok) break;
-        __syncwarp();
-        if (lane < 16) smem[L::kScales + st * 16 + lane] = scale;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(max(npc, 0) * ps) * 2u * D);
-        __syncwarp();
-        if (lane < 16 && 16 * i16 < cv && (16 * i16) % ps == 0)
-          tma_load_4d(base + L::kRing + (2 * st + (is_v ? 1 : 0)) * L::kKeys + 16 * i16 * D, is_v ? &tm_v : &tm_k, 0, sg.h,
-                      slot, page, full(st));
-        __syncwarp();
-        ++copies;
-        page = page_next;
-        slot = slot_next;
-        if (b + 1 < sg.b1) scale = scale_of(b + 1, page, slot);
-        if (b + 2 < sg.b1) locate(b + 2);
-      }
-    }
-    // No copy may be in flight when the CTA ends, whatever ended the loop.
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer_ns();
-      for (int n = max(0, copies - L::kStages); n < copies; ++n)
-        while (!mbar_try_wait(full(n % L::kStages), (n / L::kStages) & 1u))
-          if (globaltimer_ns() - t0 > p.timeout_ns) break;
-    }
-    return;
-  }
-
-  // ================================================================== the sums
-  const int gr = lane >> 2, t4 = lane & 3;
+  const int gr = lane >> 2, t4 = lane & 3, group = warp >> 3, part8 = warp & 7;
+  const int hg = p.hg, hh = part8 & (hg - 1), tb = part8 / hg, per_block = 8 / hg, keys = 128 / hg;
   const int grp = p.c.group, H = p.c.hkv * grp;
   constexpr int kSteps = D / 16;  // m16n8k16 products of a score tile, and tiles of Oᵀ
-  // Places in a warp's 16 rows of K and V.
-  uint32_t k_at[2][D / 64], v_at[D / 32];
+
+  // ---- the warp's blocks: number x is the tb-th 16 slots of unit u0 + group + kGroups·x.  16 of
+  // them are looked up at a time, a lane each, and the next 16 while these are copied.
+  struct Block {
+    long long k, v;        // offsets of its first row; −1: nothing to copy
+    uint32_t scales;       // of K, and of V << 8
+  };
+  auto look_up = [&](int x) -> Block {
+    Block r = {-1, -1, 0u};
+    const int u = u0 + group + L::kGroups * (x + lane);
+    if (u >= u1 || lane >= kLookUp) return r;
+    const Segment sg = segment_at<RowsPlan>(p, tab, u, u1);
+    const int j = sg.b0 * keys + 16 * tb;
+    if (j >= sg.k.len) return r;
+    const int blk = j / p.c.page_size, slot = j - blk * p.c.page_size, h = sg.h * hg + hh;
+    const int page = page_for_read(p.c, sg.s, blk);
+    r.k = page * p.c.k_st[0] + slot * p.c.k_st[1] + h * p.c.k_st[2];
+    r.v = page * p.c.v_st[0] + slot * p.c.v_st[1] + h * p.c.v_st[2];
+    const long long i = (static_cast<long long>(page) * p.c.hkv + h) * fp.f.per + (slot >> 4);
+    r.scales = fp.f.ks[i] | static_cast<uint32_t>(fp.f.vs[i]) << 8;
+    return r;
+  };
+  // The warp's places in shared memory: where this lane copies to (its row of the first 4 or 8,
+  // 16 bytes), and the rows and runs of the fragments that it reads.
+  const uint32_t ring = base + L::kRing + warp * L::kStages * 2 * L::kKeys;
+  constexpr int kRunsRow = D / 16, kRowsStep = 32 / kRunsRow, kSteps16 = 16 / kRowsStep;  // runs a row; rows a copy
+  const int my_row = lane / kRunsRow, my_run = lane % kRunsRow;
+  const uint32_t to[2] = {ring + run_at<D>(my_row, my_run), ring + run_at<D>(my_row + kRowsStep, my_run)};
+  uint32_t k_at[2][D / 64], v_at[2];
 #pragma unroll
   for (int hf = 0; hf < D / 64; ++hf) {
-    k_at[0][hf] = chunk_at<D>(16 * warp + key_of<D>(gr), 4 * hf + t4);
-    k_at[1][hf] = chunk_at<D>(16 * warp + 8 + key_of<D>(gr), 4 * hf + t4);
+    k_at[0][hf] = ring + run_at<D>(key_of<D>(gr), 4 * hf + t4);
+    k_at[1][hf] = ring + run_at<D>(8 + key_of<D>(gr), 4 * hf + t4);
   }
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    v_at[c] = L::kKeys + chunk_at<D>(16 * warp + (lane & 8) + key_of<D>(lane & 7), 2 * c + (lane >> 4));
+  for (int i = 0; i < 2; ++i)
+    v_at[i] = ring + L::kKeys + run_at<D>(key_of<D>(2 * t4 + i), D == 128 ? gr : gr >> 1) + (D == 128 ? 0 : 8 * (gr & 1));
+  uint16_t* const scales = reinterpret_cast<uint16_t*>(smem + L::kScales) + warp * L::kStages;
+  longlong2* const offsets = reinterpret_cast<longlong2*>(smem + L::kOffsets) + warp * kLookUp;
+  const uint8_t* const k_lane = fp.f.k + my_row * p.c.k_st[1] + 16 * my_run;
+  const uint8_t* const v_lane = fp.f.v + my_row * p.c.v_st[1] + 16 * my_run;
+  auto publish = [&](const Block& r) {
+    __syncwarp();
+    if (lane < kLookUp) offsets[lane] = make_longlong2(r.k, r.v);
+    __syncwarp();
+  };
+  auto copy = [&](int x, int st) {
+    const longlong2 off = offsets[x & (kLookUp - 1)];
+    if (off.x >= 0) {
+      const uint8_t *const k = k_lane + off.x, *const v = v_lane + off.y;
+      const uint32_t at = st * 2 * L::kKeys;
+#pragma unroll
+      for (int i = 0; i < kSteps16; ++i)
+        copy_async(to[i & 1] + at + (i >> 1) * 2 * kRowsStep * D, k + i * kRowsStep * p.c.k_st[1]);
+#pragma unroll
+      for (int i = 0; i < kSteps16; ++i)
+        copy_async(to[i & 1] + L::kKeys + at + (i >> 1) * 2 * kRowsStep * D, v + i * kRowsStep * p.c.v_st[1]);
+    }
+    copy_commit();
+  };
+  auto keep_scales = [&](const Block& r, int x, int st) {
+    if (lane == (x & (kLookUp - 1))) scales[st] = static_cast<uint16_t>(r.scales);
+  };
+  Block now = look_up(0);
+  publish(now);
+#pragma unroll 1
+  for (int x = 0; x < L::kStages; ++x) copy(x, x);
+#pragma unroll 1
+  for (int x = 0; x < L::kStages; ++x) keep_scales(now, x, x);
+  Block next = look_up(kLookUp);
 
-  int g = 0;
-  bool ok = true;
+  int x = 0, st = 0;  // the block at work and its place in the ring
   for (int u = u0; u < u1;) {
     const Segment sg = segment_at<RowsPlan>(p, tab, u, u1);
     const bool first_of_cta = u == u0;
     u += sg.b1 - sg.b0;
-    const int row0 = sg.m * p.rows, n_rows = min(sg.k.n * grp - row0, p.rows);
+    const int h = sg.h * hg + hh, row0 = sg.m * p.rows, n_rows = min(sg.k.n * grp - row0, p.rows);
     // ---- Q: the rows of this thread's fragments (row gr of each tile), as f16
     uint32_t qf[NT][kSteps][2];
     float mult[NT][2];  // of the scores in its columns (rows 2·t4 and 2·t4 + 1)
     auto q_row = [&](int r) {
       const int rr = row0 + min(r, n_rows - 1);
-      return fp.q + (sg.k.q0 + rr / grp) * fp.q_st[0] + (sg.h * grp + rr % grp) * fp.q_st[1];
+      return fp.q + (sg.k.q0 + rr / grp) * fp.q_st[0] + (h * grp + rr % grp) * fp.q_st[1];
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -281,133 +282,157 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1)
       mult[nt][0] = __shfl_sync(0xffffffffu, rest, 8 * t4);
       mult[nt][1] = __shfl_sync(0xffffffffu, rest, 8 * t4 + 4);
     }
-    float o[NT][kSteps][4], m_run[NT][2], l_run[NT][2];
+    // O, sums and references: pairs of columns (rows 2·t4 and 2·t4 + 1 of Q) side by side.
+    uint64_t o[NT][kSteps][2], l_run[NT];
+    float m_run[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][c][i] = 0.f;
-      m_run[nt][0] = m_run[nt][1] = -INFINITY;
-      l_run[nt][0] = l_run[nt][1] = 0.f;
+      for (int c = 0; c < kSteps; ++c) o[nt][c][0] = o[nt][c][1] = 0ull;
+      m_run[nt][0] = m_run[nt][1] = kNone;
+      l_run[nt] = 0ull;
     }
-    // Scores (log2 units; −inf where a row does not see a key) to P: a reference that is
-    // exceeded by more than kTau moves, and with it O and the sums.
-    auto weigh = [&](float(&s)[NT][4]) {
-      bool need = false;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mx[nt][i] = fmaxf(s[nt][i], s[nt][i + 2]);
-          need = need || mx[nt][i] > m_run[nt][i] + kTau || (m_run[nt][i] == -INFINITY && mx[nt][i] > -INFINITY);
-        }
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float m = mx[nt][i];
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            if (m > m_run[nt][i]) {
-              const float alpha = ex2_mufu(m_run[nt][i] - m);
-              m_run[nt][i] = m;
-              l_run[nt][i] *= alpha;
-#pragma unroll
-              for (int c = 0; c < kSteps; ++c) {
-                o[nt][c][i] *= alpha;
-                o[nt][c][i + 2] *= alpha;
-              }
-            }
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float m = m_run[nt][i & 1];
-          s[nt][i] = ex2_mufu(s[nt][i] - (m == -INFINITY ? 0.f : m - kShift));
-          l_run[nt][i & 1] += s[nt][i];
-        }
-    };
-
-    for (int b = sg.b0; b < sg.b1; ++b, ++g) {
-      const int st = g % L::kStages;
-      ok = ok && wait_bar(full(st), (g / L::kStages) & 1, wc);
-      ok = !__any_sync(0xffffffffu, !ok);
-      const int nv = min(sg.k.len - (b << 7) - 16 * warp, 16);  // keys of this warp
-      if (ok && nv > 0) {
-        const uint32_t tile = base + L::kRing + 2 * st * L::kKeys;
-        const float ka = power_of(scale_byte(smem[L::kScales + st * 16 + warp]));
-        const float vb = power_of(scale_byte(smem[L::kScales + st * 16 + 8 + warp]));
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-#pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          uint32_t lo[4], hi[4];
-          ld_shared_v4(tile + k_at[0][hf], lo);
-          ld_shared_v4(tile + k_at[1][hf], hi);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(lo[j]), e4m3x2_to_f16x2(hi[j]), e4m3x2_to_f16x2(lo[j] >> 16),
-                                   e4m3x2_to_f16x2(hi[j] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a, qf[nt][4 * hf + j][0], qf[nt][4 * hf + j][1]);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[nt][i] = s[nt][i] * mult[nt][i & 1] * ka;
-            if (nv < 16 && key_of<D>(gr) + (i & 2 ? 8 : 0) >= nv) s[nt][i] = -INFINITY;
-          }
-        weigh(s);
-        uint32_t pf[NT][2];
+    // Products s of the tile to P, 2^(s·f − reference + 7), 0 where `hidden`.  A reference
+    // that is exceeded by more than kTau moves, and with it O and the sums.
+    auto weigh = [&](float(&s)[NT][4], const float(&f)[NT][2], auto hidden) {
+      float e[NT][4], top = -INFINITY;
+      auto exponents = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          pf[nt][0] = transposed(pack_f16x2(s[nt][0], s[nt][1]));
-          pf[nt][1] = transposed(pack_f16x2(s[nt][2], s[nt][3]));
+          const uint64_t f2 = pack2(f[nt][0], f[nt][1]), r2 = pack2(kShift - m_run[nt][0], kShift - m_run[nt][1]);
+          unpack2(ffma2(pack2(s[nt][0], s[nt][1]), f2, r2), e[nt][0], e[nt][1]);
+          unpack2(ffma2(pack2(s[nt][2], s[nt][3]), f2, r2), e[nt][2], e[nt][3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (hidden(nt, i)) e[nt][i] = -INFINITY;
         }
-        // Codes behind the sequence's end: their P is 0, but a NaN would spread.
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        if (nv < 16) {
+      };
+      exponents();
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            keep[x] = (key_of<D>(2 * t4) + 8 * x < nv ? 0xffffu : 0u) |
-                      (key_of<D>(2 * t4 + 1) + 8 * x < nv ? 0xffff0000u : 0u);
-        }
+      for (int nt = 0; nt < NT; ++nt) top = fmaxf(top, fmaxf(fmaxf(e[nt][0], e[nt][1]), fmaxf(e[nt][2], e[nt][3])));
+      if (__any_sync(0xffffffffu, top > kShift + kTau)) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[4];
-          ldmatrix_x4_trans(tile + v_at[c], r);
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            // (key 2t, value 2g), (2t, 2g + 1), (2t + 1, 2g), (2t + 1, 2g + 1) → pairs of keys
-            const uint32_t w0 = __byte_perm(r[2 * y] & keep[0], 0u, 0x3120), w1 = __byte_perm(r[2 * y + 1] & keep[1], 0u, 0x3120);
-            const uint32_t a[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w0 >> 16), e4m3x2_to_f16x2(w1),
-                                   e4m3x2_to_f16x2(w1 >> 16)};
+          for (int i = 0; i < 2; ++i) {
+            float m = m_run[nt][i];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float pv[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(pv, a, pf[nt][0], pf[nt][1]);
+            for (int y = 0; y < 2; ++y)
+              if (!hidden(nt, i + 2 * y)) m = fmaxf(m, s[nt][i + 2 * y] * f[nt][i]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[nt][2 * c + y][i] = fmaf(pv[i], vb, o[nt][2 * c + y][i]);
-            }
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            alpha[i] = m == m_run[nt][i] ? 1.f : ex2_mufu(m_run[nt][i] - m);
+            m_run[nt][i] = m;
+          }
+          const uint64_t a2 = pack2(alpha[0], alpha[1]);
+          l_run[nt] = fmul2(l_run[nt], a2);
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) {
+            o[nt][c][0] = fmul2(o[nt][c][0], a2);
+            o[nt][c][1] = fmul2(o[nt][c][1], a2);
           }
         }
+        exponents();
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = ex2_mufu(e[nt][i]);
+        l_run[nt] = fadd2(fadd2(l_run[nt], pack2(s[nt][0], s[nt][1])), pack2(s[nt][2], s[nt][3]));
+      }
+    };
+    // One block of 16 keys, `nv` of them of the sequence (all, without MASK).
+    auto block = [&](int nv, auto mask_tag) {
+      constexpr bool MASK = decltype(mask_tag)::value;
+      const uint32_t at = st * 2 * L::kKeys, sc = scales[st];
+      uint32_t kw[D / 32][4];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) ld_shared_v4(k_at[i & 1][i >> 1] + at, kw[i]);
+      const float ka = power_of(scale_byte(sc & 0xFFu)), vb = power_of(scale_byte(sc >> 8));
+      // (two sums a tile: half the chain of products)
+      float s[NT][4], s2[NT][4], f[NT][2];
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t lo = kw[2 * hf][j], hi = kw[2 * hf + 1][j];
+          const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(lo >> 16),
+                                 e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma<true>(j & 1 ? s2[nt] : s[nt], a, qf[nt][4 * hf + j][0], qf[nt][4 * hf + j][1], hf > 0 || j > 1);
+        }
+      // Keys 2·t4, 2·t4 + 1 and both + 8, this lane's run of D / 8 values.
+      uint32_t w[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (D == 128) ld_shared_v4(v_at[i & 1] + at + (i >> 1) * 8 * D, w[i]);
+        else ld_shared_v2(v_at[i & 1] + at + (i >> 1) * 8 * D, w[i]);
+        // (codes behind the sequence's end: their P is 0, but a NaN would spread)
+        if (MASK && key_of<D>(2 * t4 + (i & 1)) + 4 * (i & 2) >= nv)
+#pragma unroll
+          for (int y = 0; y < D / 32; ++y) w[i][y] = 0u;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
+        f[nt][0] = mult[nt][0] * ka;
+        f[nt][1] = mult[nt][1] * ka;
+      }
+      weigh(s, f, [&](int, int i) { return MASK && key_of<D>(gr) + (i & 2 ? 8 : 0) >= nv; });
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        pf[nt][0] = transposed(pack_f16x2(s[nt][0], s[nt][1]));
+        pf[nt][1] = transposed(pack_f16x2(s[nt][2], s[nt][3]));
+      }
+      const uint64_t vb2 = pack2(vb, vb);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) {
+        // Values 2c and 2c + 1 of the run, in pairs of keys.
+        const uint32_t w0 = __byte_perm(w[0][c >> 1], w[1][c >> 1], c & 1 ? 0x7362 : 0x5140),
+                       w1 = __byte_perm(w[2][c >> 1], w[3][c >> 1], c & 1 ? 0x7362 : 0x5140);
+        const uint32_t a[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w0 >> 16), e4m3x2_to_f16x2(w1),
+                               e4m3x2_to_f16x2(w1 >> 16)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float pv[4];
+          mma<true>(pv, a, pf[nt][0], pf[nt][1], false);
+          o[nt][c][0] = ffma2(pack2(pv[0], pv[1]), vb2, o[nt][c][0]);
+          o[nt][c][1] = ffma2(pack2(pv[2], pv[3]), vb2, o[nt][c][1]);
+        }
+      }
+    };
+
+    for (;; ++x) {
+      // (units of the segment come in order: its last is u − 1)
+      const int unit = u0 + group + L::kGroups * x;
+      if (unit >= u) break;
+      copy_wait<L::kStages - 1>();
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(empty(st));
+      const int nv = sg.k.len - (sg.b1 - (u - unit)) * keys - 16 * tb;  // keys from the block's first on
+      if (nv >= 16) block(16, std::false_type{});
+      else if (nv > 0) block(nv, std::true_type{});
+      // The block's place is free: on with the one that is kStages ahead.
+      const int ahead = x + L::kStages;
+      if ((ahead & (kLookUp - 1)) == 0) {
+        now = next;
+        publish(now);
+        next = look_up(ahead + kLookUp);
+      }
+      copy(ahead, st);
+      __syncwarp();
+      keep_scales(now, ahead, st);
+      st = st + 1 == L::kStages ? 0 : st + 1;
     }
-    // ---- the new tokens' own keys, 16 a warp from the last on (whose cached keys are often none)
-    const int k0 = 16 * (L::kWarps - 1 - warp);
-    if (ok && sg.b1 == sg.k.db + 1 && k0 < sg.k.n) {
+    // ---- the new tokens' own keys, 16 at a time, from the head's last warp on (whose cached keys
+    // are often none)
+    const int sharers = per_block * L::kGroups;
+#pragma unroll 1
+    for (int k0 = 16 * (sharers - 1 - (tb + per_block * group)); sg.b1 == sg.k.db + 1 && k0 < sg.k.n;
+         k0 += 16 * sharers) {
       uint32_t mine = 0u;  // which of the 16 keys row `lane` of the tile sees
       {
         const int t = (row0 + min(lane, n_rows - 1)) / grp;
@@ -422,14 +447,10 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1)
             if (i == k0 >> 5) mine = (anc[i] >> (k0 & 16)) & 0xffffu;
         }
       }
-      const uint16_t* const kn = fp.kn + static_cast<long long>(sg.h) * fp.kn_st[1];
-      const uint16_t* const vn = fp.vn + static_cast<long long>(sg.h) * fp.vn_st[1];
+      const uint16_t* const kn = fp.kn + static_cast<long long>(h) * fp.kn_st[1];
+      const uint16_t* const vn = fp.vn + static_cast<long long>(h) * fp.vn_st[1];
       const int ja = k0 + gr, jb = ja + 8;
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+      float s[NT][4], f[NT][2];
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int it = 0; it < D / 32; ++it) {
@@ -440,105 +461,158 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 q = *reinterpret_cast<const uint4*>(q_row(8 * nt + gr) + c);
           const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
-          mma_bf16(s[nt], a0, q.x, q.y);
-          mma_bf16(s[nt], a1, q.z, q.w);
+          mma<false>(s[nt], a0, q.x, q.y, it > 0);
+          mma<false>(s[nt], a1, q.z, q.w, true);
         }
       }
+      uint32_t see[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t see[2] = {__shfl_sync(0xffffffffu, mine, 8 * nt + 2 * t4),
-                                 __shfl_sync(0xffffffffu, mine, 8 * nt + 2 * t4 + 1)};
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[nt][i] = (see[i & 1] >> (gr + (i & 2 ? 8 : 0))) & 1u ? s[nt][i] * p.scale_log2 : -INFINITY;
-      }
-      weigh(s);
+        for (int i = 0; i < 2; ++i) {
+          see[nt][i] = __shfl_sync(0xffffffffu, mine, 8 * nt + 2 * t4 + i) >> gr;
+          f[nt][i] = p.scale_log2;
+        }
+      weigh(s, f, [&](int nt, int i) { return ((see[nt][i & 1] >> (i & 2 ? 8 : 0)) & 1u) == 0u; });
       uint32_t pf[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         pf[nt][0] = transposed(pack_bf16x2(s[nt][0], s[nt][1]));
         pf[nt][1] = transposed(pack_bf16x2(s[nt][2], s[nt][3]));
       }
+      uint4 y[4][D / 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = k0 + 2 * t4 + (i & 1) + 4 * (i & 2);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+          y[i][e] = j < sg.k.n ? *reinterpret_cast<const uint4*>(vn + (sg.k.q0 + j) * fp.vn_st[0] + D / 8 * gr + 8 * e) : zero;
+      }
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
-        uint32_t w[4];
+        auto word = [&](int i) {
+          const uint4& z = y[i][c >> 2];
+          return (c & 3) == 0 ? z.x : (c & 3) == 1 ? z.y : (c & 3) == 2 ? z.z : z.w;
+        };
+        const uint32_t a[4] = {__byte_perm(word(0), word(1), 0x5410), __byte_perm(word(0), word(1), 0x7632),
+                               __byte_perm(word(2), word(3), 0x5410), __byte_perm(word(2), word(3), 0x7632)};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = k0 + 2 * t4 + (x & 1) + (x & 2 ? 8 : 0);
-          w[x] = j < sg.k.n
-                     ? *reinterpret_cast<const uint32_t*>(vn + (sg.k.q0 + j) * fp.vn_st[0] + 16 * c + 2 * gr)
-                     : 0u;
+        for (int nt = 0; nt < NT; ++nt) {
+          float z[4];
+          unpack2(o[nt][c][0], z[0], z[1]);
+          unpack2(o[nt][c][1], z[2], z[3]);
+          mma<false>(z, a, pf[nt][0], pf[nt][1], true);
+          o[nt][c][0] = pack2(z[0], z[1]);
+          o[nt][c][1] = pack2(z[2], z[3]);
         }
-        const uint32_t a[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                               __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][c], a, pf[nt][0], pf[nt][1]);
       }
     }
-    // ---- the warps' sums meet
+    // ---- the warps of a head meet: half of them hand their maxima, sums and O to the other
+    // half, until one is left
+    // `pair`: by a barrier of the two warps that share the slot, otherwise by one of all warps,
+    // since the next level's pairs are others.
+    auto meet = [&](int slot, bool gives, bool takes, auto pair) {
+      auto both = [&]() {
+        if constexpr (decltype(pair)::value) asm volatile("bar.sync %0, 64;" ::"r"(1 + slot) : "memory");
+        else asm volatile("bar.sync 9, %0;" ::"n"(32 * L::kWarps) : "memory");
+      };
+      float4* const ml = reinterpret_cast<float4*>(smem + L::kMl) + slot * NT * 32 + lane;
+      ulonglong2* const half = reinterpret_cast<ulonglong2*>(smem + L::kMerge + slot * L::kMergeWarp) + lane;
+      uint64_t mine[NT], theirs[NT];
+      if (gives)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float l0, l1;
+          unpack2(l_run[nt], l0, l1);
+          ml[nt * 32] = make_float4(m_run[nt][0], m_run[nt][1], l0, l1);
+        }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float l = l_run[nt][i];
+      for (int x = 0; x < 2; ++x) {
+        if (gives)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-        if (gr == 0)
-          reinterpret_cast<float2*>(smem + L::kMl)[warp * 8 * NT + 8 * nt + 2 * t4 + i] =
-              make_float2(m_run[nt][i] == -INFINITY ? -INFINITY : m_run[nt][i] - kShift, l);
+          for (int i = 0; i < NT * kSteps / 2; ++i) {
+            const uint64_t(&y)[2] = o[i / (kSteps / 2)][x * (kSteps / 2) + i % (kSteps / 2)];
+            half[i * 32] = make_ulonglong2(y[0], y[1]);
+          }
+        both();
+        if (takes) {
+          if (x == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float4 y = ml[nt * 32];
+              const float their_m[2] = {y.x, y.y};
+              float a[2], b[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float& m = m_run[nt][i];
+                const float top = fmaxf(m, their_m[i]);
+                // (a warp that saw nothing has sum and O of 0, or NaN that stays)
+                a[i] = m == top ? 1.f : ex2_mufu(m - top);
+                b[i] = their_m[i] == top ? 1.f : ex2_mufu(their_m[i] - top);
+                m = top;
+              }
+              mine[nt] = pack2(a[0], a[1]);
+              theirs[nt] = pack2(b[0], b[1]);
+              l_run[nt] = ffma2(pack2(y.z, y.w), theirs[nt], fmul2(l_run[nt], mine[nt]));
+            }
+#pragma unroll
+          for (int i = 0; i < NT * kSteps / 2; ++i) {
+            const ulonglong2 y = half[i * 32];
+            const int nt = i / (kSteps / 2);
+            uint64_t(&z)[2] = o[nt][x * (kSteps / 2) + i % (kSteps / 2)];
+            z[0] = ffma2(y.x, theirs[nt], fmul2(z[0], mine[nt]));
+            z[1] = ffma2(y.y, theirs[nt], fmul2(z[1], mine[nt]));
+          }
+        }
+        both();
       }
+    };
+    if (L::kGroups > 1) {
+      meet(part8, group == 1, group == 0, std::true_type{});  // (warps part8 and part8 + 8)
+      if (per_block > 1) asm volatile("bar.sync 9, %0;" ::"n"(32 * L::kWarps) : "memory");
+    }
+    for (int w = per_block / 2; w > 0; w >>= 1)
+      meet(hh + hg * (tb & (w - 1)), group == 0 && tb >= w && tb < 2 * w, group == 0 && tb < w, std::false_type{});
+    if (group != 0 || tb != 0) continue;
+    // ---- the head's rows, by its one warp
     const bool whole = sg.b0 == 0 && sg.b1 == sg.k.db + 1;
     const int slot = 2 * cta + (first_of_cta ? 0 : 1);
-    float* const merge = reinterpret_cast<float*>(smem + L::kMerge);
-    constexpr int kPer = D / 32;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (8 * nt >= n_rows) break;  // (the same for all warps)
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
+      for (int x = 4; x < 32; x <<= 1) l_run[nt] = fadd2(l_run[nt], __shfl_xor_sync(0xffffffffu, l_run[nt], x));
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * t4 + i) * L::kPitch + 16 * c + 2 * gr) =
-              make_float2(o[nt][c][i], o[nt][c][i + 2]);
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * L::kWarps) : "memory");
-      // Warp w joins row w: its lanes kPer values each.
-      const int r = 8 * nt + warp;
-      if (r < n_rows && ok) {
-        const float2* const ml = reinterpret_cast<const float2*>(smem + L::kMl) + r;
-        float mx = -INFINITY, sum = 0.f, acc[kPer] = {};
-#pragma unroll
-        for (int w = 0; w < L::kWarps; ++w) mx = fmaxf(mx, ml[w * 8 * NT].x);
-#pragma unroll
-        for (int w = 0; w < L::kWarps; ++w) {
-          const float2 x = ml[w * 8 * NT];
-          const float f = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : ex2_mufu(x.x - mx);
-          sum += f * x.y;
-          const float* const src = merge + (w * 8 + warp) * L::kPitch + lane * kPer;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) acc[i] += f * src[i];
-        }
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * nt + 2 * t4 + i;
+        if (r >= n_rows) continue;
+        auto of = [&](uint64_t two) {  // this row's of a pair
+          float a, b;
+          unpack2(two, a, b);
+          return i ? b : a;
+        };
+        const float l = of(l_run[nt]), m = l == 0.f ? -INFINITY : m_run[nt][i] - kShift;
         if (whole) {
-          const int rr = row0 + r, hq = sg.h * grp + rr % grp;
+          const int rr = row0 + r, hq = h * grp + rr % grp;
           const long long token = sg.k.q0 + rr / grp;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          uint16_t* const dst = p.o + (token * H + hq) * D + lane * kPer;
-          if constexpr (kPer == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-          else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-          if (lane == 0)
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint4* const dst = reinterpret_cast<uint4*>(p.o + (token * H + hq) * D + D / 8 * gr);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) {
+            auto two = [&](int c) { return pack_bf16x2(of(o[nt][4 * e + c][0]) * inv, of(o[nt][4 * e + c][1]) * inv); };
+            dst[e] = make_uint4(two(0), two(1), two(2), two(3));
+          }
+          if (gr == 0)
             p.lse[static_cast<long long>(hq) * p.c.total + token] =
-                sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.69314718055994531f;
+                l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
         } else {
-          const long long part = static_cast<long long>(slot) * p.rows + r;
-          float* const dst = p.ws_o + part * D + lane * kPer;
-          if constexpr (kPer == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
-          if (lane == 0) p.ws_ml[part] = make_float2(mx, sum);
+          const long long part = (static_cast<long long>(slot) * hg + hh) * p.rows + r;
+          float4* const dst = reinterpret_cast<float4*>(p.ws_o + part * D + D / 8 * gr);
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e)
+            dst[e] = make_float4(of(o[nt][2 * e][0]), of(o[nt][2 * e][1]), of(o[nt][2 * e + 1][0]), of(o[nt][2 * e + 1][1]));
+          if (gr == 0) p.ws_ml[part] = make_float2(m, l);
         }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * L::kWarps) : "memory");
     }
   }
 }
@@ -556,7 +630,7 @@ cudaError_t launch(const CacheAttnFp8Launch& a) {
     if (e != cudaSuccess) return e;
     configured[a.device] = true;
   }
-  cache_attn_fp8_kernel<D, NT><<<a.grid, L::kThreads, smem, a.stream>>>(a.k, a.v, p);
+  cache_attn_fp8_kernel<D, NT><<<a.grid, L::kThreads, smem, a.stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<D, RowsPlan>(p.a, a.grid, a.stream);

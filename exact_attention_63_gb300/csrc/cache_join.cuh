@@ -17,18 +17,20 @@ constexpr int kWideRows = 64;  // parts of more rows lie chunk by chunk, [D/4][r
 // WAY = kJoinFew: a block takes one row, its eight warps deal out the parts (few rows;
 // one long sequence leaves a part on every CTA).  kJoinRows: a block takes 32 rows, a
 // warp four at once.  kJoinWide: parts that lie chunk by chunk; a block takes 32 rows,
-// a lane a row, a warp a quarter of its values.
-enum { kJoinFew, kJoinRows, kJoinWide };
+// a lane a row, a warp a quarter of its values.  kJoinEight: a block takes 8 rows, a warp
+// one with all of its parts (tiles of 8 or 16 rows, of which half and more may be empty).
+enum { kJoinFew, kJoinRows, kJoinWide, kJoinEight };
 
 template <int D, int WAY, class Plan>
 __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max) {
-  constexpr int kPer = D / 32, SPLIT = 8;
+  constexpr int kPer = D / 32, SPLIT = WAY == kJoinEight ? 1 : 8;
   __shared__ float s_acc[WAY == kJoinFew ? SPLIT : 1][D];
   __shared__ float2 s_ml[SPLIT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned int chunks = WAY == kJoinFew ? p.rows : (p.rows + 31) / 32;
+  constexpr int kRows = WAY == kJoinFew ? 1 : WAY == kJoinEight ? 8 : 32;  // of a block
+  const unsigned int chunks = (p.rows + kRows - 1) / kRows;
   unsigned int x = blockIdx.x;
-  const int row0 = static_cast<int>(x % chunks) * (WAY == kJoinFew ? 1 : 32);
+  const int row0 = static_cast<int>(x % chunks) * kRows;
   x /= chunks;
   const int m = static_cast<int>(x % mt_max);
   x /= mt_max;
@@ -41,13 +43,15 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   if (row0 >= n_rows) return;
   const int units = p.ws_table[p.c.n_seq], nb = k.db + 1;
   grid = min(grid, units);
-  const int ua = p.ws_table[s] + (h * row_tiles(p, k.n) + m) * nb;
+  const int ua = p.ws_table[s] + (h / p.hg * row_tiles(p, k.n) + m) * nb;
   auto cta_of = [&](int u) { return static_cast<int>(((u + 1ll) * grid - 1) / units); };
   const int c0 = cta_of(ua), c1 = cta_of(ua + nb - 1);
   if (c0 == c1) return;  // one CTA did it all and has written the rows
   // Every CTA's part but the first's is the first of its range.
   const int slot0 = 2 * c0 + (range_start(units, c0, grid) >= ua ? 0 : 1);
-  auto part_of = [&](int c, int r) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * p.rows + r; };
+  const int in_run = h % p.hg;
+  auto slot_of = [&](int c) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * p.hg + in_run; };
+  auto part_of = [&](int c, int r) { return slot_of(c) * p.rows + r; };
 
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
   auto load = [&](int c, int r) { return *reinterpret_cast<const Vec*>(p.ws_o + part_of(c, r) * D + lane * kPer); };
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
       const float w = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
       sum += w * ml.y;
       const float4* src = reinterpret_cast<const float4*>(p.ws_o) +
-                          (static_cast<long long>(c == c0 ? slot0 : 2 * c) * (D / 4) + first) * p.rows + r;
+                          (slot_of(c) * (D / 4) + first) * p.rows + r;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const float4 y = src[static_cast<long long>(i) * p.rows];
@@ -142,12 +146,13 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
       if (r0 + j < n_rows) finish(r0 + j, m_j, s_j, acc[j], lane == 8 * j);
     }
   } else {
-    const int r = row0;
+    const int r = WAY == kJoinEight ? row0 + warp : row0, mine = WAY == kJoinEight ? 0 : warp;
+    if (r >= n_rows) return;
     float mx = -INFINITY, sum = 0.f, acc[kPer] = {};
-    for (int c = c0 + warp + lane * SPLIT; c <= c1; c += 32 * SPLIT) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
+    for (int c = c0 + mine + lane * SPLIT; c <= c1; c += 32 * SPLIT) mx = fmaxf(mx, p.ws_ml[part_of(c, r)].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    for (int cb = c0 + warp; cb <= c1; cb += 32 * SPLIT) {
+    for (int cb = c0 + mine; cb <= c1; cb += 32 * SPLIT) {
       const int c = cb + lane * SPLIT;
       float w = 0.f;
       if (c <= c1) {
@@ -169,24 +174,26 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (WAY == kJoinFew) {  // the warps' sums
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
-    if (lane == 0) s_ml[warp] = make_float2(mx, sum);
-    __syncthreads();
-    if (warp != 0) return;
-    mx = -INFINITY;
+      for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
+      if (lane == 0) s_ml[warp] = make_float2(mx, sum);
+      __syncthreads();
+      if (warp != 0) return;
+      mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < SPLIT; ++w) mx = fmaxf(mx, s_ml[w].x);
-    sum = 0.f;
+      for (int w = 0; w < SPLIT; ++w) mx = fmaxf(mx, s_ml[w].x);
+      sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+      for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
 #pragma unroll
-    for (int w = 0; w < SPLIT; ++w) {
-      const float2 ml = s_ml[w];
-      const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
-      sum += f * ml.y;
+      for (int w = 0; w < SPLIT; ++w) {
+        const float2 ml = s_ml[w];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mx);
+        sum += f * ml.y;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += f * s_acc[w][lane * kPer + i];
+        for (int i = 0; i < kPer; ++i) acc[i] += f * s_acc[w][lane * kPer + i];
+      }
     }
     finish(r, mx, sum, acc, lane == 0);
   }
@@ -202,8 +209,9 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   // call, so and otherwise: 8 tiles of 48 rows in 152 parts 21 and 34 us at d = 128; 64
   // tiles of 4 rows 19 and 23 us at d = 64, 23 and 24 us at 128; 256 tiles of 4 rows 57
   // and 52 us at 128; 32 tiles of 32 rows 22 and 20 us at 128, 16 and 20 us at 64).
-  const bool few = !wide && (tiles * D <= 8ll * grid || tiles * p.rows * D <= 128ll * grid);
-  const long long blocks = tiles * (few ? p.rows : (p.rows + 31) / 32);
+  const bool few = !wide && (tiles * D <= 8ll * p.hg * grid || tiles * p.rows * D <= 128ll * grid);
+  const bool eight = Plan::kEight && !few && p.rows <= 16;
+  const long long blocks = tiles * (few ? p.rows : eight ? (p.rows + 7) / 8 : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.
   cudaLaunchAttribute attr;
@@ -216,6 +224,7 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide, Plan>, p, grid, mt_max);
+  if (eight) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinEight, Plan>, p, grid, mt_max);
   return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew, Plan>, p, grid, mt_max)
              : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows, Plan>, p, grid, mt_max);
 }

@@ -55,6 +55,7 @@ struct CacheAttnParams {
   float2* ws_ml;         // [2 * grid, rows] running maximum (log2) and sum of a part
   float* ws_o;           // [2 * grid, rows, d] its unnormalised output
   int rows;              // row pitch of the parts
+  int hg;                // key heads that a CTA works on at a time
   int nt;                // tokens of a row tile: nt * group <= 128 rows
   int ntt;               // tokens of a CTA's row tiles
   int piece;             // key rows of one copy: the largest power of two in page_size, at most 64
@@ -110,7 +111,7 @@ struct Fp8Pages {
 };
 
 struct CacheAttnFp8Launch {
-  CUtensorMap k, v;      // box (d, 1, piece, 1) of bytes
+  CUtensorMap k, v;      // (d, slot, head, page), box (d, piece, hg, 1) of bytes
   CacheAttnParams p;
   Fp8Pages f;
   const uint16_t* q;

@@ -28,6 +28,7 @@ __device__ __forceinline__ KeyPlan key_plan(const CacheAttnParams& p, int s) {
   return k;
 }
 struct BlockPlan {
+  static constexpr bool kEight = false;  // (ways of the join that its tiles use)
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
 };
 // Row tiles that the (token, head of the group) rows of n new tokens make.
@@ -38,14 +39,15 @@ __host__ __device__ __forceinline__ int row_tiles(const CacheAttnParams& p, int 
 template <class Plan>
 __device__ __forceinline__ int units_of(const CacheAttnParams& p, int s) {
   const KeyPlan k = Plan::of(p, s);
-  return k.n == 0 ? 0 : p.c.hkv * row_tiles(p, k.n) * (k.db + 1);
+  return k.n == 0 ? 0 : p.c.hkv / p.hg * row_tiles(p, k.n) * (k.db + 1);
 }
 
 __device__ __forceinline__ int range_start(int units, int cta, int grid) {
   return static_cast<int>(static_cast<long long>(units) * cta / grid);
 }
 
-// A CTA's share of one (sequence, key head, row tile): blocks [b0, b1).
+// A CTA's share of one (sequence, run of hg key heads, row tile): blocks [b0, b1).  h: the
+// number of the run.
 struct Segment {
   int s, h, m, b0, b1;
   KeyPlan k;
