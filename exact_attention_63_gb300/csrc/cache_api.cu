@@ -186,7 +186,8 @@ Tiles fp8_tiles(int group, int max_new, int d, int hg) {
   Tiles t;
   t.nt = t.ntt = 0;
   t.per_cta = 1;
-  t.rows = static_cast<long long>(group) * max_new <= 8 ? 8 : 16;
+  const long long all = static_cast<long long>(group) * max_new;
+  t.rows = all <= 8 ? 8 : all <= 16 ? 16 : 32;
   t.max_ctas = attn::kCacheMaxCtas / 2;
   const size_t ends = 2ull * t.max_ctas * t.rows * hg;
   t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));

@@ -133,10 +133,12 @@ struct FL {
   static constexpr int kWarps = 8 * kGroups;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kKeys = 16u * D;             // bytes of a block's K or V, of one head
-  static constexpr int kStages = (D == 128 ? 3 : 6) * (2 / kGroups);  // blocks of a warp: one at work, the others on their way
+  static constexpr bool kQShared = NT > 2;               // Q's fragments do not fit beside O
+  static constexpr int kStages = (D == 128 ? 3 : 6) * (NT == 2 ? 2 : 1);  // blocks of a warp: one at work, the others on their way
   static constexpr uint32_t kRing = 0;                   // [warp][stage][K, V][16 rows]
   static constexpr uint32_t kMergeWarp = NT * D / 32 * 32 * 16;  // half of a warp's O, as its lanes hold it
-  static constexpr uint32_t kMerge = kWarps * kStages * 2 * kKeys;
+  static constexpr uint32_t kQ = kWarps * kStages * 2 * kKeys;   // [warp][two products][tile][lane]
+  static constexpr uint32_t kMerge = kQ + (kQShared ? kWarps * NT * D / 16 * 256 : 0);
   static constexpr uint32_t kMl = kMerge + 4 * kGroups * kMergeWarp;  // [8][NT][2][lane] maximum and sum
   static constexpr uint32_t kOffsets = kMl + 8 * NT * 2 * 32 * 8;    // [warp][kLookUp] of K and V, bytes
   static constexpr uint32_t kScales = kOffsets + kWarps * kLookUp * 16;  // [warp][stage] bytes of K and V
@@ -249,7 +251,8 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
     u += sg.b1 - sg.b0;
     const int h = sg.h * hg + hh, row0 = sg.m * p.rows, n_rows = min(sg.k.n * grp - row0, p.rows);
     // ---- Q: the rows of this thread's fragments (row gr of each tile), as f16
-    uint32_t qf[NT][kSteps][2];
+    uint32_t qf[L::kQShared ? 1 : NT][kSteps][2];
+    uint4* const q_own = reinterpret_cast<uint4*>(smem + L::kQ) + warp * (NT * kSteps / 2) * 32 + lane;
     float mult[NT][2];  // of the scores in its columns (rows 2·t4 and 2·t4 + 1)
     auto q_row = [&](int r) {
       const int rr = row0 + min(r, n_rows - 1);
@@ -275,9 +278,20 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          qf[nt][4 * hf + i / 2][i & 1] =
-              pack_f16x2(__uint_as_float(w[hf][i] << 16) * f, __uint_as_float(w[hf][i] & 0xFFFF0000u) * f);
+        for (int j = 0; j < 2; ++j) {  // two products
+          uint32_t two[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = w[hf][4 * j + i];
+            two[i] = pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+          }
+          if constexpr (L::kQShared) {
+            q_own[((2 * hf + j) * NT + nt) * 32] = make_uint4(two[0], two[1], two[2], two[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[nt][4 * hf + 2 * j + i / 2][i & 1] = two[i];
+          }
+        }
       const float rest = up == 127 ? 0.5f * inv : inv;  // (2^−127 is no normal number)
       mult[nt][0] = __shfl_sync(0xffffffffu, rest, 8 * t4);
       mult[nt][1] = __shfl_sync(0xffffffffu, rest, 8 * t4 + 4);
@@ -351,17 +365,28 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
       for (int i = 0; i < D / 32; ++i) ld_shared_v4(k_at[i & 1][i >> 1] + at, kw[i]);
       const float ka = power_of(scale_byte(sc & 0xFFu)), vb = power_of(scale_byte(sc >> 8));
       // (two sums a tile: half the chain of products)
-      float s[NT][4], s2[NT][4], f[NT][2];
+      float s[NT][4], s2[L::kQShared ? 1 : NT][4], f[NT][2];
 #pragma unroll
       for (int hf = 0; hf < D / 64; ++hf)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = kw[2 * hf][j], hi = kw[2 * hf + 1][j];
-          const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(lo >> 16),
-                                 e4m3x2_to_f16x2(hi >> 16)};
+        for (int j2 = 0; j2 < 2; ++j2) {
+          uint4 qq[L::kQShared ? NT : 1];
+          if constexpr (L::kQShared)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma<true>(j & 1 ? s2[nt] : s[nt], a, qf[nt][4 * hf + j][0], qf[nt][4 * hf + j][1], hf > 0 || j > 1);
+            for (int nt = 0; nt < NT; ++nt) qq[nt] = q_own[((2 * hf + j2) * NT + nt) * 32];
+#pragma unroll
+          for (int j = 2 * j2; j < 2 * j2 + 2; ++j) {
+            const uint32_t lo = kw[2 * hf][j], hi = kw[2 * hf + 1][j];
+            const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(lo >> 16),
+                                   e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (L::kQShared)
+                mma<true>(s[nt], a, j & 1 ? qq[nt].z : qq[nt].x, j & 1 ? qq[nt].w : qq[nt].y, hf > 0 || j > 0);
+              else
+                mma<true>(j & 1 ? s2[nt] : s[nt], a, qf[nt][4 * hf + j][0], qf[nt][4 * hf + j][1], hf > 0 || j > 1);
+            }
+          }
         }
       // Keys 2·t4, 2·t4 + 1 and both + 8, this lane's run of D / 8 values.
       uint32_t w[4][D / 32];
@@ -377,7 +402,8 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
+        for (int i = 0; i < 4; ++i)
+          if constexpr (!L::kQShared) s[nt][i] += s2[nt][i];
         f[nt][0] = mult[nt][0] * ka;
         f[nt][1] = mult[nt][1] * ka;
       }
@@ -639,8 +665,8 @@ cudaError_t launch(const CacheAttnFp8Launch& a) {
 }  // namespace
 
 cudaError_t launch_cache_attn_fp8(const CacheAttnFp8Launch& a) {
-  if (a.p.c.d == 64) return a.p.rows > 8 ? launch<64, 2>(a) : launch<64, 1>(a);
-  return a.p.rows > 8 ? launch<128, 2>(a) : launch<128, 1>(a);
+  if (a.p.c.d == 64) return a.p.rows > 16 ? launch<64, 4>(a) : a.p.rows > 8 ? launch<64, 2>(a) : launch<64, 1>(a);
+  return a.p.rows > 16 ? launch<128, 4>(a) : a.p.rows > 8 ? launch<128, 2>(a) : launch<128, 1>(a);
 }
 
 }  // namespace attn
