@@ -29,7 +29,8 @@ LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["attn_api.cu", "attn_static.cu", "attn_fwd_d64.cu", "attn_fwd_d64_causal.cu", "attn_fwd_d128.cu",
            "attn_fwd_d128_causal.cu", "attn_bwd.cu", "attn_fwd_fp8.cu", "cache_api.cu", "cache_attn.cu", "cache_weights.cu",
-           "cache_evict.cu", "cache_fp8.cu", "cache_attn_fp8.cu", "cache_pages.cu", "rotary.cu"]
+           "cache_evict.cu", "cache_fp8.cu", "cache_attn_fp8.cu",
+           "cache_attn_fp8_wide.cu", "cache_pages.cu", "rotary.cu"]
 BIND_SOURCE = "cache_bind.cpp"
 BIND_PATH = os.path.join(PKG, "_cache_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -256,10 +256,8 @@ int usable_device(int* dev, unsigned int** status, int* sms) {
   return ATTN_OK;
 }
 
-namespace {
-int encode_4d(CUtensorMap* m, CUtensorMapDataType type, int bytes, CUtensorMapSwizzle swizzle,
-              CUtensorMapL2promotion promotion, const void* ptr, const long long dims[4], const long long strides[3],
-              const int box[4]) {
+int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
+                   const int box[4]) {
   auto enc = get_encode_fn();
   if (enc == nullptr) {
     std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled unavailable");
@@ -271,31 +269,17 @@ int encode_4d(CUtensorMap* m, CUtensorMapDataType type, int bytes, CUtensorMapSw
   for (int i = 0; i < 4; ++i) {
     gd[i] = static_cast<cuuint64_t>(dims[i]);
     bx[i] = static_cast<cuuint32_t>(box[i]);
-    if (i < 3) gs[i] = static_cast<cuuint64_t>(strides[i]) * bytes;
+    if (i < 3) gs[i] = static_cast<cuuint64_t>(strides[i]) * 2;
   }
-  const CUresult r = enc(m, type, 4, const_cast<void*>(ptr), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                         promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gd, gs, bx, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     std::snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (CUresult %d)",
                   static_cast<int>(r));
     return ATTN_ERR_LAUNCH;
   }
   return ATTN_OK;
-}
-}  // namespace
-
-int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
-                   const int box[4]) {
-  return encode_4d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   ptr, dims, strides, box);
-}
-
-int encode_u8_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3], const int box[4]) {
-  // Rows of 128 (64) bytes whose neighbours are other heads': a wider fetch into L2 reads
-  // what somebody else wants much later.
-  const bool wide = box[0] == 128;
-  return encode_4d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B, ptr, dims, strides, box);
 }
 
 namespace {

@@ -52,10 +52,6 @@ int usable_device(int* dev, unsigned int** status, int* sms);
 int encode_bf16_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3],
                    const int box[4]);
 
-// The same over bytes; boxes whose rows are 128 bytes get the 128-byte swizzle, others
-// the 64-byte one.
-int encode_u8_4d(CUtensorMap* m, const void* ptr, const long long dims[4], const long long strides[3], const int box[4]);
-
 // FP8 (E4M3) inputs, d = 128 (attn_fwd_fp8.cu).
 cudaError_t launch_fwd_fp8(const LaunchArgs& a, bool causal);
 

@@ -172,29 +172,44 @@ int check_fp8(const attn_cache* a, const void* k_scales, const void* v_scales, C
   return ATTN_OK;
 }
 
-// Pages as (d, slot, head, page): a copy of several heads lies head by head.
-int encode_codes(CUtensorMap* m, const void* ptr, const CacheParams& c, const long long st[3], int piece, int hg) {
-  const long long dims[4] = {c.d, c.page_size, c.hkv, c.n_pages}, strides[3] = {st[1], st[2], st[0]};
-  const int box[4] = {c.d, piece, hg, 1};
-  return attn::encode_u8_4d(m, ptr, dims, strides, box);
-}
-
-// The 8-bit cache's attention: rows of a tile, key heads that a CTA works on at a time, and
-// the workspace as above.  Any number of rows and heads up to the largest may be asked for,
-// so `most` counts full tiles of eight heads.
-Tiles fp8_tiles(int group, int max_new, int d, int hg) {
-  Tiles t;
-  t.nt = t.ntt = 0;
-  t.per_cta = 1;
-  const long long all = static_cast<long long>(group) * max_new;
-  t.rows = all <= 8 ? 8 : all <= 16 ? 16 : 32;
-  t.max_ctas = attn::kCacheMaxCtas / 2;
-  const size_t ends = 2ull * t.max_ctas * t.rows * hg;
+// The 8-bit cache's attention: the kernel for many rows or few, rows of a tile, key heads that
+// a CTA works on at a time, and the workspace as above.  `most` is what any number of
+// tokens up to max_new needs, of any number of sequences.
+// More rows go to the converting kernel: one token tile of 64 rows, 64 sequences of up to
+// 8191 at d = 128, takes 287 us there and 396 in two tiles here; 32 rows 278 and 223.
+constexpr int kFp8FewRows = 32;
+struct Fp8Tiles {
+  bool wide;
+  int rows, hg, nt, max_ctas;
+  size_t ml, o, bytes;
+};
+Fp8Tiles fp8_tiles_of(int rows, int hg, int max_ctas, int d) {
+  Fp8Tiles t = {false, rows, hg, 0, max_ctas, 0, 0, 0};
+  const size_t ends = 2ull * max_ctas * rows * hg;
   t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
   t.o = t.ml + up256(ends * sizeof(float2));
   t.bytes = t.o + ends * d * sizeof(float);
-  t.most = t.bytes;
   return t;
+}
+Fp8Tiles fp8_tiles(int group, int max_new, int d, int hg) {
+  const long long all = static_cast<long long>(group) * max_new;
+  if (all <= kFp8FewRows) return fp8_tiles_of(all <= 8 ? 8 : all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
+  // As many tiles as 128 rows make, of about as many tokens each.
+  const int most = tile_tokens(group, max_new), tiles = (max_new + most - 1) / most, nt = (max_new + tiles - 1) / tiles;
+  Fp8Tiles t = fp8_tiles_of(nt * group, 1, attn::kCacheMaxCtas, d);
+  t.wide = true;
+  t.nt = nt;
+  return t;
+}
+size_t fp8_workspace(int group, int max_new, int d, int hg) {
+  const long long all = static_cast<long long>(group) * max_new;
+  size_t most = 0;
+  auto count = [&](const Fp8Tiles& t) { most = t.bytes > most ? t.bytes : most; };
+  count(fp8_tiles_of(8, hg, attn::kCacheMaxCtas / 2, d));
+  if (all > 8) count(fp8_tiles_of(16, hg, attn::kCacheMaxCtas / 2, d));
+  if (all > 16) count(fp8_tiles_of(32, hg, attn::kCacheMaxCtas / 2, d));
+  if (all > kFp8FewRows) count(fp8_tiles_of(tile_tokens(group, max_new) * group, 1, attn::kCacheMaxCtas, d));
+  return most;
 }
 
 // Key heads of a run: as many as a CTA's eight warps hold, where the heads allow it; of one
@@ -387,7 +402,7 @@ size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen
   if (H < 1 || num_kv_heads < 1 || H % num_kv_heads != 0 || H / num_kv_heads > 128 || max_seqlen < 1 ||
       max_seqlen > ATTN_CACHE_MAX_NEW || (d != 64 && d != 128))
     return 0;
-  return fp8_tiles(H / num_kv_heads, max_seqlen, d, heads_at_once(num_kv_heads, 2)).most;
+  return fp8_workspace(H / num_kv_heads, max_seqlen, d, heads_at_once(num_kv_heads, 2));
 }
 
 int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
@@ -402,7 +417,7 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   if (x->k == nullptr || x->v == nullptr) return ATTN_ERR_NULL;
   if (x->max_seqlen > ATTN_CACHE_MAX_NEW) return ATTN_ERR_SHAPE;
   const int hg = heads_at_once(c.hkv, c.n_seq);
-  const Tiles w = fp8_tiles(c.group, c.max_new, c.d, hg);
+  const Fp8Tiles w = fp8_tiles(c.group, c.max_new, c.d, hg);
   const long long tiles = (static_cast<long long>(c.group) * c.max_new + w.rows - 1) / w.rows;
   // Units and rows of the two kernels' grids.
   if (tiles * c.n_seq * c.hkv > kMaxInt / (c.cap / 128 + 3) || tiles * c.n_seq * c.hkv * w.rows > kMaxInt ||
@@ -432,15 +447,17 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   a.p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
   a.p.rows = w.rows;
-  const int low = c.page_size & -c.page_size;
-  a.p.hg = hg;
-  a.p.piece = low < 128 / hg ? low : 128 / hg;
+  a.p.hg = w.hg;
+  a.p.nt = a.p.ntt = w.nt;
+  a.p.piece = attn::kFp8Block;
   a.p.scale_log2 = scale * 1.4426950408889634f;
-  a.grid = sms < w.max_ctas ? sms : w.max_ctas;
+  const int ctas = w.wide ? 2 * sms : sms;
+  a.grid = ctas < w.max_ctas ? ctas : w.max_ctas;
   a.stream = stream;
-  if ((rc = encode_codes(&a.k, a.f.k, c, c.k_st, a.p.piece, hg)) != ATTN_OK ||
-      (rc = encode_codes(&a.v, a.f.v, c, c.v_st, a.p.piece, hg)) != ATTN_OK)
-    return rc;
+  if (w.wide) {
+    if ((rc = encode_queries(&a.q_map, x, c, a.q_st, w.nt)) != ATTN_OK) return rc;
+    return fail(attn::launch_cache_attn_fp8_wide(a), "8-bit cache attention launch");
+  }
   return fail(attn::launch_cache_attn_fp8(a), "8-bit cache attention launch");
 }
 

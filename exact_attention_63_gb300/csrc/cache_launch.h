@@ -111,7 +111,7 @@ struct Fp8Pages {
 };
 
 struct CacheAttnFp8Launch {
-  CUtensorMap k, v;      // (d, slot, head, page), box (d, piece, hg, 1) of bytes
+  CUtensorMap q_map;     // many rows: box (64, group, 1, nt)
   CacheAttnParams p;
   Fp8Pages f;
   const uint16_t* q;
@@ -122,6 +122,7 @@ struct CacheAttnFp8Launch {
   cudaStream_t stream;
 };
 cudaError_t launch_cache_attn_fp8(const CacheAttnFp8Launch& a);
+cudaError_t launch_cache_attn_fp8_wide(const CacheAttnFp8Launch& a);
 
 struct CacheAppendFp8Params {
   CacheParams c;

@@ -233,6 +233,16 @@ def test_malformed_tables_stay_inside():
     assert k.shape == c.k_codes.shape and v.shape == c.v_codes.shape
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_wait_limit(d):
+    """Many rows: the converters lay out no keys, the call ends, the status says so, and the next call is right."""
+    c = Fp8Case([300, 77], [40, 1], 8, 2, d, 16, seed=11).cuda()
+    attend(c, options=attn.make_options(timeout_ms=20, test_flags=attn.TEST_WITHHOLD_KV))
+    assert attn.get_status() == -8
+    o, lse = attend(c)
+    check(c, o, lse)
+
+
 # ------------------------------------------------------------------ append and gather
 
 APPEND = [
