@@ -30,7 +30,7 @@ __device__ __forceinline__ int find_warp(int n, long long x, int lane, F at) {
 // numbers of two sequences never meet and the host needs no lengths.
 //   A lane holds 8 elements of 2 (d = 128) or 4 rows at a time; all 16 rows are in flight.
 template <int D>
-__global__ void __launch_bounds__(256) cache_append_fp8_kernel(const CacheAppendFp8Params p, int items) {
+__global__ void __launch_bounds__(256, 4) cache_append_fp8_kernel(const CacheAppendFp8Params p, int items) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kSteps = 16 / kAtOnce;  // lanes a row, rows a step
   const CacheParams& c = p.c;
   const int lane = threadIdx.x & 31;

@@ -63,8 +63,10 @@ __device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float(sta
 
 // VEC: elements of an access, the largest power of two up to 8 that divides part/2.
 template <int D, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
-  extern __shared__ float2 turns[];  // [per_cta][part / 2]
+__global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const RotaryParams p) {
+  // [per_cta][VEC][part / 2 / VEC]: lanes read neighbouring runs of VEC pairs, the same pair of each at
+  // a time (in the pairs' own order they met in banks, four at a time).
+  extern __shared__ float2 turns[];
   const int first = blockIdx.x * p.per_cta, n = min(p.per_cta, p.batch * p.rows - first), half = p.part / 2;
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
     const int r = i / half, f = i - r * half, row = first + r, b = p.by_rows(row), at = row - b * p.rows;
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
     const float half_turns = static_cast<float>(static_cast<long long>(turn)) * 1.0842021724855044e-19f;  // 2^−63
     float sn, cs;
     sincospif(half_turns, &sn, &cs);
-    turns[i] = make_float2(cs * p.magnitude, (p.inverse ? -sn : sn) * p.magnitude);
+    turns[r * half + f % VEC * (half / VEC) + f / VEC] = make_float2(cs * p.magnitude, (p.inverse ? -sn : sn) * p.magnitude);
   }
   __syncthreads();
   constexpr int kItems = D / (2 * VEC);  // of a head
@@ -93,10 +95,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
     if (!turn && x == y) continue;
     Bits<VEC> u = load<VEC>(x + lo), w = load<VEC>(x + hi);
     if (turn) {
-      const float2* const cs = turns + r * half + VEC * c;
+      const float2* const cs = turns + r * half + c;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float2 t = cs[e];
+        const float2 t = cs[e * (half / VEC)];
         // pair e: (u[e], w[e]), or neighbours in (u, w)
         uint16_t& a = !INTERLEAVED ? u.v[e] : (2 * e < VEC ? u.v[2 * e] : w.v[2 * e - VEC]);
         uint16_t& z = !INTERLEAVED ? w.v[e] : (2 * e + 1 < VEC ? u.v[2 * e + 1] : w.v[2 * e + 1 - VEC]);
