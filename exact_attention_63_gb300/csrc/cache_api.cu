@@ -180,11 +180,11 @@ int check_fp8(const attn_cache* a, const void* k_scales, const void* v_scales, C
 constexpr int kFp8FewRows = 32;
 struct Fp8Tiles {
   bool wide;
-  int rows, hg, nt, max_ctas;
+  int rows, hg, nt, per_cta, max_ctas;
   size_t ml, o, bytes;
 };
 Fp8Tiles fp8_tiles_of(int rows, int hg, int max_ctas, int d) {
-  Fp8Tiles t = {false, rows, hg, 0, max_ctas, 0, 0, 0};
+  Fp8Tiles t = {false, rows, hg, 0, 1, max_ctas, 0, 0, 0};
   const size_t ends = 2ull * max_ctas * rows * hg;
   t.ml = up256((attn::kCacheMaxSeq + 1) * sizeof(int));
   t.o = t.ml + up256(ends * sizeof(float2));
@@ -196,9 +196,11 @@ Fp8Tiles fp8_tiles(int group, int max_new, int d, int hg) {
   if (all <= kFp8FewRows) return fp8_tiles_of(all <= 8 ? 8 : all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
   // As many tiles as 128 rows make, of about as many tokens each.
   const int most = tile_tokens(group, max_new), tiles = (max_new + most - 1) / most, nt = (max_new + tiles - 1) / tiles;
-  Fp8Tiles t = fp8_tiles_of(nt * group, 1, attn::kCacheMaxCtas, d);
+  const int per_cta = tiles > 1 ? 2 : 1;
+  Fp8Tiles t = fp8_tiles_of(per_cta * nt * group, 1, attn::kCacheMaxCtas / per_cta, d);
   t.wide = true;
   t.nt = nt;
+  t.per_cta = per_cta;
   return t;
 }
 size_t fp8_workspace(int group, int max_new, int d, int hg) {
@@ -273,6 +275,7 @@ int attn_fwd_cache(const attn_cache* cache, const attn_new_tokens* x, const int*
   a.p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
   a.p.rows = w.rows;
+  a.p.wide = w.rows > attn::kWideRows;
   a.p.hg = 1;
   a.p.nt = w.nt;
   a.p.ntt = w.ntt;
@@ -448,10 +451,15 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   a.p.ws_o = reinterpret_cast<float*>(ws + w.o);
   a.p.rows = w.rows;
   a.p.hg = w.hg;
-  a.p.nt = a.p.ntt = w.nt;
+  // Parts chunk by chunk where their tiles are many: the join of few tiles takes a row a block (one
+  // sequence of 4096 and 60 tokens in 19 parts: 37 us chunk by chunk).
+  a.p.wide = w.rows > attn::kWideRows && tiles * c.n_seq * c.hkv * c.d > 8ll * (2 / w.per_cta * sms);
+  a.p.nt = w.nt;
+  a.p.ntt = w.per_cta * w.nt;
+  a.tiles = w.per_cta;
   a.p.piece = attn::kFp8Block;
   a.p.scale_log2 = scale * 1.4426950408889634f;
-  const int ctas = w.wide ? 2 * sms : sms;
+  const int ctas = w.wide && w.per_cta == 1 ? 2 * sms : sms;
   a.grid = ctas < w.max_ctas ? ctas : w.max_ctas;
   a.stream = stream;
   if (w.wide) {

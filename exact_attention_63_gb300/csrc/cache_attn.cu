@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(CL<D, MT>::kThreads, 3 - MT)
               // Row by row, or (many rows) four values of every row side by side, so
               // that a warp's store is one run of bytes: as 32 pieces of 16 bytes the
               // parts of a tile of 256 rows took 6 us to leave the SM.
-              const bool wide = p.rows > kWideRows;
+              const bool wide = p.wide;
               uint4* dst = reinterpret_cast<uint4*>(p.ws_o) +
                            (wide ? (static_cast<long long>(slot) * (D / 4) + 8 * c) * p.rows + tile * p.nt * grp + r
                                  : part * (D / 4) + 8 * c);

@@ -12,12 +12,16 @@
 // memory takes to deliver it.  A block's codes are in registers before the last one's are
 // done with, so the copies of two CTAs an SM are under the products and exponentials.
 //
-// Warps: 0 loads Q (TMA), 1 issues S, 2 issues P·V, 3 looks up what the converters copy (pages,
-// scales, new tokens; four units at a time and up to twelve ahead, so that nobody waits for a page table); 4 to 7
-// softmax; 8 to 15 converters.  Two CTAs share an SM (256 TMEM columns each), and the registers
-// are split between the roles.
+// Row tiles: MT = 1, up to 128 rows a sequence and key head: two CTAs share an SM (256 TMEM columns
+// each).  MT = 2, more rows: one CTA an SM has two tiles of 128, which share every block the
+// converters lay out, two blocks of K and V at a time.
+// Warps: 0 and 1 load a tile's Q (TMA) and issue its S, 2 issues both tiles' P·V, 3 looks up what
+// the converters copy (pages, scales, new tokens; four units at a time and up to twelve ahead,
+// so that nobody waits for a page table); then four a tile for the softmax and eight converters.  The
+// registers are split between the roles.
 //
-// TMEM columns: S of half x of a block at [64x, 64x + 64), P (bf16) over its first half; O [128, 128 + d).
+// TMEM columns of a tile (256·tile + …): S of half x of a block at [64x, 64x + 64), P (bf16) over
+// its first half; O [128, 128 + d).
 #include "attn_fwd_kernel.cuh"
 #include "cache_join.cuh"
 #include "fp8_device.cuh"
@@ -28,9 +32,23 @@ namespace attn {
 namespace {
 
 constexpr float kTau = 8.0f;  // log2: a row's reference maximum moves when exceeded by more (p ≤ 2^8)
-// Registers a thread of the issuers' warpgroup, the softmax's and the converters' two; together what the block is launched with.
-constexpr int kLaunchRegs = 64, kIssuerRegs = 24, kSoftmaxRegs = 120, kConverterRegs = 56;
-static_assert(kIssuerRegs + kSoftmaxRegs + 2 * kConverterRegs == 4 * kLaunchRegs, "the split has to add up");
+// Registers a thread of the issuers' warpgroup, the softmax's (MT of them) and the converters'
+// two; together no more than what the block is launched with.  (MT = 2 with 152 and 64: 80 us
+// instead of 75 for trees of up to 60 tokens; with sixteen converters, 136 and 48: 102.)
+template <int MT>
+struct Regs {
+  static constexpr int kConverters = 8;
+  static constexpr int kLaunch = MT == 1 ? 64 : 96, kIssuer = MT == 1 ? 24 : 40, kSoftmax = MT == 1 ? 120 : 144,
+                       kConverter = MT == 1 ? 56 : 72;
+  static_assert(kIssuer + MT * kSoftmax + kConverters / 4 * kConverter <= (1 + MT + kConverters / 4) * kLaunch,
+                "the split has to fit");
+};
+
+// The blocks of the bf16 cache's kernel.
+struct ConvertPlan {
+  static constexpr bool kEight = true;
+  static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
+};
 
 struct CacheAttnFp8WideParams {
   CacheAttnParams a;
@@ -50,20 +68,22 @@ struct Unit {
 };
 constexpr int kBatches = 4;       // of four units each
 
-template <int D>
+template <int D, int MT>
 struct WL {
-  static constexpr int kThreads = 512;
+  static constexpr int kConverter0 = 4 + 4 * MT;   // first converter warp
+  static constexpr int kConverters = Regs<MT>::kConverters;
+  static constexpr int kThreads = 32 * (kConverter0 + kConverters);
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTile = 128u * D * 2;  // 128 rows of Q, K or V: [half][128 rows][128 B]
-  static constexpr int kStages = D == 128 ? 1 : 2;
-  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
-  // q_full, q_empty, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], pv_done[2], done[2],
-  // u_full[kBatches], u_empty[kBatches]
-  static constexpr int kNumBars = 2 + 4 * kStages + 8 + 2 * kBatches;
+  static constexpr int kStages = D == 128 && MT == 1 ? 1 : 2;
+  static constexpr uint32_t kQ = 0, kK = MT * kTile, kV = kK + kStages * kTile, kBar = kV + kStages * kTile;
+  // k_full[S], k_empty[S], v_full[S], v_empty[S], u_full[kBatches], u_empty[kBatches], then a tile's q_full,
+  // q_empty, s_full[2], p_full[2], pv_done[2], done; pv_end
+  static constexpr int kNumBars = 4 * kStages + 2 * kBatches + 9 * MT + 1;
   static constexpr uint32_t kUnits = (kBar + 8 * kNumBars + 15) & ~15u;  // [batch][4] Unit
   static constexpr uint32_t kMisc = kUnits + kBatches * 4 * sizeof(Unit);  // TMEM base, abort flag
   static constexpr uint32_t kSums = kMisc + 8;            // one int per warp
-  static constexpr uint32_t kTable = (kSums + 64 + 15) & ~15u;
+  static constexpr uint32_t kTable = (kSums + kThreads / 8 + 15) & ~15u;
   static constexpr uint32_t kBytes = kTable + 1024;       // + alignment; the table comes on top
   static constexpr uint32_t kColO = 128;
 };
@@ -84,28 +104,31 @@ __device__ __forceinline__ void to_bf16(const uint4& codes, float f, uint4& lo, 
   hi = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
-template <int D>
-__global__ void __launch_bounds__(WL<D>::kThreads, 2)
+template <int D, int MT>
+__global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
     cache_attn_fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const CacheAttnFp8WideParams fp) {
-  using L = WL<D>;
+  using L = WL<D, MT>;
+  using R = Regs<MT>;
   const CacheAttnParams& p = fp.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBar;
-  const uint32_t q_full = bars, q_empty = bars + 8;
-  auto k_full = [&](int s) { return bars + 8u * (2 + s); };
-  auto k_empty = [&](int s) { return bars + 8u * (2 + L::kStages + s); };
-  auto v_full = [&](int s) { return bars + 8u * (2 + 2 * L::kStages + s); };
-  auto v_empty = [&](int s) { return bars + 8u * (2 + 3 * L::kStages + s); };
-  constexpr uint32_t kB = 2 + 4 * L::kStages;
-  auto s_full = [&](int x) { return bars + 8u * (kB + x); };
-  auto p_full = [&](int x) { return bars + 8u * (kB + 2 + x); };
-  auto pv_done = [&](int x) { return bars + 8u * (kB + 4 + x); };
-  auto done = [&](int x) { return bars + 8u * (kB + 6 + x); };
-  auto u_full = [&](int i) { return bars + 8u * (kB + 8 + i); };
-  auto u_empty = [&](int i) { return bars + 8u * (kB + 8 + kBatches + i); };
+  auto k_full = [&](int s) { return bars + 8u * s; };
+  auto k_empty = [&](int s) { return bars + 8u * (L::kStages + s); };
+  auto v_full = [&](int s) { return bars + 8u * (2 * L::kStages + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (3 * L::kStages + s); };
+  auto u_full = [&](int i) { return bars + 8u * (4 * L::kStages + i); };
+  auto u_empty = [&](int i) { return bars + 8u * (4 * L::kStages + kBatches + i); };
+  constexpr uint32_t kB = 4 * L::kStages + 2 * kBatches;
+  auto q_full = [&](int i) { return bars + 8u * (kB + 9 * i); };  // tile i, half x
+  auto q_empty = [&](int i) { return bars + 8u * (kB + 9 * i + 1); };
+  auto s_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 2 + x); };
+  auto p_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 4 + x); };
+  auto pv_done = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 6 + x); };
+  auto done = [&](int i) { return bars + 8u * (kB + 9 * i + 8); };
+  const uint32_t pv_end = bars + 8u * (kB + 9 * MT);
   Unit* const found = reinterpret_cast<Unit*>(smem + L::kUnits);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
@@ -114,36 +137,39 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
   const int cta = blockIdx.x;
 
   if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_alloc(smem_u32(tmem_slot), 256 * MT);
     tmem_relinquish();
     tc_fence_before();
   }
   if (threadIdx.x == 32) {
     *abort_flag = 0u;
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(k_full(s), 8);
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 8);
+      mbar_init(k_full(s), L::kConverters);
+      mbar_init(k_empty(s), MT);  // (each tile's issuer answers for its own reads)
+      mbar_init(v_full(s), L::kConverters);
       mbar_init(v_empty(s), 1);
     }
     for (int i = 0; i < kBatches; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 8);
+      mbar_init(u_empty(i), L::kConverters);
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(s_full(x), 1);
-      mbar_init(p_full(x), 4);
-      mbar_init(pv_done(x), 1);
-      mbar_init(done(x), 1);
+    for (int i = 0; i < MT; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(s_full(i, x), 1);
+        mbar_init(p_full(i, x), 4);
+        mbar_init(pv_done(i, x), 1);
+      }
+      mbar_init(done(i), 1);
     }
+    mbar_init(pv_end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
   if (threadIdx.x == 64) tma_prefetch_desc(&tm_q);
   prefix_table(p.c.n_seq, tab, reinterpret_cast<int*>(smem + L::kSums),
-               [&](int s) { return units_of<BlockPlan>(p, s); });
+               [&](int s) { return units_of<ConvertPlan>(p, s); });
   tc_fence_after();
   const int units = tab[p.c.n_seq];
   if (cta == 0)
@@ -151,7 +177,7 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
   const int grid = min(static_cast<int>(gridDim.x), units);  // CTAs with work: each of them at least one unit
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= grid) {
-    if (warp == 0) tmem_dealloc(*tmem_slot, 256);
+    if (warp == 0) tmem_dealloc(*tmem_slot, 256 * MT);
     return;
   }
   const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
@@ -159,91 +185,98 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
-    if (lane == 0 && warp == 0) {
-      // ============================================================== Q
-      int ns = 0;
-      bool ok = true;
-      for (int u = u0; u < u1 && ok; ++ns) {
-        const Segment sg = segment_at<BlockPlan>(p, tab, u, u1);
-        u += sg.b1 - sg.b0;
-        ok = wait_bar(q_empty, (ns & 1) ^ 1u, wc);
-        if (!ok) break;
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.nt * p.c.group) * 128u * L::kHalves);
-        for (int hf = 0; hf < L::kHalves; ++hf)
-          tma_load_4d(base + L::kQ + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + sg.m * p.nt, q_full);
-      }
-      // No copy may be in flight when the CTA ends, whatever ended the loop.
-      const uint64_t t0 = globaltimer_ns();
-      if (ns > 0)
-        while (!mbar_try_wait(q_full, (ns - 1) & 1))
-          if (globaltimer_ns() - t0 > p.timeout_ns) break;
-    } else if (lane == 0 && warp == 1) {
-      // ======================================================= S issuer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssuer));
+    if (lane == 0 && warp < MT) {
+      // ================================================ a tile's Q and S
       constexpr uint32_t idS = idesc_bf16(128, 64, false);
-      const uint64_t dq = sdesc_kmajor_sw128(base + L::kQ);
-      int g = 0, ns = 0;
+      const int tile = warp;
+      const uint32_t q_at = base + L::kQ + tile * L::kTile;
+      const uint64_t dq = sdesc_kmajor_sw128(q_at);
+      int g = 0, nq = 0, e = 0;  // blocks of the CTA; copies of Q; blocks of this tile (fewer, where a segment has rows for the first only)
       bool ok = true;
-      for (int u = u0; u < u1 && ok; ++ns) {
-        const Segment sg = segment_at<BlockPlan>(p, tab, u, u1);
+      for (int u = u0; u < u1 && ok;) {
+        const Segment sg = segment_at<ConvertPlan>(p, tab, u, u1);
         u += sg.b1 - sg.b0;
-        ok = wait_bar(q_full, ns & 1, wc);
+        const int t0 = sg.m * p.ntt + tile * p.nt;
+        const bool now = tile == 0 || sg.k.n > t0;
+        if (now) {
+          ok = nq == 0 || wait_bar(q_empty(tile), (nq - 1) & 1, wc);
+          if (!ok) break;
+          mbar_arrive_expect_tx(q_full(tile), static_cast<uint32_t>(p.nt * p.c.group) * 128u * L::kHalves);
+          for (int hf = 0; hf < L::kHalves; ++hf)
+            tma_load_4d(q_at + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + t0, q_full(tile));
+          ok = wait_bar(q_full(tile), nq & 1, wc);
+          ++nq;
+        }
         for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
           const int st = g % L::kStages;
           ok = wait_bar(k_full(st), (g / L::kStages) & 1, wc);
-          const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            // The half's last product has read its P, which lies over S.
-            if (g > 0) ok = ok && wait_bar(pv_done(x), (g - 1) & 1, wc);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              mma_ss(tmem + 64 * x, dq + o, dk + o + ((x * 8192) >> 4), idS, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(s_full(x));
-          }
           if (!ok) break;
+          if (now) {
+            const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // The half's last product has read its P, which lies over S.
+              if (e > 0) ok = ok && wait_bar(pv_done(tile, x), (e - 1) & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + 256 * tile + 64 * x, dq + o, dk + o + ((x * 8192) >> 4), idS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(s_full(tile, x));
+            }
+            ++e;
+            if (!ok) break;
+            if (b == sg.b1 - 1) mma_commit(q_empty(tile));
+          }
           mma_commit(k_empty(st));
-          if (b == sg.b1 - 1) mma_commit(q_empty);
         }
       }
-      mma_commit(done(0));
+      mma_commit(done(tile));
+      // No product and no copy may be in flight when the CTA ends, whatever ended the loop.
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(done(0), 0))
-        if (globaltimer_ns() - t0 > p.timeout_ns) break;
+      auto drain = [&](uint32_t bar, uint32_t parity) {
+        while (!mbar_try_wait(bar, parity))
+          if (globaltimer_ns() - t0 > p.timeout_ns) break;
+      };
+      drain(done(tile), 0);
+      if (nq > 0) drain(q_full(tile), (nq - 1) & 1);
     } else if (lane == 0 && warp == 2) {
-      // ===================================================== P·V issuer
+      // ==================================================== P·V of all tiles
       constexpr uint32_t idPV = idesc_bf16(128, D, true);
-      int g = 0;
+      int g = 0, e1 = 0;  // blocks of the CTA (and of the first tile), blocks of the second
       bool ok = true;
       for (int u = u0; u < u1 && ok;) {
-        const Segment sg = segment_at<BlockPlan>(p, tab, u, u1);
+        const Segment sg = segment_at<ConvertPlan>(p, tab, u, u1);
         u += sg.b1 - sg.b0;
+        const int tiles = MT == 2 && sg.k.n - sg.m * p.ntt > p.nt ? 2 : 1;
         for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
           const int st = g % L::kStages;
           ok = wait_bar(v_full(st), (g / L::kStages) & 1, wc);
           const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            ok = ok && wait_bar(p_full(x), g & 1, wc);
-            if (!ok) break;
-            tc_fence_after();
+          for (int x = 0; x < 2; ++x)
+            for (int i = 0; i < tiles; ++i) {
+              ok = ok && wait_bar(p_full(i, x), (i == 0 ? g : e1) & 1, wc);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t t = tmem + 256 * i;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(tmem + L::kColO, tmem + 64 * x + kk * 8, dv + (((4 * x + kk) * 2048) >> 4), idPV,
-                     (b > sg.b0 || x > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(pv_done(x));
-          }
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(t + L::kColO, t + 64 * x + kk * 8, dv + (((4 * x + kk) * 2048) >> 4), idPV,
+                       (b > sg.b0 || x > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(pv_done(i, x));
+            }
           if (!ok) break;
           mma_commit(v_empty(st));
+          if (tiles == 2) ++e1;
         }
       }
-      mma_commit(done(1));
+      mma_commit(pv_end);
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(done(1), 0))
+      while (!mbar_try_wait(pv_end, 0))
         if (globaltimer_ns() - t0 > p.timeout_ns) break;
     }
     if (warp == 3) {
@@ -256,7 +289,7 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
         uint8_t ks = 0, vs = 0;
         Segment sg = {};
         if (u < u1) {
-          sg = segment_at<BlockPlan>(p, tab, u, u1);
+          sg = segment_at<ConvertPlan>(p, tab, u, u1);
           const int j = (sg.b0 << 7) + 16 * i;
           if (j < sg.k.len) {
             const int blk = j / p.c.page_size, slot = j - blk * p.c.page_size;
@@ -287,25 +320,20 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
         warp_arrive(u_full(slot), lane);
       }
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConverterRegs));
+  } else if (warp >= L::kConverter0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kConverter));
     // ========================================================= converters
-    // A lane has 16 codes of a row, a step of the eight warps 32 rows (d = 64: 64).
-    constexpr int kRuns = D / 16, kStep = 256 / kRuns, kSteps = 128 / kStep;
-    const int tid = threadIdx.x - 256, run = tid % kRuns, row0 = tid / kRuns;
+    // A lane has 16 codes of a row, a step of eight warps 32 rows (d = 64: 64).
+    constexpr int kRuns = D / 16, kStep = 32 * L::kConverters / kRuns, kSteps = 128 / kStep;
+    const int tid = threadIdx.x - 32 * L::kConverter0, run = tid % kRuns, row0 = tid / kRuns;
     const uint8_t *const k_lane = fp.f.k + (row0 & 15) * p.c.k_st[1] + 16 * run,
                   *const v_lane = fp.f.v + (row0 & 15) * p.c.v_st[1] + 16 * run;
     auto load = [&](uint4(&x)[kSteps], const Unit& un, bool v) {
       const uint8_t* const from = v ? v_lane : k_lane;
       const long long* const at = (v ? un.v_at : un.k_at) + (row0 >> 4);
-      if (un.cached == 128) {
+      if (un.cached == 128)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) x[i] = __ldcs(reinterpret_cast<const uint4*>(from + at[i * kStep / 16]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-          if (at[i * kStep / 16] >= 0) x[i] = __ldcs(reinterpret_cast<const uint4*>(from + at[i * kStep / 16]));
-      }
     };
     // Where the two runs of 8 bf16 elements go (rows of a step further on lie as far on); lanes
     // that would meet in a bank write them in the other order.
@@ -346,18 +374,21 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
           }
           return;
         }
-#pragma unroll
+        // A tail, new tokens, or both: few of all units, so their codes are read here and the code is short.
+        const uint8_t* const from = v ? v_lane : k_lane;
+        const long long* const at = (v ? un.v_at : un.k_at) + (row0 >> 4);
+        const long long* const fst = v ? fp.vn_st : fp.kn_st;
+#pragma unroll 1
         for (int i = 0; i < kSteps; ++i) {
           const int row = i * kStep + row0;
           uint4 lo, hi;
           if (row < cached) {
-            to_bf16(x[i], scale[i * kStep / 16], lo, hi);
+            to_bf16(*reinterpret_cast<const uint4*>(from + at[i * kStep / 16]), scale[i * kStep / 16], lo, hi);
           } else if (row >= off && row < off + fresh) {
-            const long long* const fst = v ? fp.vn_st : fp.kn_st;
-            const uint4* const from = reinterpret_cast<const uint4*>((v ? fp.vn : fp.kn) + (un.q0 + row - off) * fst[0] +
-                                                                     un.h * fst[1] + 16 * run);
-            lo = from[0];
-            hi = from[1];
+            const uint4* const own = reinterpret_cast<const uint4*>((v ? fp.vn : fp.kn) + (un.q0 + row - off) * fst[0] +
+                                                                    un.h * fst[1] + 16 * run);
+            lo = own[0];
+            hi = own[1];
           } else {
             // No key: S is masked there, but a NaN times P's 0 would spread from V.
             if (!v) continue;
@@ -389,20 +420,22 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
       if ((g & 3) == 3) warp_arrive(u_empty(g / 4 % kBatches), lane);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmax));
     // ============================================================ softmax
+    const int tile = MT == 1 ? 0 : (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
-    const uint32_t t_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_base = tmem + 256 * tile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tO = t_base + L::kColO;
     const float sc = p.scale_log2;
     const uint64_t sc2 = pack2(sc, sc);
-    int g = 0;
+    int g = 0;  // blocks of this tile
     bool ok = true;
     for (int u = u0; u < u1 && ok;) {
-      const Segment sg = segment_at<BlockPlan>(p, tab, u, u1);
+      const Segment sg = segment_at<ConvertPlan>(p, tab, u, u1);
       const bool first_of_cta = u == u0;
       u += sg.b1 - sg.b0;
-      const int t0 = sg.m * p.nt, n_rows = min(sg.k.n - t0, p.nt) * p.c.group;
+      const int t0 = sg.m * p.ntt + tile * p.nt, n_rows = min(sg.k.n - t0, p.nt) * p.c.group;
+      if (MT == 2 && n_rows <= 0) continue;
       const bool active = (warp & 3) * 32 < n_rows;
       float m_run = -INFINITY, l_run = 0.f;
       uint32_t anc[4] = {0u, 0u, 0u, 0u};  // the new tokens this row sees
@@ -422,7 +455,7 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
       auto block = [&](int b, int x, auto mask_tag) -> bool {
         constexpr bool MASK = decltype(mask_tag)::value;
         const uint32_t tS = t_base + 64 * x;
-        const bool got = wait_bar_cold(s_full(x), g & 1, wc);
+        const bool got = wait_bar_cold(s_full(tile, x), g & 1, wc);
         if (__any_sync(0xffffffffu, !got)) return false;
         tc_fence_after();
         uint32_t vis[2];
@@ -476,7 +509,7 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
             if (b > sg.b0 || x > 0) {
               const float alpha = need ? ex2_mufu(m_run - m_new) : 1.f;
               // (the product before this one: the other half's, or the last block's)
-              const bool landed = wait_bar(pv_done(x ^ 1), (x > 0 ? g : g - 1) & 1, wc);
+              const bool landed = wait_bar(pv_done(tile, x ^ 1), (x > 0 ? g : g - 1) & 1, wc);
               if (__any_sync(0xffffffffu, !landed)) return false;
               tc_fence_after();
 #pragma unroll 1
@@ -523,7 +556,7 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
           tmem_wait_st();
         }
         tc_fence_before();
-        warp_arrive(p_full(x), lane);
+        warp_arrive(p_full(tile, x), lane);
         return true;
       };
       for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g)
@@ -533,14 +566,15 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
       if (active) {
-        const bool landed = wait_bar_cold(pv_done(1), (g - 1) & 1, wc);
+        const bool landed = wait_bar_cold(pv_done(tile, 1), (g - 1) & 1, wc);
         if (__any_sync(0xffffffffu, !landed)) { ok = false; break; }
         tc_fence_after();
         const bool whole = sg.b0 == 0 && sg.b1 == sg.k.db + 1;
         const int grp = p.c.group, t = t0 + r / grp, hq = sg.h * grp + r % grp, H = p.c.hkv * grp;
         const long long token = sg.k.q0 + t;
         const int slot = 2 * cta + (first_of_cta ? 0 : 1);
-        const long long part = static_cast<long long>(slot) * p.rows + r;
+        const int in_part = tile * p.nt * grp + r;
+        const long long part = static_cast<long long>(slot) * p.rows + in_part;
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -561,9 +595,9 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
               }
             } else {
               // Row by row, or (many rows) four values of every row side by side.
-              const bool wide = p.rows > kWideRows;
+              const bool wide = p.wide;
               uint4* dst = reinterpret_cast<uint4*>(p.ws_o) +
-                           (wide ? (static_cast<long long>(slot) * (D / 4) + 8 * c) * p.rows + r : part * (D / 4) + 8 * c);
+                           (wide ? (static_cast<long long>(slot) * (D / 4) + 8 * c) * p.rows + in_part : part * (D / 4) + 8 * c);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 *dst = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
@@ -588,39 +622,40 @@ __global__ void __launch_bounds__(WL<D>::kThreads, 2)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 256 * MT);
   }
 }
 
-template <int D>
+template <int D, int MT>
 cudaError_t launch(const CacheAttnFp8Launch& a) {
-  using L = WL<D>;
+  using L = WL<D, MT>;
   const CacheAttnFp8WideParams p = {a.p, a.f, a.kn, a.vn, {a.kn_st[0], a.kn_st[1]}, {a.vn_st[0], a.vn_st[1]}};
   const unsigned int smem = L::kBytes + 4u * (p.a.c.n_seq + 1);
   static volatile int state[64] = {};  // per device: 0 not checked, 1 usable, -1 not usable
   if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
   if (state[a.device] == 0) {
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, cache_attn_fp8_wide_kernel<D>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, cache_attn_fp8_wide_kernel<D, MT>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs == kLaunchRegs)
-      e = cudaFuncSetAttribute(cache_attn_fp8_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (fa.numRegs == Regs<MT>::kLaunch)
+      e = cudaFuncSetAttribute(cache_attn_fp8_wide_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                L::kBytes + 4 * (kCacheMaxSeq + 1));
     if (e != cudaSuccess) return e;
-    state[a.device] = fa.numRegs == kLaunchRegs ? 1 : -1;
+    state[a.device] = fa.numRegs == Regs<MT>::kLaunch ? 1 : -1;
   }
   // (the roles' registers would not add up to what the block has, and a role would wait for ever)
   if (state[a.device] < 0) return cudaErrorNotSupported;
-  cache_attn_fp8_wide_kernel<D><<<a.grid, L::kThreads, smem, a.stream>>>(a.q_map, p);
+  cache_attn_fp8_wide_kernel<D, MT><<<a.grid, L::kThreads, smem, a.stream>>>(a.q_map, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, BlockPlan>(p.a, a.grid, a.stream);
+  return launch_join<D, ConvertPlan>(p.a, a.grid, a.stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn_fp8_wide(const CacheAttnFp8Launch& a) {
-  return a.p.c.d == 64 ? launch<64>(a) : launch<128>(a);
+  if (a.p.c.d == 64) return a.tiles == 2 ? launch<64, 2>(a) : launch<64, 1>(a);
+  return a.tiles == 2 ? launch<128, 2>(a) : launch<128, 1>(a);
 }
 
 }  // namespace attn

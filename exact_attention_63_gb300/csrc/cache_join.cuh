@@ -10,8 +10,6 @@
 namespace attn {
 namespace {
 
-constexpr int kWideRows = 64;  // parts of more rows lie chunk by chunk, [D/4][rows][4]
-
 // Joins the parts of the tiles that were split.  With the parts' maxima m_i and
 // sums l_i:  m = max m_i,  O = Σ 2^(m_i − m) O_i / Σ 2^(m_i − m) l_i.
 // WAY = kJoinFew: a block takes one row, its eight warps deal out the parts (few rows;
@@ -161,12 +159,14 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
         sum += w * ml.y;
       }
       const int n = min(32, (c1 - cb) / SPLIT + 1);
-      for (int i = 0; i < n; i += 16) {  // sixteen parts in flight; behind the last, weight 0
+      for (int i = 0; i < n; i += 16) {  // sixteen parts in flight
         Vec y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = load(min(cb + (i + e) * SPLIT, c1), r);
+        for (int e = 0; e < 16; ++e)
+          if (i + e < n) y[e] = load(cb + (i + e) * SPLIT, r);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
+          if (i + e >= n) break;
           const float we = __shfl_sync(0xffffffffu, w, i + e);
           if (we != 0.f) add(acc, we, y[e]);
         }
@@ -203,14 +203,17 @@ template <int D, class Plan>
 cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream) {
   const int mt_max = row_tiles(p, p.c.max_new);
   const long long tiles = static_cast<long long>(p.c.n_seq) * p.c.hkv * mt_max;
-  const bool wide = p.rows > kWideRows;
+  const bool wide = p.wide;
   // A row a block where a tile has many parts on average, which the other kind reads one
   // after the other, or where there are few such blocks for the GPU (GPU time of a whole
   // call, so and otherwise: 8 tiles of 48 rows in 152 parts 21 and 34 us at d = 128; 64
   // tiles of 4 rows 19 and 23 us at d = 64, 23 and 24 us at 128; 256 tiles of 4 rows 57
   // and 52 us at 128; 32 tiles of 32 rows 22 and 20 us at 128, 16 and 20 us at 64).
-  const bool few = !wide && (tiles * D <= 8ll * p.hg * grid || tiles * p.rows * D <= 128ll * grid);
-  const bool eight = Plan::kEight && !few && p.rows <= 16;
+  const bool row_a_block = !wide && (tiles * D <= 8ll * p.hg * grid || tiles * p.rows * D <= 128ll * grid);
+  // Where a warp may take a row with all its parts (the 8-bit cache): unless the blocks of a row
+  // each fit on the SMs at a time (8 tiles of 240 rows in 19 parts: 26 us a row a block).
+  const bool few = row_a_block && (!Plan::kEight || tiles * p.rows <= 4ll * grid);
+  const bool eight = Plan::kEight && !few && !wide && (row_a_block || p.rows <= 16);
   const long long blocks = tiles * (few ? p.rows : eight ? (p.rows + 7) / 8 : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.

@@ -9,6 +9,7 @@
 
 namespace attn {
 
+constexpr int kWideRows = 64;        // parts of more rows may lie chunk by chunk
 constexpr int kCacheMaxSeq = 2048;   // sequences of one call: their offsets are kept in shared memory
 constexpr int kCacheMaxCtas = 320;   // row tiles at work at a time (two per SM); sizes the attention's workspace
 
@@ -56,6 +57,7 @@ struct CacheAttnParams {
   float* ws_o;           // [2 * grid, rows, d] its unnormalised output
   int rows;              // row pitch of the parts
   int hg;                // key heads that a CTA works on at a time
+  bool wide;             // parts lie chunk by chunk, [d/4][rows][4]
   int nt;                // tokens of a row tile: nt * group <= 128 rows
   int ntt;               // tokens of a CTA's row tiles
   int piece;             // key rows of one copy: the largest power of two in page_size, at most 64
@@ -118,6 +120,7 @@ struct CacheAttnFp8Launch {
   const uint16_t* kn;
   const uint16_t* vn;
   long long q_st[2], kn_st[2], vn_st[2];  // element strides: token, head
+  int tiles;             // many rows: row tiles of a CTA, 2 where a sequence may have more than 128 rows
   int grid, device;
   cudaStream_t stream;
 };
