@@ -2,6 +2,11 @@
 
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -231,6 +236,79 @@ def test_malformed_tables_stay_inside():
     cache.cache_gather_fp8(*c.pages(), c.table, c.seq_lens, c.cu, c.total)
     torch.cuda.synchronize()
     assert k.shape == c.k_codes.shape and v.shape == c.v_codes.shape
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hkv,group,new", [(8, 4, 1), (8, 1, 8), (6, 2, 1), (16, 1, 1), (16, 3, 4), (12, 2, 5), (5, 4, 4), (8, 4, 8), (8, 8, 5),
+                                           (2, 40, 1), (1, 33, 1), (1, 16, 1), (4, 17, 1), (8, 4, 33)])
+def test_attention_of_head_counts(hkv, group, new, d):
+    """Runs of 8, 4, 2 and 1 key heads, tiles of 8, 16, 32 and more rows, one sequence and several."""
+    for lens in ([300], [129, 0, 700, 33]):
+        c = Fp8Case(lens, [new, 1, new, 0][:len(lens)], hkv * group, hkv, d, 48, seed=hkv).cuda()
+        o, lse = attend(c)
+        check(c, o, lse)
+
+
+@pytest.mark.parametrize("new", [1, 3, 9, 40])
+def test_attention_of_2048_sequences(new):
+    """The most sequences of a call: their table is as large as it gets beside every kernel's tiles."""
+    lens = [(7 * i) % 40 for i in range(2048)]
+    c = Fp8Case(lens, [new if i % 97 == 0 else int(i % 5 == 0) for i in range(2048)], 4, 1, 64, 16, seed=19).cuda()
+    o, lse = attend(c)
+    check(c, o, lse)
+
+
+def test_random_calls():
+    """Seeded calls over the range of the contract: heads, groups, pages, lengths from 0, trees, padded bounds."""
+    r = np.random.default_rng(20)
+    for i in range(60):
+        n, hkv = int(r.integers(1, 9)), int(r.choice([1, 2, 3, 4, 8]))
+        group, d, page = int(r.choice([1, 2, 3, 4, 7, 8])), int(r.choice([64, 128])), int(r.choice([16, 32, 48, 64, 128, 256]))
+        new = [int(x) for x in r.choice([0, 1, 1, 2, 4, 7, 13, 40, 128], n)]
+        lens = [int(x) for x in r.integers(0, int(r.choice([20, 300, 1500])), n)]
+        if not sum(new):
+            new[0] = 1
+        c = Fp8Case(lens, new, hkv * group, hkv, d, page, seed=i, tree=str(r.choice(["random", "chain", "roots", "line"])),
+                    spread=int(r.choice([0, 0, 3]))).cuda()
+        o, lse = cache.attn_fwd_cache_fp8(c.q, c.k_new, c.v_new, *c.pages(), c.table, c.seq_lens, c.cu,
+                                          min(128, c.max_new() + int(r.choice([0, 0, 5]))), parents=c.parents)
+        check(c, o, lse)
+
+
+def test_first_calls_in_a_graph_and_from_two_threads():
+    """A process whose first calls are captured, and two threads with streams of their own."""
+    code = textwrap.dedent("""
+        import sys
+        sys.path[:0] = ["tests", "."]
+        import torch
+        from concurrent.futures import ThreadPoolExecutor
+        from exact_attention_63_gb300 import attn, cache, rotary
+        from fp8_cache_reference import Fp8Case
+        from test_cache_fp8_gpu import attend, check
+        cases = [Fp8Case([200, 33], [t, 1], 8, 2, 128, 16, seed=t).cuda() for t in (1, 40)]
+        freq = rotary.rotary_frequencies(128).cuda()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = [attend(c) for c in cases]
+            turned = rotary.rotary_fwd(cases[0].q, cases[0].k_new, None, freq)
+            lens = cases[0].seq_lens
+            cache.cache_gather_fp8(*cases[0].pages(), cases[0].table, lens, cases[0].cu, cases[0].total)
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, o in zip(cases, outs):
+            check(c, *o)
+        def work(i):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    o = attend(cases[i])
+                torch.cuda.current_stream().synchronize()
+                return o
+        with ThreadPoolExecutor(2) as pool:
+            for o, want in zip(pool.map(work, (0, 1)), outs):
+                assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+        assert attn.get_status() == 0
+    """)
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), timeout=240)
 
 
 @pytest.mark.parametrize("d", [64, 128])
