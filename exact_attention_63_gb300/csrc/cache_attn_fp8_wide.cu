@@ -2,23 +2,26 @@
 // (cache_attn_fp8.cu has the formulas, and the kernel for few).
 //
 // With more than 32 rows a sequence and key head the products belong on the tensor core's
-// tcgen05 instructions, whose operands have 16 bits: eight warps (the converters) read the
+// tcgen05 instructions, whose operands have 16 bits: 8 or 16 warps (the converters) read the
 // codes, 16 bytes a lane and whole rows of a head at a time, take them to bf16 with their
 // scales, which is exact, and lay them out in shared memory as TMA would; all that follows is as over a
 // cache of bf16 (cache_attn.cu): S of 64 keys at a time, the softmax of one row a thread with P over
 // S, O in tensor memory, units of 128 keys dealt out evenly, parts joined by a second kernel.
 //   Each code costs the converters about three instructions and the shared memory 4 bytes
 // (written once, read once), half of what its 128 bytes a cycle carry in the time that
-// memory takes to deliver it.  A block's codes are in registers before the last one's are
-// done with, so the copies of two CTAs an SM are under the products and exponentials.
+// memory takes to deliver it.  A run's registers take the codes that come next (K's, V's, the next
+// block's K's) as soon as it is converted, so memory is at work under products and exponentials.
 //
 // Row tiles: MT = 1, up to 128 rows a sequence and key head: two CTAs share an SM (256 TMEM columns
 // each).  MT = 2, more rows: one CTA an SM has two tiles of 128, which share every block the
 // converters lay out, two blocks of K and V at a time.
 // Warps: 0 and 1 load a tile's Q (TMA) and issue its S, 2 issues both tiles' P·V, 3 looks up what
 // the converters copy (pages, scales, new tokens; four units at a time and up to twelve ahead,
-// so that nobody waits for a page table); then four a tile for the softmax and eight converters.  The
-// registers are split between the roles.
+// so that nobody waits for a page table); then four a tile for the softmax and the converters: 8, or with
+// MT = 2 16 (64 tokens over 64 sequences of up to 8191: 352 us, with 8 of them 396).
+//   The registers are split between the roles.  Next to nothing may spill: shared memory takes up nearly all
+// of L1, so a reload comes from L2, and in the chain product, softmax, product it shows (with the issuers at
+// 40 registers instead of 56 the trees took 74 us instead of 70, 64 tokens 444 instead of 412).
 //
 // TMEM columns of a tile (256·tile + …): S of half x of a block at [64x, 64x + 64), P (bf16) over
 // its first half; O [128, 128 + d).
@@ -33,13 +36,13 @@ namespace {
 
 constexpr float kTau = 8.0f;  // log2: a row's reference maximum moves when exceeded by more (p ≤ 2^8)
 // Registers a thread of the issuers' warpgroup, the softmax's (MT of them) and the converters'
-// two; together no more than what the block is launched with.  (MT = 2 with 152 and 64: 80 us
-// instead of 75 for trees of up to 60 tokens; with sixteen converters, 136 and 48: 102.)
+// (two or four); together no more than what the block is launched with.  (MT = 1 with 24, 120 and 56:
+// 278 us instead of 240 for 16 tokens over 64 sequences; with 40, 120 and 48: 269.)
 template <int MT>
 struct Regs {
-  static constexpr int kConverters = 8;
-  static constexpr int kLaunch = MT == 1 ? 64 : 96, kIssuer = MT == 1 ? 24 : 40, kSoftmax = MT == 1 ? 120 : 144,
-                       kConverter = MT == 1 ? 56 : 72;
+  static constexpr int kConverters = MT == 1 ? 8 : 16;
+  static constexpr int kLaunch = MT == 1 ? 64 : 72, kIssuer = MT == 1 ? 32 : 56, kSoftmax = MT == 1 ? 112 : 128,
+                       kConverter = MT == 1 ? 56 : 48;
   static_assert(kIssuer + MT * kSoftmax + kConverters / 4 * kConverter <= (1 + MT + kConverters / 4) * kLaunch,
                 "the split has to fit");
 };
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
   auto u_full = [&](int i) { return bars + 8u * (4 * L::kStages + i); };
   auto u_empty = [&](int i) { return bars + 8u * (4 * L::kStages + kBatches + i); };
   constexpr uint32_t kB = 4 * L::kStages + 2 * kBatches;
-  auto q_full = [&](int i) { return bars + 8u * (kB + 9 * i); };  // tile i, half x
+  auto q_full = [&](int i) { return bars + 8u * (kB + 9 * i); };  // of tile i
   auto q_empty = [&](int i) { return bars + 8u * (kB + 9 * i + 1); };
   auto s_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 2 + x); };
   auto p_full = [&](int i, int x) { return bars + 8u * (kB + 9 * i + 4 + x); };
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
     if (lane == 0 && warp < MT) {
       // ================================================ a tile's Q and S
       constexpr uint32_t idS = idesc_bf16(128, 64, false);
-      const int tile = warp;
+      const int tile = MT == 1 ? 0 : warp;
       const uint32_t q_at = base + L::kQ + tile * L::kTile;
       const uint64_t dq = sdesc_kmajor_sw128(q_at);
       int g = 0, nq = 0, e = 0;  // blocks of the CTA; copies of Q; blocks of this tile (fewer, where a segment has rows for the first only)
@@ -323,18 +326,11 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
   } else if (warp >= L::kConverter0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kConverter));
     // ========================================================= converters
-    // A lane has 16 codes of a row, a step of eight warps 32 rows (d = 64: 64).
+    // A lane has 16 codes of a row, a step of eight warps 32 rows (d = 64: 64; sixteen warps twice that).
     constexpr int kRuns = D / 16, kStep = 32 * L::kConverters / kRuns, kSteps = 128 / kStep;
     const int tid = threadIdx.x - 32 * L::kConverter0, run = tid % kRuns, row0 = tid / kRuns;
     const uint8_t *const k_lane = fp.f.k + (row0 & 15) * p.c.k_st[1] + 16 * run,
                   *const v_lane = fp.f.v + (row0 & 15) * p.c.v_st[1] + 16 * run;
-    auto load = [&](uint4(&x)[kSteps], const Unit& un, bool v) {
-      const uint8_t* const from = v ? v_lane : k_lane;
-      const long long* const at = (v ? un.v_at : un.k_at) + (row0 >> 4);
-      if (un.cached == 128)
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) x[i] = __ldcs(reinterpret_cast<const uint4*>(from + at[i * kStep / 16]));
-    };
     // Where the two runs of 8 bf16 elements go (rows of a step further on lie as far on); lanes
     // that would meet in a bank write them in the other order.
     const int half = run >> 2, first = ((2 * run & 7) + half) ^ (row0 & 7);
@@ -344,7 +340,12 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
       *reinterpret_cast<uint4*>(first_at + tile + row * 128) = half ? hi : lo;
       *reinterpret_cast<uint4*>(second_at + tile + row * 128) = half ? lo : hi;
     };
-    uint4 kx[kSteps], vx[kSteps];
+    // K's codes, then V's in their places as K's are converted, then the next block's K's.  (V's in
+    // registers of their own, asked for earlier, cost spills: 64 rows 308 us instead of 240.)
+    uint4 x[kSteps];
+    auto load = [&](int i, const Unit& un, bool v) {
+      x[i] = __ldcs(reinterpret_cast<const uint4*>((v ? v_lane : k_lane) + (v ? un.v_at : un.k_at)[(row0 >> 4) + i * kStep / 16]));
+    };
     const int units_here = u1 - u0;
     bool ok = !(p.test_flags & 1u);
     // Unit g's entry; the first of a batch waits for it.
@@ -355,15 +356,22 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
       return !__any_sync(0xffffffffu, !got);
     };
     ok = ok && arrived(0);
-    if (ok) {
-      load(kx, unit(0), false);
-      load(vx, unit(0), true);
-    }
+    if (ok && unit(0).cached == 128)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) load(i, unit(0), false);
     for (int g = 0; g < units_here && ok; ++g) {
       const Unit& un = unit(g);
       const int st = g % L::kStages, ph = (g / L::kStages) & 1;
       const int cached = un.cached, off = un.off, fresh = un.fresh;
-      auto convert = [&](uint32_t tile, const uint4(&x)[kSteps], bool v) {
+      const bool more = g + 1 < units_here;
+      if (more) ok = arrived(g + 1);
+      if (!ok) break;
+      const Unit& after = unit(more ? g + 1 : g);
+      const bool after_full = more && after.cached == 128;
+      // The unit's K or V; what comes next (its V, the next one's K) is asked for as places get free.
+      auto convert = [&](uint32_t tile, bool v) {
+        const Unit& next = v ? after : un;
+        const bool next_full = v ? after_full : cached == 128;
         const float* const scale = (v ? un.v_scale : un.k_scale) + (row0 >> 4);
         if (cached == 128) {
 #pragma unroll
@@ -371,6 +379,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
             uint4 lo, hi;
             to_bf16(x[i], scale[i * kStep / 16], lo, hi);
             put(tile, i * kStep + row0, lo, hi);
+            if (next_full) load(i, next, !v);
           }
           return;
         }
@@ -396,26 +405,22 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
           }
           put(tile, row, lo, hi);
         }
+        if (next_full)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) load(i, next, !v);
       };
       bool got = wait_bar(k_empty(st), ph ^ 1u, wc);
       ok = !__any_sync(0xffffffffu, !got);
       if (!ok) break;
-      convert(L::kK + st * L::kTile, kx, false);
+      convert(L::kK + st * L::kTile, false);
       fence_proxy_async_smem();
       warp_arrive(k_full(st), lane);
-      const bool more = g + 1 < units_here;
-      if (more) {
-        ok = arrived(g + 1);
-        if (!ok) break;
-        load(kx, unit(g + 1), false);
-      }
       got = wait_bar(v_empty(st), ph ^ 1u, wc);
       ok = !__any_sync(0xffffffffu, !got);
       if (!ok) break;
-      convert(L::kV + st * L::kTile, vx, true);
+      convert(L::kV + st * L::kTile, true);
       fence_proxy_async_smem();
       warp_arrive(v_full(st), lane);
-      if (more) load(vx, unit(g + 1), true);
       // The batch's last entry has been read.
       if ((g & 3) == 3) warp_arrive(u_empty(g / 4 % kBatches), lane);
     }
