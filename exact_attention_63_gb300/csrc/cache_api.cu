@@ -175,9 +175,10 @@ int check_fp8(const attn_cache* a, const void* k_scales, const void* v_scales, C
 // The 8-bit cache's attention: the kernel for many rows or few, rows of a tile, key heads that
 // a CTA works on at a time, and the workspace as above.  `most` is what any number of
 // tokens up to max_new needs, of any number of sequences.
-// More rows go to the converting kernel: one token tile of 64 rows, 64 sequences of up to
-// 8191 at d = 128, takes 287 us there and 396 in two tiles here; 32 rows 278 and 223.
-constexpr int kFp8FewRows = 32;
+// More rows go to the converting kernel.  64 sequences of up to 8191: at d = 128 64 rows take 235 us
+// there and 396 in two tiles here, 32 rows 225 and 224, but over 2000 and 100 keys 83 and 59 us and 84
+// and 72, over one sequence of 32768 32 and 39; at d = 64 32 rows take 154 us and 121.
+constexpr int few_rows(int d) { return d == 128 ? 16 : 32; }
 struct Fp8Tiles {
   bool wide;
   int rows, hg, nt, per_cta, max_ctas;
@@ -193,7 +194,7 @@ Fp8Tiles fp8_tiles_of(int rows, int hg, int max_ctas, int d) {
 }
 Fp8Tiles fp8_tiles(int group, int max_new, int d, int hg) {
   const long long all = static_cast<long long>(group) * max_new;
-  if (all <= kFp8FewRows) return fp8_tiles_of(all <= 8 ? 8 : all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
+  if (all <= few_rows(d)) return fp8_tiles_of(all <= 8 ? 8 : all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
   // As many tiles as 128 rows make, of about as many tokens each.
   const int most = tile_tokens(group, max_new), tiles = (max_new + most - 1) / most, nt = (max_new + tiles - 1) / tiles;
   const int per_cta = tiles > 1 ? 2 : 1;
@@ -209,8 +210,8 @@ size_t fp8_workspace(int group, int max_new, int d, int hg) {
   auto count = [&](const Fp8Tiles& t) { most = t.bytes > most ? t.bytes : most; };
   count(fp8_tiles_of(8, hg, attn::kCacheMaxCtas / 2, d));
   if (all > 8) count(fp8_tiles_of(16, hg, attn::kCacheMaxCtas / 2, d));
-  if (all > 16) count(fp8_tiles_of(32, hg, attn::kCacheMaxCtas / 2, d));
-  if (all > kFp8FewRows) count(fp8_tiles_of(tile_tokens(group, max_new) * group, 1, attn::kCacheMaxCtas, d));
+  if (all > 16 && few_rows(d) > 16) count(fp8_tiles_of(32, hg, attn::kCacheMaxCtas / 2, d));
+  if (all > few_rows(d)) count(fp8_tiles_of(tile_tokens(group, max_new) * group, 1, attn::kCacheMaxCtas, d));
   return most;
 }
 

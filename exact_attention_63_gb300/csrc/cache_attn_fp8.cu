@@ -666,7 +666,7 @@ cudaError_t launch(const CacheAttnFp8Launch& a) {
 
 cudaError_t launch_cache_attn_fp8(const CacheAttnFp8Launch& a) {
   if (a.p.c.d == 64) return a.p.rows > 16 ? launch<64, 4>(a) : a.p.rows > 8 ? launch<64, 2>(a) : launch<64, 1>(a);
-  return a.p.rows > 16 ? launch<128, 4>(a) : a.p.rows > 8 ? launch<128, 2>(a) : launch<128, 1>(a);
+  return a.p.rows > 8 ? launch<128, 2>(a) : launch<128, 1>(a);  // (more rows: the other kernel)
 }
 
 }  // namespace attn

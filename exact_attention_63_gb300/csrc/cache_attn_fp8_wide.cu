@@ -1,7 +1,7 @@
 // Attention of new tokens over a paged cache of E4M3 codes and over each other, many rows
 // (cache_attn_fp8.cu has the formulas, and the kernel for few).
 //
-// With more than 32 rows a sequence and key head the products belong on the tensor core's
+// With more than 16 rows a sequence and key head (d = 64: 32) the products belong on the tensor core's
 // tcgen05 instructions, whose operands have 16 bits: 8 or 16 warps (the converters) read the
 // codes, 16 bytes a lane and whole rows of a head at a time, take them to bf16 with their
 // scales, which is exact, and lay them out in shared memory as TMA would; all that follows is as over a
@@ -107,6 +107,25 @@ __device__ __forceinline__ void to_bf16(const uint4& codes, float f, uint4& lo, 
   hi = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
+// wait_bar for roles with few registers: the flag by its 32-bit address.
+__device__ __forceinline__ bool wait_few(uint32_t bar, uint32_t parity, uint32_t flag, const CacheAttnParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15) == 0) {
+      uint32_t set;
+      asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(set) : "r"(flag) : "memory");
+      if (set) return false;
+      if (globaltimer_ns() - t0 > p.timeout_ns) {
+        asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(flag), "r"(1u) : "memory");
+        atomicOr(p.status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
     cache_attn_fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const CacheAttnFp8WideParams fp) {
@@ -187,6 +206,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
 
+  const uint32_t flag = base + L::kMisc + 4;  // abort_flag
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssuer));
     if (lane == 0 && warp < MT) {
@@ -203,24 +223,24 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
         const int t0 = sg.m * p.ntt + tile * p.nt;
         const bool now = tile == 0 || sg.k.n > t0;
         if (now) {
-          ok = nq == 0 || wait_bar(q_empty(tile), (nq - 1) & 1, wc);
+          ok = nq == 0 || wait_few(q_empty(tile), (nq - 1) & 1, flag, p);
           if (!ok) break;
           mbar_arrive_expect_tx(q_full(tile), static_cast<uint32_t>(p.nt * p.c.group) * 128u * L::kHalves);
           for (int hf = 0; hf < L::kHalves; ++hf)
             tma_load_4d(q_at + hf * 16384, &tm_q, 64 * hf, 0, sg.h, sg.k.q0 + t0, q_full(tile));
-          ok = wait_bar(q_full(tile), nq & 1, wc);
+          ok = wait_few(q_full(tile), nq & 1, flag, p);
           ++nq;
         }
         for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
           const int st = g % L::kStages;
-          ok = wait_bar(k_full(st), (g / L::kStages) & 1, wc);
+          ok = wait_few(k_full(st), (g / L::kStages) & 1, flag, p);
           if (!ok) break;
           if (now) {
             const uint64_t dk = sdesc_kmajor_sw128(base + L::kK + st * L::kTile);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               // The half's last product has read its P, which lies over S.
-              if (e > 0) ok = ok && wait_bar(pv_done(tile, x), (e - 1) & 1, wc);
+              if (e > 0) ok = ok && wait_few(pv_done(tile, x), (e - 1) & 1, flag, p);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -257,12 +277,12 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
         const int tiles = MT == 2 && sg.k.n - sg.m * p.ntt > p.nt ? 2 : 1;
         for (int b = sg.b0; b < sg.b1 && ok; ++b, ++g) {
           const int st = g % L::kStages;
-          ok = wait_bar(v_full(st), (g / L::kStages) & 1, wc);
+          ok = wait_few(v_full(st), (g / L::kStages) & 1, flag, p);
           const uint64_t dv = sdesc_mnmajor_sw128(base + L::kV + st * L::kTile, 16384);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             for (int i = 0; i < tiles; ++i) {
-              ok = ok && wait_bar(p_full(i, x), (i == 0 ? g : e1) & 1, wc);
+              ok = ok && wait_few(p_full(i, x), (i == 0 ? g : e1) & 1, flag, p);
               if (!ok) break;
               tc_fence_after();
               const uint32_t t = tmem + 256 * i;
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
           }
         }
         const int slot = n % kBatches;
-        const bool got = wait_bar(u_empty(slot), ((n / kBatches) & 1) ^ 1u, wc);
+        const bool got = wait_few(u_empty(slot), ((n / kBatches) & 1) ^ 1u, flag, p);
         ok = !__any_sync(0xffffffffu, !got);
         if (!ok) break;
         Unit& to = found[4 * slot + (lane >> 3)];
@@ -329,8 +349,15 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
     // A lane has 16 codes of a row, a step of eight warps 32 rows (d = 64: 64; sixteen warps twice that).
     constexpr int kRuns = D / 16, kStep = 32 * L::kConverters / kRuns, kSteps = 128 / kStep;
     const int tid = threadIdx.x - 32 * L::kConverter0, run = tid % kRuns, row0 = tid / kRuns;
-    const uint8_t *const k_lane = fp.f.k + (row0 & 15) * p.c.k_st[1] + 16 * run,
-                  *const v_lane = fp.f.v + (row0 & 15) * p.c.v_st[1] + 16 * run;
+    // Where the lane's run of the i-th step lies.  (For two tiles of d = 128 the row's distance is worked out
+    // again each time, which is cheaper than the spills that four more registers cost: 64 tokens over 64
+    // sequences 342 us instead of 352; elsewhere nothing spills for them, 64 rows 240 instead of 258.)
+    auto codes_at = [&](int i, const Unit& un, bool v) -> const uint4* {
+      int r = row0;
+      if (D == 128 && MT == 2) asm volatile("" : "+r"(r));
+      return reinterpret_cast<const uint4*>((v ? fp.f.v : fp.f.k) + (v ? un.v_at : un.k_at)[(r >> 4) + i * kStep / 16] +
+                                            (r & 15) * (v ? p.c.v_st[1] : p.c.k_st[1]) + 16 * run);
+    };
     // Where the two runs of 8 bf16 elements go (rows of a step further on lie as far on); lanes
     // that would meet in a bank write them in the other order.
     const int half = run >> 2, first = ((2 * run & 7) + half) ^ (row0 & 7);
@@ -343,9 +370,7 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
     // K's codes, then V's in their places as K's are converted, then the next block's K's.  (V's in
     // registers of their own, asked for earlier, cost spills: 64 rows 308 us instead of 240.)
     uint4 x[kSteps];
-    auto load = [&](int i, const Unit& un, bool v) {
-      x[i] = __ldcs(reinterpret_cast<const uint4*>((v ? v_lane : k_lane) + (v ? un.v_at : un.k_at)[(row0 >> 4) + i * kStep / 16]));
-    };
+    auto load = [&](int i, const Unit& un, bool v) { x[i] = __ldcs(codes_at(i, un, v)); };
     const int units_here = u1 - u0;
     bool ok = !(p.test_flags & 1u);
     // Unit g's entry; the first of a batch waits for it.
@@ -384,15 +409,13 @@ __global__ void __launch_bounds__(WL<D, MT>::kThreads, 3 - MT)
           return;
         }
         // A tail, new tokens, or both: few of all units, so their codes are read here and the code is short.
-        const uint8_t* const from = v ? v_lane : k_lane;
-        const long long* const at = (v ? un.v_at : un.k_at) + (row0 >> 4);
         const long long* const fst = v ? fp.vn_st : fp.kn_st;
 #pragma unroll 1
         for (int i = 0; i < kSteps; ++i) {
           const int row = i * kStep + row0;
           uint4 lo, hi;
           if (row < cached) {
-            to_bf16(*reinterpret_cast<const uint4*>(from + at[i * kStep / 16]), scale[i * kStep / 16], lo, hi);
+            to_bf16(*codes_at(i, un, v), scale[i * kStep / 16], lo, hi);
           } else if (row >= off && row < off + fresh) {
             const uint4* const own = reinterpret_cast<const uint4*>((v ? fp.vn : fp.kn) + (un.q0 + row - off) * fst[0] +
                                                                     un.h * fst[1] + 16 * run);

@@ -593,9 +593,9 @@ int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cud
  *             suffice for every smaller max_seqlen and any total too.
  * Codes and scales are exact in the products; P is rounded to 16 bits, statistics
  * and sums are fp32 (of P up to 2^15 where few rows are, so v beyond about 2^100 may
- * leave their range).  Up to 32 rows (new tokens of a sequence times query heads of a
- * key head, by max_seqlen) no thread waits for another's copies: opts then
- * change nothing.
+ * leave their range).  Up to 16 rows at d = 128 and 32 at d = 64 (new tokens of a sequence
+ * times query heads of a key head, by max_seqlen) no thread waits for another's
+ * copies: opts then change nothing.
  */
 size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen, int d);
 int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
