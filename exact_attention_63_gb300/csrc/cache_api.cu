@@ -194,7 +194,8 @@ Fp8Tiles fp8_tiles_of(int rows, int hg, int max_ctas, int d) {
 }
 Fp8Tiles fp8_tiles(int group, int max_new, int d, int hg) {
   const long long all = static_cast<long long>(group) * max_new;
-  if (all <= few_rows(d)) return fp8_tiles_of(all <= 8 ? 8 : all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
+  if (all <= 8) return fp8_tiles_of(8, hg, attn::kCacheMaxCtas, d);  // two ranges a CTA, if apart
+  if (all <= few_rows(d)) return fp8_tiles_of(all <= 16 ? 16 : 32, hg, attn::kCacheMaxCtas / 2, d);
   // As many tiles as 128 rows make, of about as many tokens each.
   const int most = tile_tokens(group, max_new), tiles = (max_new + most - 1) / most, nt = (max_new + tiles - 1) / tiles;
   const int per_cta = tiles > 1 ? 2 : 1;
@@ -208,7 +209,7 @@ size_t fp8_workspace(int group, int max_new, int d, int hg) {
   const long long all = static_cast<long long>(group) * max_new;
   size_t most = 0;
   auto count = [&](const Fp8Tiles& t) { most = t.bytes > most ? t.bytes : most; };
-  count(fp8_tiles_of(8, hg, attn::kCacheMaxCtas / 2, d));
+  count(fp8_tiles_of(8, hg, attn::kCacheMaxCtas, d));
   if (all > 8) count(fp8_tiles_of(16, hg, attn::kCacheMaxCtas / 2, d));
   if (all > 16 && few_rows(d) > 16) count(fp8_tiles_of(32, hg, attn::kCacheMaxCtas / 2, d));
   if (all > few_rows(d)) count(fp8_tiles_of(tile_tokens(group, max_new) * group, 1, attn::kCacheMaxCtas, d));
@@ -461,7 +462,13 @@ int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void
   a.p.piece = attn::kFp8Block;
   a.p.scale_log2 = scale * 1.4426950408889634f;
   const int ctas = w.wide && w.per_cta == 1 ? 2 * sms : sms;
-  a.grid = ctas < w.max_ctas ? ctas : w.max_ctas;
+  const int most = w.wide ? w.max_ctas : attn::kCacheMaxCtas / 2;
+  a.grid = ctas < most ? ctas : most;
+  // Where each CTA has eight tiles or more, most of the time is in their starts and ends, which two
+  // groups of warps overlap better apart (8 key heads, d = 128: 2000 sequences of up to 50 97 us instead of
+  // 111, of up to 500 261 instead of 268); fewer tiles cost more parts to join (1024 of up to 500 157
+  // instead of 154, 608 112 instead of 106).
+  a.apart = !w.wide && w.rows == 8 && tiles * c.n_seq * (c.hkv / hg) >= 8 * a.grid;
   a.stream = stream;
   if (w.wide) {
     if ((rc = encode_queries(&a.q_map, x, c, a.q_st, w.nt)) != ATTN_OK) return rc;

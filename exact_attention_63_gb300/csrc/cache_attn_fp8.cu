@@ -26,7 +26,8 @@
 //
 // Work units are blocks of 128 / hg keys of hg key heads (8 where the number of heads is a
 // multiple of 8) of one sequence and row tile, 32 KB of codes at d = 128, dealt out evenly
-// as in cache_attn.cu; the parts of a tile are joined by the same second kernel.  With all
+// as in cache_attn.cu, a range for each CTA or (up to 8 rows, where tiles are many) for each of its two
+// groups of eight warps; the parts of a tile are joined by the same second kernel.  With all
 // heads of a token in one block the pages are read as they lie (hg = 1: 220 us where 8 takes
 // 146, before the copies).
 #include "cache_join.cuh"
@@ -47,6 +48,7 @@ struct CacheAttnFp8Params {
   const uint16_t* kn;
   const uint16_t* vn;
   long long q_st[2], kn_st[2], vn_st[2];
+  bool apart;            // a range of units for each group of eight warps instead of each CTA
 };
 
 // The blocks of 128 / hg cached keys; the new tokens go with the last.
@@ -165,17 +167,21 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
   const int units = tab[p.c.n_seq];
   if (cta == 0)
     for (int i = threadIdx.x; i <= p.c.n_seq; i += L::kThreads) p.ws_table[i] = tab[i];
-  const int grid = min(static_cast<int>(gridDim.x), units);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (cta >= grid) return;
-  const int u0 = range_start(units, cta, grid), u1 = range_start(units, cta + 1, grid);
-
+  // The ranges of units: a CTA's, or (apart) one for each of its two groups of warps.
   const int gr = lane >> 2, t4 = lane & 3, group = warp >> 3, part8 = warp & 7;
+  const bool apart = L::kGroups > 1 && fp.apart;
+  const int groups = apart ? 1 : L::kGroups, share = apart ? 0 : group;  // that share a range; which of them
+  const int range = apart ? cta + group * static_cast<int>(gridDim.x) : cta;
+  const int grid = min(static_cast<int>(gridDim.x) * (apart ? 2 : 1), units);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (range >= grid) return;
+  const int u0 = range_start(units, range, grid), u1 = range_start(units, range + 1, grid);
+
   const int hg = p.hg, hh = part8 & (hg - 1), tb = part8 / hg, per_block = 8 / hg, keys = 128 / hg;
   const int grp = p.c.group, H = p.c.hkv * grp;
   constexpr int kSteps = D / 16;  // m16n8k16 products of a score tile, and tiles of Oᵀ
 
-  // ---- the warp's blocks: number x is the tb-th 16 slots of unit u0 + group + kGroups·x.  16 of
+  // ---- the warp's blocks: number x is the tb-th 16 slots of unit u0 + share + groups·x.  16 of
   // them are looked up at a time, a lane each, while earlier ones are worked on: their pages first, and
   // with few registers in use (NT = 1) two blocks later their places and scales, so that
   // neither is waited for (one token over 64 sequences 130 -> 128 us, d = 64 76 -> 74; with
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
   };
   auto find_page = [&](int x) -> Page {
     Page r = {-1, 0, 0};
-    const int u = u0 + group + L::kGroups * (x + lane);
+    const int u = u0 + share + groups * (x + lane);
     if (u >= u1 || lane >= kLookUp) return r;
     const Segment sg = segment_at<RowsPlan>(p, tab, u, u1);
     const int j = sg.b0 * keys + 16 * tb;
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
   int x = 0, st = 0;  // the block at work and its place in the ring
   for (int u = u0; u < u1;) {
     const Segment sg = segment_at<RowsPlan>(p, tab, u, u1);
-    const bool first_of_cta = u == u0;
+    const bool first_of_range = u == u0;
     u += sg.b1 - sg.b0;
     const int h = sg.h * hg + hh, row0 = sg.m * p.rows, n_rows = min(sg.k.n * grp - row0, p.rows);
     // ---- Q: the rows of this thread's fragments (row gr of each tile), as f16
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
 
     for (;; ++x) {
       // (units of the segment come in order: its last is u − 1)
-      const int unit = u0 + group + L::kGroups * x;
+      const int unit = u0 + share + groups * x;
       if (unit >= u) break;
       copy_wait<L::kStages - 1>();
       __syncwarp();
@@ -476,9 +482,9 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
     }
     // ---- the new tokens' own keys, 16 at a time, from the head's last warp on (whose cached keys
     // are often none)
-    const int sharers = per_block * L::kGroups;
+    const int sharers = per_block * groups;
 #pragma unroll 1
-    for (int k0 = 16 * (sharers - 1 - (tb + per_block * group)); sg.b1 == sg.k.db + 1 && k0 < sg.k.n;
+    for (int k0 = 16 * (sharers - 1 - (tb + per_block * share)); sg.b1 == sg.k.db + 1 && k0 < sg.k.n;
          k0 += 16 * sharers) {
       uint32_t mine = 0u;  // which of the 16 keys row `lane` of the tile sees
       {
@@ -558,14 +564,17 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
     // half, until one is left
     // `pair`: by a barrier of the two warps that share the slot, otherwise by one of all warps,
     // since the next level's pairs are others.
+    auto all = [&]() {  // warps that go through the same segments
+      asm volatile("bar.sync %0, %1;" ::"r"(9 + (apart ? group : 0)), "r"(apart ? 256 : 32 * L::kWarps) : "memory");
+    };
     auto meet = [&](int slot, bool gives, bool takes, auto pair) {
       auto both = [&]() {
         if constexpr (decltype(pair)::value) asm volatile("bar.sync %0, 64;" ::"r"(1 + slot) : "memory");
-        else asm volatile("bar.sync 9, %0;" ::"n"(32 * L::kWarps) : "memory");
+        else all();
       };
       float4* const ml = reinterpret_cast<float4*>(smem + L::kMl) + slot * NT * 32 + lane;
       ulonglong2* const half = reinterpret_cast<ulonglong2*>(smem + L::kMerge + slot * L::kMergeWarp) + lane;
-      uint64_t mine[NT], theirs[NT];
+      uint64_t ours[NT], theirs[NT];
       if (gives)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -598,32 +607,33 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
                 b[i] = their_m[i] == top ? 1.f : ex2_mufu(their_m[i] - top);
                 m = top;
               }
-              mine[nt] = pack2(a[0], a[1]);
+              ours[nt] = pack2(a[0], a[1]);
               theirs[nt] = pack2(b[0], b[1]);
-              l_run[nt] = ffma2(pack2(y.z, y.w), theirs[nt], fmul2(l_run[nt], mine[nt]));
+              l_run[nt] = ffma2(pack2(y.z, y.w), theirs[nt], fmul2(l_run[nt], ours[nt]));
             }
 #pragma unroll
           for (int i = 0; i < NT * kSteps / 2; ++i) {
             const ulonglong2 y = half[i * 32];
             const int nt = i / (kSteps / 2);
             uint64_t(&z)[2] = o[nt][x * (kSteps / 2) + i % (kSteps / 2)];
-            z[0] = ffma2(y.x, theirs[nt], fmul2(z[0], mine[nt]));
-            z[1] = ffma2(y.y, theirs[nt], fmul2(z[1], mine[nt]));
+            z[0] = ffma2(y.x, theirs[nt], fmul2(z[0], ours[nt]));
+            z[1] = ffma2(y.y, theirs[nt], fmul2(z[1], ours[nt]));
           }
         }
         both();
       }
     };
-    if (L::kGroups > 1) {
+    if (groups > 1) {
       meet(part8, group == 1, group == 0, std::true_type{});  // (warps part8 and part8 + 8)
-      if (per_block > 1) asm volatile("bar.sync 9, %0;" ::"n"(32 * L::kWarps) : "memory");
+      if (per_block > 1) all();
     }
     for (int w = per_block / 2; w > 0; w >>= 1)
-      meet(hh + hg * (tb & (w - 1)), group == 0 && tb >= w && tb < 2 * w, group == 0 && tb < w, std::false_type{});
-    if (group != 0 || tb != 0) continue;
+      meet((apart ? 4 * group : 0) + hh + hg * (tb & (w - 1)), share == 0 && tb >= w && tb < 2 * w, share == 0 && tb < w,
+           std::false_type{});
+    if (share != 0 || tb != 0) continue;
     // ---- the head's rows, by its one warp
     const bool whole = sg.b0 == 0 && sg.b1 == sg.k.db + 1;
-    const int slot = 2 * cta + (first_of_cta ? 0 : 1);
+    const int slot = 2 * range + (first_of_range ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
 template <int D, int NT>
 cudaError_t launch(const CacheAttnFp8Launch& a) {
   using L = FL<D, NT>;
-  CacheAttnFp8Params p = {a.p, a.f, a.q, a.kn, a.vn, {a.q_st[0], a.q_st[1]}, {a.kn_st[0], a.kn_st[1]}, {a.vn_st[0], a.vn_st[1]}};
+  CacheAttnFp8Params p = {a.p, a.f, a.q, a.kn, a.vn, {a.q_st[0], a.q_st[1]}, {a.kn_st[0], a.kn_st[1]}, {a.vn_st[0], a.vn_st[1]}, a.apart};
   const unsigned int smem = L::kBytes + 4u * (p.a.c.n_seq + 1);
   static volatile bool configured[64] = {};
   if (a.device < 0 || a.device >= 64) return cudaErrorInvalidDevice;
@@ -680,7 +690,7 @@ cudaError_t launch(const CacheAttnFp8Launch& a) {
   cache_attn_fp8_kernel<D, NT><<<a.grid, L::kThreads, smem, a.stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<D, RowsPlan>(p.a, a.grid, a.stream);
+  return launch_join<D, RowsPlan>(p.a, a.apart ? 2 * a.grid : a.grid, a.stream);
 }
 
 }  // namespace

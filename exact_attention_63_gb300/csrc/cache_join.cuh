@@ -19,8 +19,20 @@ namespace {
 // one with all of its parts (tiles of 8 or 16 rows, of which half and more may be empty).
 enum { kJoinFew, kJoinRows, kJoinWide, kJoinEight };
 
+// The last s with tab[s] <= u of s in [0, n), tab[0] <= u: the warp tries 32 places at a time.
+__device__ __forceinline__ int find_seq_warp(const int* tab, int n, int u, int lane) {
+  int lo = 0, hi = n;  // the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + step * lane;
+    const uint32_t below = __ballot_sync(0xffffffffu, at < hi && tab[at] <= u);
+    lo += step * (31 - __clz(below));
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 template <int D, int WAY, class Plan>
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max) {
+__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p, int grid, int mt_max, int ends) {
   constexpr int kPer = D / 32, SPLIT = WAY == kJoinEight ? 1 : 8;
   __shared__ float s_acc[WAY == kJoinFew ? SPLIT : 1][D];
   __shared__ float2 s_ml[SPLIT];
@@ -30,19 +42,39 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   unsigned int x = blockIdx.x;
   const int row0 = static_cast<int>(x % chunks) * kRows;
   x /= chunks;
-  const int m = static_cast<int>(x % mt_max);
-  x /= mt_max;
-  const int h = static_cast<int>(x % p.c.hkv), s = static_cast<int>(x / p.c.hkv);
-  const KeyPlan k = Plan::of(p, s);
-  const int grp = p.c.group, first_row = m * p.rows, n_rows = min(k.n * grp - first_row, p.rows);
-  // The attention kernel's results, complete and visible.  Every block waits, so
-  // that this kernel never ends before that one.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row0 >= n_rows) return;
-  const int units = p.ws_table[p.c.n_seq], nb = k.db + 1;
-  grid = min(grid, units);
-  const int ua = p.ws_table[s] + (h / p.hg * row_tiles(p, k.n) + m) * nb;
+  int m, h, s, ua, units;
+  KeyPlan k;
   auto cta_of = [&](int u) { return static_cast<int>(((u + 1ll) * grid - 1) / units); };
+  if (Plan::kEight && ends) {
+    // The block's tile is the one that the end of a CTA's range divides.
+    const int c = static_cast<int>(x / p.hg) + 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    units = p.ws_table[p.c.n_seq];
+    grid = min(grid, units);
+    if (c >= grid) return;
+    const int u = range_start(units, c, grid);
+    s = find_seq_warp(p.ws_table, p.c.n_seq, u, lane);
+    k = Plan::of(p, s);
+    const int rem = u - p.ws_table[s], hm = rem / (k.db + 1), mt = row_tiles(p, k.n);
+    ua = u - (rem - hm * (k.db + 1));
+    if (ua == u || cta_of(ua) != c - 1) return;  // no tile, or an earlier end's
+    m = hm % mt;
+    h = hm / mt * p.hg + static_cast<int>(x % p.hg);
+  } else {
+    m = static_cast<int>(x % mt_max);
+    x /= mt_max;
+    h = static_cast<int>(x % p.c.hkv);
+    s = static_cast<int>(x / p.c.hkv);
+    k = Plan::of(p, s);
+    // The attention kernel's results, complete and visible.  Every block waits, so
+    // that this kernel never ends before that one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    units = p.ws_table[p.c.n_seq];
+    grid = min(grid, units);
+    ua = p.ws_table[s] + (h / p.hg * row_tiles(p, k.n) + m) * (k.db + 1);
+  }
+  const int grp = p.c.group, first_row = m * p.rows, n_rows = min(k.n * grp - first_row, p.rows), nb = k.db + 1;
+  if (row0 >= n_rows) return;
   const int c0 = cta_of(ua), c1 = cta_of(ua + nb - 1);
   if (c0 == c1) return;  // one CTA did it all and has written the rows
   // Every CTA's part but the first's is the first of its range.
@@ -214,7 +246,11 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   // each fit on the SMs at a time (8 tiles of 240 rows in 19 parts: 26 us a row a block).
   const bool few = row_a_block && (!Plan::kEight || tiles * p.rows <= 4ll * grid);
   const bool eight = Plan::kEight && !few && !wide && (row_a_block || p.rows <= 16);
-  const long long blocks = tiles * (few ? p.rows : eight ? (p.rows + 7) / 8 : (p.rows + 31) / 32);
+  // By the ends of the CTAs' ranges where these are far fewer than the tiles, most of which are then
+  // no CTA's part (a whole call with 8 key heads in 152 ranges, so and otherwise: 200 sequences 56 and
+  // 55 us, 512 57 and 63, 1216 60 and 88).
+  const bool ends = Plan::kEight && grid > 1 && tiles > 2ll * (grid - 1) * p.hg;
+  const long long blocks = (ends ? (grid - 1) * p.hg : tiles) * (few ? p.rows : eight ? (p.rows + 7) / 8 : (p.rows + 31) / 32);
   // The join starts while the attention kernel runs and waits for its end on the
   // device, which hides its launch.
   cudaLaunchAttribute attr;
@@ -226,10 +262,10 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide, Plan>, p, grid, mt_max);
-  if (eight) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinEight, Plan>, p, grid, mt_max);
-  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew, Plan>, p, grid, mt_max)
-             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows, Plan>, p, grid, mt_max);
+  if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide, Plan>, p, grid, mt_max, ends);
+  if (eight) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinEight, Plan>, p, grid, mt_max, ends);
+  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew, Plan>, p, grid, mt_max, ends)
+             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows, Plan>, p, grid, mt_max, ends);
 }
 
 }  // namespace

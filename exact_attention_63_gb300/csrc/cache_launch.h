@@ -121,6 +121,7 @@ struct CacheAttnFp8Launch {
   const uint16_t* vn;
   long long q_st[2], kn_st[2], vn_st[2];  // element strides: token, head
   int tiles;             // many rows: row tiles of a CTA, 2 where a sequence may have more than 128 rows
+  bool apart;            // up to 8 rows: the two groups of warps of a CTA work on ranges of their own
   int grid, device;
   cudaStream_t stream;
 };

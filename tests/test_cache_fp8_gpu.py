@@ -258,6 +258,17 @@ def test_attention_of_2048_sequences(new):
     check(c, o, lse)
 
 
+@pytest.mark.parametrize("n_seq,hkv,group,new,d", [(700, 8, 4, 1, 128), (2048, 8, 2, 2, 128), (1900, 8, 1, 3, 64), (1300, 2, 4, 2, 64), (1250, 3, 8, 1, 128),
+                                                   (640, 16, 2, 1, 128), (420, 8, 4, 6, 128), (330, 8, 4, 8, 64), (400, 4, 8, 20, 64)])
+def test_attention_of_many_tiles(n_seq, hkv, group, new, d):
+    """More tiles than CTAs, by far: ranges of each group of warps, and a join that goes by the ranges' ends."""
+    lens = [(37 * i * i + 11) % 70 if i % 9 else 0 for i in range(n_seq)]
+    news = [new if i % 3 else (i // 3) % (new + 1) for i in range(n_seq)]
+    c = Fp8Case(lens, news, hkv * group, hkv, d, 32, seed=n_seq).cuda()
+    o, lse = attend(c)
+    check(c, o, lse)
+
+
 def test_random_calls():
     """Seeded calls over the range of the contract: heads, groups, pages, lengths from 0, trees, padded bounds."""
     r = np.random.default_rng(20)
