@@ -13,9 +13,10 @@
 // becomes an f16 number (exactly) in one instruction for two.
 //   A warp has a key head and every (16 / hg)-th block of 16 slots of its CTA's range, a block
 // being one block of scales: 2^a is one factor of its scores, 2^b one of its product, which
-// is added to O in fp32.  Each lane copies the bytes that it will read itself, so nothing is
-// handed from thread to thread: no barrier, no wait of one warp for another before the end of a
-// tile, where the warps of a head meet.  (With a loading warp and TMA the copies' issue set the pace, two
+// is added to O in fp32.  Each warp copies the bytes that it will read itself, lanes for one
+// another (in order by their wait and a __syncwarp before the reads, one after them), so nothing is
+// handed from warp to warp: no wait of one for another before the end of a tile, where the warps
+// of a head meet.  (With a loading warp and TMA the copies' issue set the pace, two
 // to four cycles a row of 128 or 64 bytes: 146 us for one token over 64 sequences of up to
 // 8191 at d = 128, 113 at d = 64.)
 //   Q's rows are scaled by a power of two to a maximum of 2^14 … 2^15 before they become f16:
@@ -475,8 +476,8 @@ __global__ void __launch_bounds__(FL<D, NT>::kThreads, 1) cache_attn_fp8_kernel(
         publish(now);
         if (!kTwice) next = find_block(find_page(ahead + kLookUp));
       }
+      __syncwarp();  // (every lane has read the block: it holds bytes that others copied)
       copy(ahead, st);
-      __syncwarp();
       keep_scales(now, ahead, st);
       st = st + 1 == L::kStages ? 0 : st + 1;
     }
