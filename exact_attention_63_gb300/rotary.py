@@ -159,20 +159,26 @@ def rotary_bwd(dq, dk, positions, inv_freq, interleaved: bool = False, magnitude
 
 
 class _Rotary(torch.autograd.Function):
+    """The turn, or the turn back (``inverse``): each is the other's gradient."""
+
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, interleaved, magnitude):
+    def forward(ctx, q, k, positions, inv_freq, interleaved, magnitude, inverse):
         ctx.save_for_backward(positions, inv_freq)
-        ctx.cfg = (interleaved, magnitude)
-        return _turn(q, k, positions, inv_freq, interleaved, magnitude, None, None, False, None)
+        ctx.cfg = (interleaved, magnitude, inverse)
+        return _turn(q, k, positions, inv_freq, interleaved, magnitude, None, None, inverse, None)
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, inv_freq = ctx.saved_tensors
-        grads = _turn(dq.contiguous(), None if dk is None else dk.contiguous(), positions, inv_freq, *ctx.cfg, None, None,
-                      True, None)
-        return (*grads, None, None, None, None)
+        interleaved, magnitude, inverse = ctx.cfg
+        dq, dk = dq.contiguous(), None if dk is None else dk.contiguous()
+        if torch.is_grad_enabled():  # (create_graph: the gradients have gradients)
+            grads = _Rotary.apply(dq, dk, positions, inv_freq, interleaved, magnitude, not inverse)
+        else:
+            grads = _turn(dq, dk, positions, inv_freq, interleaved, magnitude, None, None, not inverse, None)
+        return (*grads, None, None, None, None, None)
 
 
 def rotary(q, k, positions, inv_freq, interleaved: bool = False, magnitude: float = 1.0):
-    """rotary_fwd with gradients to q and k; what attn.attention then takes."""
-    return _Rotary.apply(q, k, positions, inv_freq, interleaved, magnitude)
+    """rotary_fwd with gradients to q and k, of any order; what attn.attention then takes."""
+    return _Rotary.apply(q, k, positions, inv_freq, interleaved, magnitude, False)
