@@ -49,7 +49,7 @@ struct Regs {
 
 // The blocks of the bf16 cache's kernel.
 struct ConvertPlan {
-  static constexpr bool kEight = true;
+  static constexpr bool kEight = true, kRuns = false;
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
 };
 

@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kRows = WAY == kJoinFew ? 1 : WAY == kJoinEight ? 8 : 32;  // of a block
   const unsigned int chunks = (p.rows + kRows - 1) / kRows;
+  const int hg = heads_of<Plan>(p);
   unsigned int x = blockIdx.x;
   const int row0 = static_cast<int>(x % chunks) * kRows;
   x /= chunks;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   auto cta_of = [&](int u) { return static_cast<int>(((u + 1ll) * grid - 1) / units); };
   if (Plan::kEight && ends) {
     // The block's tile is the one that the end of a CTA's range divides.
-    const int c = static_cast<int>(x / p.hg) + 1;
+    const int c = static_cast<int>(x / hg) + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     units = p.ws_table[p.c.n_seq];
     grid = min(grid, units);
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
     ua = u - (rem - hm * (k.db + 1));
     if (ua == u || cta_of(ua) != c - 1) return;  // no tile, or an earlier end's
     m = hm % mt;
-    h = hm / mt * p.hg + static_cast<int>(x % p.hg);
+    h = hm / mt * hg + static_cast<int>(x % hg);
   } else {
     m = static_cast<int>(x % mt_max);
     x /= mt_max;
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     units = p.ws_table[p.c.n_seq];
     grid = min(grid, units);
-    ua = p.ws_table[s] + (h / p.hg * row_tiles(p, k.n) + m) * (k.db + 1);
+    ua = p.ws_table[s] + (h / hg * row_tiles(p, k.n) + m) * (k.db + 1);
   }
   const int grp = p.c.group, first_row = m * p.rows, n_rows = min(k.n * grp - first_row, p.rows), nb = k.db + 1;
   if (row0 >= n_rows) return;
@@ -79,8 +80,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   if (c0 == c1) return;  // one CTA did it all and has written the rows
   // Every CTA's part but the first's is the first of its range.
   const int slot0 = 2 * c0 + (range_start(units, c0, grid) >= ua ? 0 : 1);
-  const int in_run = h % p.hg;
-  auto slot_of = [&](int c) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * p.hg + in_run; };
+  const int in_run = h % hg;
+  auto slot_of = [&](int c) { return static_cast<long long>(c == c0 ? slot0 : 2 * c) * hg + in_run; };
   auto part_of = [&](int c, int r) { return slot_of(c) * p.rows + r; };
 
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;

@@ -29,6 +29,7 @@ __device__ __forceinline__ KeyPlan key_plan(const CacheAttnParams& p, int s) {
 }
 struct BlockPlan {
   static constexpr bool kEight = false;  // (ways of the join that its tiles use)
+  static constexpr bool kRuns = false;   // units of more than one key head: p.hg of them
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
 };
 // Row tiles that the (token, head of the group) rows of n new tokens make.
@@ -36,10 +37,16 @@ __host__ __device__ __forceinline__ int row_tiles(const CacheAttnParams& p, int 
   return (n * p.c.group + p.rows - 1) / p.rows;
 }
 
+// Key heads of a unit.
+template <class Plan>
+__device__ __forceinline__ int heads_of(const CacheAttnParams& p) {
+  return Plan::kRuns ? p.hg : 1;
+}
+
 template <class Plan>
 __device__ __forceinline__ int units_of(const CacheAttnParams& p, int s) {
   const KeyPlan k = Plan::of(p, s);
-  return k.n == 0 ? 0 : p.c.hkv / p.hg * row_tiles(p, k.n) * (k.db + 1);
+  return k.n == 0 ? 0 : p.c.hkv / heads_of<Plan>(p) * row_tiles(p, k.n) * (k.db + 1);
 }
 
 __device__ __forceinline__ int range_start(int units, int cta, int grid) {
