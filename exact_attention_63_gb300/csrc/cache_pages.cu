@@ -18,29 +18,30 @@ constexpr int kPagesThreads = 512, kPagesCtas = 8;
 constexpr int kFewTokens = 4096;  // slots of so many tokens are written by the same CTAs
 
 // get(s, i), then put(s, i, what it got), for all i in [0, count) with tab[s] <= i < tab[s + 1]:
-// a warp has a run of the numbers, 32 lanes side by side and four steps at once.
+// a warp has a run of the numbers, 32 lanes side by side and four steps at once.  (Unsigned: up to
+// 2^31 - 1 of them are rounded up to the warps' runs.)
 template <class G, class P>
 __device__ __forceinline__ void deal_out(const int* tab, int n, int count, G get, P put) {
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kPagesThreads / 32);
-  const int warp = blockIdx.x * (kPagesThreads / 32) + (threadIdx.x >> 5);
-  const int per = ((count + warps - 1) / warps + 31) & ~31;
-  const int end = min(count, (warp + 1) * per);
-  int at = warp * per;
+  const unsigned int lane = threadIdx.x & 31, warps = gridDim.x * (kPagesThreads / 32);
+  const unsigned int warp = blockIdx.x * (kPagesThreads / 32) + (threadIdx.x >> 5);
+  const unsigned int per = ((count + warps - 1) / warps + 31) & ~31u;
+  const unsigned int end = min(static_cast<unsigned int>(count), (warp + 1) * per);
+  unsigned int at = warp * per;
   if (at >= end) return;
   int s = 0;
   for (; at < end; at += 128) {
     int who[4], got[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int i = at + 32 * k + lane;
-      if (i < end && tab[s + 1] <= i) s = find_seq(tab, n, i, s);
+      const unsigned int i = at + 32 * k + lane;
+      if (i < end && tab[s + 1] <= static_cast<int>(i)) s = find_seq(tab, n, static_cast<int>(i), s);
       who[k] = s;
-      if (i < end) got[k] = get(s, i);
+      if (i < end) got[k] = get(s, static_cast<int>(i));
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int i = at + 32 * k + lane;
-      if (i < end) put(who[k], i, got[k]);
+      const unsigned int i = at + 32 * k + lane;
+      if (i < end) put(who[k], static_cast<int>(i), got[k]);
     }
   }
 }
