@@ -329,7 +329,7 @@ def attn_bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
 class _Attention(torch.autograd.Function):
     """attn_fwd as an autograd function: the forward keeps O and LSE, the
     backward hands them with dO to attn_bwd (the LSE output itself is not
-    differentiated)."""
+    differentiated, nor are the gradients)."""
 
     @staticmethod
     def forward(ctx, q, k, v, causal, scale, causal_align, deterministic):
@@ -340,6 +340,7 @@ class _Attention(torch.autograd.Function):
         return o, lse
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, do, _dlse):
         q, k, v, o, lse = ctx.saved_tensors
         causal, scale, causal_align, deterministic = ctx.cfg
@@ -351,7 +352,8 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, causal: bool = False, scale: float | None = None, causal_align: str = "top-left",
               deterministic: bool = False):
     """Exact attention with gradients: returns (o, lse) like attn_fwd, and
-    o's gradient flows back to q, k and v through attn_bwd.  (batch, seq,
+    o's gradient flows back to q, k and v through attn_bwd (first derivatives
+    only: differentiating them raises an error).  (batch, seq,
     heads, head_dim) bf16 CUDA tensors, strided views allowed as for
     attn_fwd; k and v may have fewer heads than q.  ``deterministic`` selects attn_bwd's bit-reproducible
     schedule."""
