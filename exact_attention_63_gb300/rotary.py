@@ -129,11 +129,11 @@ def _turn(q, k, positions, inv_freq, interleaved, magnitude, q_out, k_out, inver
         elif positions.shape != (rows,):
             raise ValueError(f"positions must be [{rows}]" + (f" or [{batch}, {rows}]" if q.dim() == 4 else "") +
                              f", not {tuple(positions.shape)}")
-    if batch * rows == 0 or any(s[2][2] == 0 for s in sides):
+    turned = [ctypes.byref(r) for r, _, shape in sides if shape[2]]
+    if batch * rows == 0 or not turned:
         return tuple(outs)
-    rc = attn.lib().attn_rotary(ctypes.byref(sides[0][0]), ctypes.byref(sides[1][0]) if k is not None else None, batch, rows,
-                                d, pp, ps, fp, 2 * pairs, int(bool(interleaved)), float(magnitude), int(inverse),
-                                cache._stream(dev))
+    rc = attn.lib().attn_rotary(turned[0], turned[1] if len(turned) > 1 else None, batch, rows, d, pp, ps, fp, 2 * pairs,
+                                int(bool(interleaved)), float(magnitude), int(inverse), cache._stream(dev))
     if rc:
         attn._check(rc)
     return tuple(outs)

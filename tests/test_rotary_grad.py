@@ -97,3 +97,23 @@ def pair_sum(x, part, interleaved):
     u, w = (slice(0, part, 2), slice(1, part, 2)) if interleaved else (slice(0, part // 2), slice(part // 2, part))
     y[..., u] = y[..., w] = x[..., u] + x[..., w]
     return y
+
+
+@pytest.mark.gpu
+def test_a_side_without_heads_leaves_the_other_as_it_is():
+    """k (or q) of no heads has nothing to turn; q (or k) is turned all the same, forward and back."""
+    need_gpu()
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn((2, 9, 3, 64), generator=g).bfloat16().cuda()
+    none = x[:, :, :0]
+    freq = rotary.rotary_frequencies(64).cuda()
+    for op in (rotary.rotary_fwd, rotary.rotary_bwd):
+        want, _ = op(x, None, None, freq)
+        for out in (None, torch.full_like(x, 7.0)):
+            (a, b), (c, d) = op(x, none, None, freq, q_out=out), op(none, x, None, freq, k_out=out)
+            assert torch.equal(a, want) and torch.equal(d, want) and b.shape == c.shape == none.shape
+            assert out is None or (a is out and d is out)
+    x.requires_grad_()
+    y, _ = rotary.rotary(x, none, None, freq)
+    y.sum().backward()
+    assert torch.equal(x.grad, rotary.rotary_bwd(torch.ones_like(x), None, None, freq)[0])
