@@ -55,6 +55,7 @@ struct CacheAttnFp8Params {
 // The blocks of 128 / hg cached keys; the new tokens go with the last.
 struct RowsPlan {
   static constexpr bool kEight = true, kRuns = true;
+  static constexpr int most_rows(int d) { return d == 128 ? 16 : 32; }
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) {
     KeyPlan k;
     const SeqRows r = seq_rows(p.c, s);

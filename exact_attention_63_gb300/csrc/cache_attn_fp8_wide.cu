@@ -50,6 +50,7 @@ struct Regs {
 // The blocks of the bf16 cache's kernel.
 struct ConvertPlan {
   static constexpr bool kEight = true, kRuns = false;
+  static constexpr int most_rows(int) { return 256; }
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
 };
 

@@ -18,6 +18,7 @@ namespace {
 // a lane a row, a warp a quarter of its values.  kJoinEight: a block takes 8 rows, a warp
 // one with all of its parts (tiles of 8 or 16 rows, of which half and more may be empty).
 enum { kJoinFew, kJoinRows, kJoinWide, kJoinEight };
+constexpr int kEightRows = 16;
 
 // The last s with tab[s] <= u of s in [0, n), tab[0] <= u: the warp tries 32 places at a time.
 __device__ __forceinline__ int find_seq_warp(const int* tab, int n, int u, int lane) {
@@ -246,7 +247,7 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   // Where a warp may take a row with all its parts (the 8-bit cache): unless the blocks of a row
   // each fit on the SMs at a time (8 tiles of 240 rows in 19 parts: 26 us a row a block).
   const bool few = row_a_block && (!Plan::kEight || tiles * p.rows <= 4ll * grid);
-  const bool eight = Plan::kEight && !few && !wide && (row_a_block || p.rows <= 16);
+  const bool eight = Plan::kEight && !few && !wide && (row_a_block || p.rows <= kEightRows);
   // By the ends of the CTAs' ranges where these are far fewer than the tiles, most of which are then
   // no CTA's part (a whole call with 8 key heads in 152 ranges, so and otherwise: 200 sequences 56 and
   // 55 us, 512 57 and 63, 1216 60 and 88).
@@ -263,10 +264,14 @@ cudaError_t launch_join(const CacheAttnParams& p, int grid, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide, Plan>, p, grid, mt_max, ends);
-  if (eight) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinEight, Plan>, p, grid, mt_max, ends);
-  return few ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew, Plan>, p, grid, mt_max, ends)
-             : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows, Plan>, p, grid, mt_max, ends);
+  if (few) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinFew, Plan>, p, grid, mt_max, ends);
+  if constexpr (Plan::kEight)
+    if (eight) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinEight, Plan>, p, grid, mt_max, ends);
+  if constexpr (Plan::most_rows(D) > kWideRows)
+    if (wide) return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinWide, Plan>, p, grid, mt_max, ends);
+  if constexpr (!Plan::kEight || Plan::most_rows(D) > kEightRows)
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, kJoinRows, Plan>, p, grid, mt_max, ends);
+  return cudaErrorInvalidConfiguration;  // (not reached: tiles have no more than most_rows rows)
 }
 
 }  // namespace

@@ -30,6 +30,7 @@ __device__ __forceinline__ KeyPlan key_plan(const CacheAttnParams& p, int s) {
 struct BlockPlan {
   static constexpr bool kEight = false;  // (ways of the join that its tiles use)
   static constexpr bool kRuns = false;   // units of more than one key head: p.hg of them
+  static constexpr int most_rows(int) { return 256; }  // of a CTA's tiles, by d
   static __device__ __forceinline__ KeyPlan of(const CacheAttnParams& p, int s) { return key_plan(p, s); }
 };
 // Row tiles that the (token, head of the group) rows of n new tokens make.
