@@ -708,7 +708,9 @@ def cache_pages(seq_lens, block_table, n_blocks, free_pages, n_free, page_size: 
     (missing, slots, positions): missing int32 [n_seq], the pages a sequence did not get (it then
     keeps what it had); with ``cu_new`` (int32 [n_seq + 1]), the newest cu_new[s + 1] - cu_new[s]
     tokens of each sequence get rows of slots, int64 [total], page * page_size + place (-1 where
-    pages lack), and positions, int32 [total], counted in the sequence.
+    pages lack), and positions, int32 [total], counted in the sequence.  Rows of no sequence (behind
+    cu_new's last entry, in a padded batch) are not written: in tensors that the call allocates they
+    hold anything.
     """
     if stream is None:
         bind = _bind or _first("block_table", block_table)

@@ -23,7 +23,9 @@
 // values down to 2^−28 of the largest keep all eight bits, the rest are off by less than
 // 2^−39 of it, less than the fp32 sum of the products.  P, in units where the running
 // maximum is 2^7 (at most 2^15 until it is moved), is rounded to f16: 2^−11 relative, and
-// what lies below f16's range is less than 2^−32 of the largest.
+// what lies below f16's range is less than 2^−32 of the largest.  The fp32 sums hold n keys with
+// |v| up to 2^113 / n.  The factor of a row's scores is its power of two times the block's 2^a: it leaves
+// fp32 at scale·max|q|·2^a = 2^141, and its first part is subnormal below scale·max|q| = 2^−111.
 //
 // Work units are blocks of 128 / hg keys of hg key heads (8 where the number of heads is a
 // multiple of 8) of one sequence and row tile, 32 KB of codes at d = 128, dealt out evenly

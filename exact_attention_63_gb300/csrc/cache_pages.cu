@@ -7,7 +7,7 @@
 // prefix sums for itself from the same counts; the pages that change hands are dealt out to
 // all of their warps, whoever they belong to.  Latency bounds it: two prefix sums over up to 2048
 // sequences, and the chain length → sum → stack → table.  (24,500 pages: 9 us, 24 by one CTA of 1024
-// threads.)
+// threads.)  Calls that place few tokens are one CTA's (below).
 #include "attn_gb300.h"
 #include "cache_device.cuh"
 
@@ -137,7 +137,11 @@ cudaError_t launch_cache_pages(const CachePagesParams& p, cudaStream_t stream) {
   const bool slots = p.cu != nullptr && p.total > 0, here = slots && p.total <= kFewTokens;
   cudaError_t e;
   if (here) {
-    // Few new tokens, so few pages: one CTA (4.8 us where a cluster takes 5.9).
+    // A decoding step, in which few pages change hands as a rule: one CTA (256 sequences, one token
+    // more each: 4.3 us where a cluster takes 6.0).  A step may give back any number of pages, which
+    // the host does not know.  256 requests of 4096 tokens in pages of 16, of which so many end at once, with the
+    // call that makes room for them again, by one CTA and by a cluster: 4 of them 9.7 and 11.2 us, 16 (4096
+    // pages) 11.2 and 11.6, half (32,768 pages) 25.7 and 14.3; 16 of 64 requests of 8191 (8192 pages) 12.2 and 11.2.
     cache_pages_kernel<<<1, kPagesThreads, 0, stream>>>(p, p.total);
     e = cudaGetLastError();
   } else {

@@ -8,6 +8,9 @@ the neighbours (2i, 2i + 1) (``interleaved``) or (i, i + rotary_dim / 2).
 tensor of radians a position will do.  ``rotary`` has gradients, ``rotary_fwd`` and ``rotary_bwd`` are
 its two directions; results may be written over the inputs.  Angles of far positions lose
 nothing: they are taken modulo a turn in 64 bits.
+
+Calls go through ``csrc/cache_bind.cpp`` like those of ``cache.py``, so the compiled binding has to be
+there (``attn.py`` alone does not need it).
 """
 
 from __future__ import annotations
@@ -40,7 +43,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "n
     divided by factor and the fastest stays; "by_parts" divides the pairs that turn at most
     turns[1] times over the original length, leaves those that turn at least turns[0] times, and
     goes from one to the other linearly in i (usually with the magnitude of
-    ``rotary_magnitude(factor)``).
+    ``rotary_magnitude(factor)``): the interpolation of Peng, Quesnelle, Fan and Shippole, "YaRN:
+    efficient context window extension of large language models", 2023.
     """
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and at least 2")

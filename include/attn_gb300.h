@@ -592,10 +592,14 @@ int attn_cache_compact(const attn_cache* cache, const int* kept, int budget, cud
  *   workspace : at least attn_fwd_cache_fp8_workspace_size(...) bytes, which
  *             suffice for every smaller max_seqlen and any total too.
  * Codes and scales are exact in the products; P is rounded to 16 bits, statistics
- * and sums are fp32 (of P up to 2^15 where few rows are, so v beyond about 2^100 may
- * leave their range).  Up to 16 rows at d = 128 and 32 at d = 64 (new tokens of a sequence
- * times query heads of a key head, by max_seqlen) no thread waits for another's
- * copies: opts then change nothing.
+ * and sums are fp32.  Few rows are up to 16 at d = 128 and 32 at d = 64 (new tokens of
+ * a sequence times query heads of a key head, by max_seqlen).  No warp waits for
+ * another's copies there: opts then change nothing.
+ *   What fp32 holds: P is at most 2^15 with few rows and 2^8 with more, so the sums
+ * stay in range where |v| times the keys of a sequence is below 2^113 and 2^120 (2^83
+ * and 2^90 at 2^30 keys).  With few rows, scores (and NaN where they are not) need
+ * scale * max|q| * 2^(b - 127) below 2^141 for a row's q and every scale byte b, and
+ * keep fp32's precision where scale * max|q| is at least 2^-111.
  */
 size_t attn_fwd_cache_fp8_workspace_size(int H, int num_kv_heads, int max_seqlen, int d);
 int attn_fwd_cache_fp8(const attn_cache* cache, const void* k_scales, const void* v_scales, const attn_new_tokens* x,
